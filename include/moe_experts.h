@@ -181,6 +181,19 @@ moe_status moe_experts_forward(const moe_problem* p, const void* hidden, const i
                                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The forward of e4m3 or fp4 experts on hidden rows that are quantised already, as
+ * moe_rms_norm's 8-bit output or moe_quantize_rows_fp8 leave them: hidden_q [T, H] e4m3 codes
+ * and hidden_scale [T, H/128] float32 (16-byte aligned) stand for hidden, and the forward's own
+ * quantisation is left out.  Everything else, `out` (bf16) and the workspace among it, is as
+ * in moe_experts_forward, and so is the result, bit for bit, for the same codes and
+ * scales.  MOE_ERR_UNSUPPORTED for float32 and bf16 weights.
+ */
+moe_status moe_experts_forward_quantized(const moe_problem* p, const uint8_t* hidden_q, const float* hidden_scale,
+                                         const int32_t* topk_idx, const float* topk_w, const void* w_gate_up,
+                                         const void* w_down, const void* w_gate_up_scale, const void* w_down_scale,
+                                         void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The forward without a workspace argument and without any allocation, for callers that
  * cannot allocate device memory (code under HIP graph capture, tight serving loops,
  * harnesses that forbid allocation).  Same arguments, results and errors as
@@ -322,6 +335,152 @@ enum {
  * clears the hook.  n must be 0 or 2 * MOE_STAGE_COUNT (else MOE_ERR_BAD_SHAPE).
  */
 moe_status moe_set_stage_events(void* const* events, int n);
+
+/* ---------------------------------------------------------------------------------------
+ * Dense operators around the routed experts: the norm in front of the layer, the router's
+ * projection, and the experts every token takes (gated projection, then a linear whose
+ * residual is the routed experts' output).  Forward and backward.
+ *
+ * They keep the conventions above with one addition: activations have a row pitch.  A
+ * pitch is in elements, 0 stands for packed rows, and otherwise it is at least the row's
+ * length and at most 2^22.  Weights are packed.  Types are MOE_F32 or MOE_BF16; sums,
+ * statistics and activations are computed in float32 and every output is rounded once to
+ * its type (bf16: nearest even).  Results do not depend on timing: sums over workgroups
+ * are added in a fixed order, without atomics.  Calls launch kernels only (no host wait, no
+ * allocation, no memset), so they can be captured into a HIP graph; the current device
+ * must be the one that `stream` and the buffers belong to.  Outputs do not overlap inputs,
+ * except where stated.  T == 0: forward calls enqueue nothing, backward calls write zeros
+ * to the parameters' gradients.
+ * ------------------------------------------------------------------------------------- */
+
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 /* z * Phi(z) */, MOE_ACT_RELU = 3 } moe_act;
+
+typedef struct {
+  int64_t T;          /* rows, 0 .. 2^31 - 1                                               */
+  int32_t H;          /* row length, a multiple of 8, 8 .. 65536                           */
+  int32_t dtype;      /* moe_dtype of every tensor that is not float32 by its name         */
+  float eps;          /* >= 0 and finite                                                   */
+  int64_t ldx;        /* pitch of x (backward: of dx)           a multiple of 8, or 0      */
+  int64_t ldr;        /* pitch of residual (backward: of dh)    a multiple of 8, or 0      */
+  int64_t ldh;        /* pitch of h                             a multiple of 8, or 0      */
+  int64_t ldy;        /* pitch of y (backward: of dy)           a multiple of 8, or 0      */
+} moe_norm_problem;
+
+/*
+ * Root-mean-square norm with the residual's addition.  Per row:
+ *   h = x + residual, rounded to dtype (h = x without a residual);
+ *   rstd = 1 / sqrt(mean_j h_j^2 + eps);   y_j = h_j * rstd * weight_j.
+ * The 8-bit output takes the same y in float32, before any rounding, by the rule of
+ * moe_quantize_rows_fp8 (scale amax / 448 per 128 columns, 1 for an all-zero group): the rows
+ * moe_experts_forward_quantized takes.
+ *
+ *   x [T, H], residual [T, H] or NULL, weight [H]
+ *   y [T, H] out, or NULL when q is wanted alone;  rstd [T] float32 out
+ *   h [T, H] out, required exactly when residual is given; may be x or residual itself
+ *     (same pitch), which it then replaces
+ *   q [T, H] uint8 e4m3 codes and q_scale [T, H/128] float32, packed, out; both or neither
+ *     (MOE_BF16 only, H % 128 == 0)
+ * Errors: NULL_ARG, BAD_SHAPE, UNSUPPORTED before any HIP call; HIP.
+ */
+moe_status moe_rms_norm(const moe_norm_problem* p, const void* x, const void* residual, const void* weight, void* y,
+                        void* h, float* rstd, uint8_t* q, float* q_scale, void* stream);
+
+/* Bytes of workspace moe_rms_norm_backward takes (partial sums of dweight). */
+moe_status moe_rms_norm_workspace_size(const moe_norm_problem* p, size_t* bytes);
+
+/*
+ * Gradients of moe_rms_norm's y and h (n_j = h_j * rstd, g_j = dy_j * weight_j):
+ *   dx_j = rstd * (g_j - n_j * mean_i(g_i n_i)) + dh_j;   dweight_j = sum_t dy_j n_j.
+ * dx is the gradient of x and of the residual alike.
+ *
+ *   dy [T, H], h [T, H], weight [H], rstd [T] float32 (both as the forward left them)
+ *   dh [T, H] or NULL: the gradient that reaches h along the residual stream
+ *   dx [T, H] out; may be dy or dh itself (same pitch)
+ *   dweight [H] out, or NULL
+ */
+moe_status moe_rms_norm_backward(const moe_norm_problem* p, const void* dy, const void* h, const void* weight,
+                                 const float* rstd, const void* dh, void* dx, void* dweight, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int64_t T;          /* rows, 0 .. 2^31 - 1                                               */
+  int32_t K;          /* inputs, a multiple of 8, 8 .. 65536                               */
+  int32_t N;          /* outputs, 1 .. 2^20                                                */
+  int32_t dtype;      /* moe_dtype of x, w, bias, pre, dx, dw and dbias                    */
+  int32_t out_dtype;  /* moe_dtype of y, residual and dy: dtype or MOE_F32                 */
+  int32_t act;        /* moe_act                                                           */
+  int64_t ldx;        /* pitch of x                             a multiple of 8, or 0      */
+  int64_t ldy;        /* pitch of y (backward: of dy)                                      */
+  int64_t ldr;        /* pitch of residual                                                 */
+  int64_t ldp;        /* pitch of pre                                                      */
+  int64_t lddx;       /* pitch of dx                            a multiple of 8, or 0      */
+} moe_linear_problem;
+
+/* Bytes of workspace of moe_linear (backward == 0) or moe_linear_backward. */
+moe_status moe_linear_workspace_size(const moe_linear_problem* p, int backward, size_t* bytes);
+
+/*
+ * Linear with bias, activation and residual:  z = x w^T + bias;  y = act(z) + residual.
+ *
+ *   x [T, K], w [N, K], bias [N] or NULL, residual [T, N] or NULL
+ *   y [T, N] out; may be residual itself (same pitch), which it then replaces
+ *   pre [T, N] out or NULL: z in dtype, what the backward pass of an activation reads
+ * A router's logits are a linear with out_dtype MOE_F32.
+ */
+moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w, const void* bias, const void* residual,
+                      void* y, void* pre, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of moe_linear:  dz = dy * act'(pre);  dx = dz w;  dw = dz^T x;  dbias = sum_t dz.
+ * (The gradient of the residual is dy itself.)  relu'(0) = 0.  The two products take dz
+ * rounded to dtype; dbias sums it in float32 before that rounding.
+ *
+ *   dy [T, N], x [T, K], w [N, K]; pre [T, N] (not read, may be NULL, with MOE_ACT_NONE)
+ *   dx [T, K], dw [N, K], dbias [N] out; each may be NULL, and then is not computed, and
+ *   w (without dx) and x (without dw) may be NULL too
+ */
+moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, const void* x, const void* w,
+                               const void* pre, void* dx, void* dw, void* dbias, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int64_t T;          /* rows, 0 .. 2^31 - 1                                               */
+  int32_t H;          /* inputs, a multiple of 8, 8 .. 65536                               */
+  int32_t I;          /* outputs, a multiple of 8, 8 .. 65536                              */
+  int32_t dtype;      /* moe_dtype of every tensor                                         */
+  int32_t act;        /* moe_act of the gate: SILU, GELU or RELU                           */
+  int64_t ldx;        /* pitch of x                             a multiple of 8, or 0      */
+  int64_t lda;        /* pitch of a (backward: of da)           a multiple of 8, or 0      */
+  int64_t ldp;        /* pitch of pre (rows of 2I)              a multiple of 8, or 0      */
+  int64_t lddx;       /* pitch of dx                            a multiple of 8, or 0      */
+} moe_gated_problem;
+
+/* Bytes of workspace of moe_gated_linear (backward == 0) or moe_gated_linear_backward. */
+moe_status moe_gated_linear_workspace_size(const moe_gated_problem* p, int backward, size_t* bytes);
+
+/*
+ * Gated projection (SwiGLU, GeGLU, ReGLU) in one kernel:
+ *   [gate | up] = x w_gate_up^T + bias;   a = act(gate) * up.
+ * With moe_linear as its down projection it is the expert every token takes; w_gate_up
+ * has the layout of one routed expert's weights.
+ *
+ *   x [T, H]; w_gate_up [2I, H], rows [0, I) gate, rows [I, 2I) up; bias [2I] or NULL
+ *   a [T, I] out
+ *   pre [T, 2I] out or NULL: [gate | up] in dtype, what the backward pass reads
+ */
+moe_status moe_gated_linear(const moe_gated_problem* p, const void* x, const void* w_gate_up, const void* bias, void* a,
+                            void* pre, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of moe_gated_linear:  dz = [da * up * act'(gate) | da * act(gate)];
+ * dx = dz w_gate_up;  dw = dz^T x;  dbias = sum_t dz.  Roundings as in moe_linear_backward.
+ *
+ *   da [T, I], x [T, H], w_gate_up [2I, H], pre [T, 2I]
+ *   dx [T, H], dw [2I, H], dbias [2I] out; each may be NULL, with w_gate_up and x as there
+ */
+moe_status moe_gated_linear_backward(const moe_gated_problem* p, const void* da, const void* x, const void* w_gate_up,
+                                     const void* pre, void* dx, void* dw, void* dbias, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,8 @@ import torch
 
 __all__ = [
     "experts_forward", "experts_forward_noalloc", "check_scales", "check_mfma_blocks", "route", "route_logits", "quantize_rows_fp8", "workspace_size", "plan_describe",
+    "experts_forward_quantized", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "linear", "linear_backward",
+    "gated_linear", "gated_linear_backward", "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_RELU",
     "Problem", "MoeError", "lib", "FLAG_CHECK_INDICES", "FLAG_DETERMINISTIC", "FLAG_ATOMIC_COMBINE", "FLAG_ACT_GELU", "FLAG_ACT_RELU",
     "FLAG_FORCE_GROUPED", "FLAG_FORCE_DECODE", "LIB_PATH",
 ]
@@ -37,11 +39,16 @@ FLAG_FORCE_DECODE = 8
 FLAG_ATOMIC_COMBINE = 16
 FLAG_ACT_GELU = 32
 FLAG_ACT_RELU = 64
+# moe_act
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_RELU = range(4)
 
 EXPORTS = ["moe_abi_version", "moe_status_str", "moe_workspace_size", "moe_experts_forward",
            "moe_route", "moe_route_logits", "moe_quantize_rows_fp8", "moe_plan_describe",
            "moe_set_stage_events", "moe_check_mfma_blocks", "moe_experts_forward_noalloc",
-           "moe_noalloc_scratch_bytes"]
+           "moe_noalloc_scratch_bytes", "moe_experts_forward_quantized",
+           "moe_rms_norm", "moe_rms_norm_workspace_size", "moe_rms_norm_backward",
+           "moe_linear", "moe_linear_workspace_size", "moe_linear_backward",
+           "moe_gated_linear", "moe_gated_linear_workspace_size", "moe_gated_linear_backward"]
 
 # stage ids (moe_set_stage_events)
 STAGES = ["zero", "route", "quant_x", "gate_up", "quant_act", "down", "finalize"]
@@ -52,6 +59,23 @@ class Problem(ctypes.Structure):
                 ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
                 ("weight_dtype", ctypes.c_int32), ("scale_fmt", ctypes.c_int32),
                 ("flags", ctypes.c_uint32)]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldh", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class LinearProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("ldx", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldp", ctypes.c_int64), ("lddx", ctypes.c_int64)]
+
+
+class GatedProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("ldx", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldp", ctypes.c_int64),
+                ("lddx", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -96,6 +120,20 @@ def lib():
     L.moe_plan_describe.argtypes = [P, ctypes.c_char_p, sz]
     L.moe_check_mfma_blocks.restype = ctypes.c_int
     L.moe_check_mfma_blocks.argtypes = [ctypes.c_int, vp, vp, vp, vp, ctypes.c_int, vp]
+    L.moe_experts_forward_quantized.restype = ctypes.c_int
+    L.moe_experts_forward_quantized.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    PN, PL, PG = (ctypes.POINTER(c) for c in (NormProblem, LinearProblem, GatedProblem))
+    pz = ctypes.POINTER(sz)
+    for fn, args in ((L.moe_rms_norm, [PN] + [vp] * 9), (L.moe_rms_norm_workspace_size, [PN, pz]),
+                     (L.moe_rms_norm_backward, [PN] + [vp] * 8 + [sz, vp]),
+                     (L.moe_linear, [PL] + [vp] * 7 + [sz, vp]),
+                     (L.moe_linear_workspace_size, [PL, ctypes.c_int, pz]),
+                     (L.moe_linear_backward, [PL] + [vp] * 8 + [sz, vp]),
+                     (L.moe_gated_linear, [PG] + [vp] * 6 + [sz, vp]),
+                     (L.moe_gated_linear_workspace_size, [PG, ctypes.c_int, pz]),
+                     (L.moe_gated_linear_backward, [PG] + [vp] * 8 + [sz, vp])):
+        fn.restype = ctypes.c_int
+        fn.argtypes = args
     L.moe_set_stage_events.restype = ctypes.c_int
     L.moe_set_stage_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int]
     _lib = L
@@ -249,6 +287,47 @@ def experts_forward(hidden: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.
     return out
 
 
+def experts_forward_quantized(hidden_q: torch.Tensor, hidden_scale: torch.Tensor, topk_idx: torch.Tensor,
+                              topk_w: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                              w_gate_up_scale: torch.Tensor, w_down_scale: torch.Tensor,
+                              out: Optional[torch.Tensor] = None, flags: int = 0,
+                              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """experts_forward of e4m3 or fp4 experts on rows that are quantised already
+    (moe_experts_forward_quantized): hidden_q [T,H] e4m3 codes (uint8 or float8_e4m3fn) and
+    hidden_scale [T,H/128] float32, as rms_norm_fp8 and quantize_rows_fp8 return them.  The
+    output is bf16."""
+    for name, t in (("hidden_q", hidden_q), ("hidden_scale", hidden_scale), ("topk_idx", topk_idx),
+                    ("topk_w", topk_w), ("w_gate_up", w_gate_up), ("w_down", w_down),
+                    ("w_gate_up_scale", w_gate_up_scale), ("w_down_scale", w_down_scale)):
+        _need_gpu(name, t)
+    if hidden_q.dtype not in (torch.uint8, torch.float8_e4m3fn) or hidden_q.dim() != 2:
+        raise ValueError("hidden_q must be a 2-D tensor of e4m3 codes (uint8 or float8_e4m3fn)")
+    T, H = hidden_q.shape
+    if hidden_scale.dtype != torch.float32 or H % 128 or tuple(hidden_scale.shape) != (T, H // 128):
+        raise ValueError("hidden_scale must be float32 [T, H/128]")
+    if topk_idx.dtype != torch.int32 or topk_w.dtype != torch.float32:
+        raise ValueError("topk_idx must be int32 and topk_w float32")
+    if topk_w.shape != topk_idx.shape:
+        raise ValueError("topk_w and topk_idx shapes differ")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden_q.device)
+    else:
+        _need_gpu("out", out)
+        if tuple(out.shape) != (T, H) or out.dtype != torch.bfloat16:
+            raise ValueError("out must be bf16 [T, H]")
+    prob = problem_for(out, topk_idx, w_gate_up, w_down, w_gate_up_scale, flags)
+    check_scales(prob, w_gate_up_scale, w_down_scale)
+    if workspace is None:
+        workspace = torch.empty(max(workspace_size(prob), 1), dtype=torch.uint8, device=hidden_q.device)
+    else:
+        _need_gpu("workspace", workspace)
+    _check(lib().moe_experts_forward_quantized(
+        ctypes.byref(prob), _ptr(hidden_q), _ptr(hidden_scale), _ptr(topk_idx), _ptr(topk_w), _ptr(w_gate_up),
+        _ptr(w_down), _ptr(w_gate_up_scale), _ptr(w_down_scale), _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(hidden_q.device)))
+    return out
+
+
 def experts_forward_noalloc(hidden: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                             w_gate_up: torch.Tensor, w_down: torch.Tensor,
                             w_gate_up_scale: Optional[torch.Tensor] = None,
@@ -365,3 +444,233 @@ def check_mfma_blocks(a: torch.Tensor, b: torch.Tensor, b_scale: Optional[torch.
     d = torch.empty((n, 16, 16), dtype=torch.float32, device=a.device)
     _check(lib().moe_check_mfma_blocks(fmt, _ptr(a), _ptr(b), _ptr(b_scale), _ptr(d), n, _stream(a.device)))
     return d
+
+
+# ----------------------------------------------------------------------------- dense operators
+
+def _rows(name: str, t: torch.Tensor, cols: int, dtype, T: Optional[int] = None) -> int:
+    """Checks a [T, cols] activation matrix on the GPU; returns its row pitch in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.dim() != 2 or t.shape[1] != cols or (T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'T' if T is None else T}, {cols}]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    ld, inner = t.stride()
+    if t.shape[0] <= 1:
+        ld = cols
+    if (inner != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have unit stride along its rows and rows that do not overlap")
+    return ld
+
+
+def _vector(name: str, t: torch.Tensor, shape, dtype) -> None:
+    _need_gpu(name, t)
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _float_type(name: str, t: torch.Tensor) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype not in _ACT:
+        raise ValueError(f"{name} must be a bf16 or float32 tensor")
+    return _ACT[t.dtype]
+
+
+def _one_device(**tensors) -> None:
+    devices = {t.device for t in tensors.values() if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"tensors are on different devices: {sorted(str(d) for d in devices)}")
+
+
+def _run(fn, device: torch.device, *args) -> None:
+    """Calls fn(*args, current stream of `device`) with `device` current."""
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(workspace: Optional[torch.Tensor], size_fn, *args, device):
+    """(tensor or None, bytes): the caller's workspace, or one of the size the library asks for."""
+    if workspace is not None:
+        _need_gpu("workspace", workspace)
+        return workspace, workspace.numel() * workspace.element_size()
+    n = ctypes.c_size_t(0)
+    _check(size_fn(*args, ctypes.byref(n)))
+    if n.value == 0:
+        return None, 0
+    return torch.empty(n.value, dtype=torch.uint8, device=device), n.value
+
+
+def _rms_norm(x, weight, eps, residual, fp8, with_y):
+    dt = _float_type("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    prob = NormProblem(T, H, dt, eps, _rows("x", x, H, x.dtype), 0, 0, 0)
+    _vector("weight", weight, (H,), x.dtype)
+    h = x
+    if residual is not None:
+        prob.ldr = _rows("residual", residual, H, x.dtype, T)
+        h = torch.empty((T, H), dtype=x.dtype, device=x.device)
+    _one_device(x=x, weight=weight, residual=residual)
+    y = torch.empty((T, H), dtype=x.dtype, device=x.device) if with_y else None
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    q = scale = None
+    if fp8:
+        if x.dtype != torch.bfloat16 or H % 128:
+            raise ValueError("the 8-bit output takes bf16 rows with H a multiple of 128")
+        q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
+        scale = torch.empty((T, H // 128), dtype=torch.float32, device=x.device)
+    _run(lib().moe_rms_norm, x.device, ctypes.byref(prob), x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(y),
+         None if residual is None else h.data_ptr(), rstd.data_ptr(), _addr(q), _addr(scale))
+    return q, scale, y, h, rstd
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None):
+    """(y, h, rstd): h = x + residual (x itself without one), rstd = (mean h^2 + eps)^-1/2 [T]
+    float32, y = h * rstd * weight; see moe_rms_norm.  x, residual [T,H], weight [H], bf16 or float32."""
+    _, _, y, h, rstd = _rms_norm(x, weight, eps, residual, False, True)
+    return y, h, rstd
+
+
+def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None, with_y: bool = False):
+    """(q, scales, y, h, rstd): rms_norm with its result as e4m3 codes (uint8 [T,H]) and float32
+    scales [T,H/128], the rows experts_forward_quantized takes, and y in bf16 as well when
+    with_y (else None)."""
+    return _rms_norm(x, weight, eps, residual, True, with_y)
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                      dh: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(dx, dweight) of rms_norm, from dy and dh, the gradient that reaches h along the residual
+    stream; dx is the gradient of x and of the residual.  See moe_rms_norm_backward."""
+    dt = _float_type("h", h)
+    if h.dim() != 2:
+        raise ValueError("h must be [T, H]")
+    T, H = h.shape
+    prob = NormProblem(T, H, dt, 0.0, 0, 0, _rows("h", h, H, h.dtype), _rows("dy", dy, H, h.dtype, T))
+    _vector("weight", weight, (H,), h.dtype)
+    _vector("rstd", rstd, (T,), torch.float32)
+    if dh is not None:
+        prob.ldr = _rows("dh", dh, H, h.dtype, T)
+    _one_device(dy=dy, h=h, weight=weight, rstd=rstd, dh=dh, workspace=workspace)
+    dx = torch.empty((T, H), dtype=h.dtype, device=h.device)
+    dweight = torch.empty(H, dtype=h.dtype, device=h.device)
+    L = lib()
+    ws, n = _scratch(workspace, L.moe_rms_norm_workspace_size, ctypes.byref(prob), device=h.device)
+    _run(L.moe_rms_norm_backward, h.device, ctypes.byref(prob), dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
+         rstd.data_ptr(), _addr(dh), dx.data_ptr(), dweight.data_ptr(), _addr(ws), n)
+    return dx, dweight
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           residual: Optional[torch.Tensor] = None, act: int = ACT_NONE, out_dtype: Optional[torch.dtype] = None,
+           save_pre: bool = False, workspace: Optional[torch.Tensor] = None):
+    """(y, pre): y = act(x w^T + bias) + residual in out_dtype (x's, or float32), and pre = x w^T +
+    bias when save_pre (else None).  x [T,K], w [N,K], bias [N], residual [T,N] in
+    out_dtype; see moe_linear."""
+    dt = _float_type("x", x)
+    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("x must be [T, K] and w [N, K]")
+    T, K = x.shape
+    N = w.shape[0]
+    odt = x.dtype if out_dtype is None else out_dtype
+    if odt not in _ACT:
+        raise ValueError("out_dtype must be bf16 or float32")
+    prob = LinearProblem(T, K, N, dt, _ACT[odt], act, _rows("x", x, K, x.dtype), 0, 0, 0, 0)
+    _vector("w", w, (N, K), x.dtype)
+    if bias is not None:
+        _vector("bias", bias, (N,), x.dtype)
+    if residual is not None:
+        prob.ldr = _rows("residual", residual, N, odt, T)
+    _one_device(x=x, w=w, bias=bias, residual=residual, workspace=workspace)
+    y = torch.empty((T, N), dtype=odt, device=x.device)
+    pre = torch.empty((T, N), dtype=x.dtype, device=x.device) if save_pre else None
+    L = lib()
+    ws, n = _scratch(workspace, L.moe_linear_workspace_size, ctypes.byref(prob), 0, device=x.device)
+    _run(L.moe_linear, x.device, ctypes.byref(prob), x.data_ptr(), w.data_ptr(), _addr(bias), _addr(residual),
+         y.data_ptr(), _addr(pre), _addr(ws), n)
+    return y, pre
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre: Optional[torch.Tensor] = None,
+                    act: int = ACT_NONE, need_bias: bool = False, workspace: Optional[torch.Tensor] = None):
+    """(dx, dw, dbias) of linear, dbias None without need_bias; pre is what linear saved (needed
+    with an activation).  See moe_linear_backward."""
+    dt = _float_type("x", x)
+    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("x must be [T, K] and w [N, K]")
+    T, K = x.shape
+    N = w.shape[0]
+    ody = _float_type("dy", dy)
+    prob = LinearProblem(T, K, N, dt, ody, act, _rows("x", x, K, x.dtype), _rows("dy", dy, N, dy.dtype, T), 0, 0, 0)
+    _vector("w", w, (N, K), x.dtype)
+    if act != ACT_NONE:
+        if pre is None:
+            raise ValueError("an activation's gradient needs pre")
+        prob.ldp = _rows("pre", pre, N, x.dtype, T)
+    else:
+        pre = None
+    _one_device(dy=dy, x=x, w=w, pre=pre, workspace=workspace)
+    L = lib()
+    return _backward(L.moe_linear_backward, L.moe_linear_workspace_size, prob, dy, x, w, pre, N, need_bias, workspace)
+
+
+def _backward(fn, size_fn, prob, dy, x, w, pre, cols, need_bias, workspace):
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(w)
+    dbias = torch.empty(cols, dtype=x.dtype, device=x.device) if need_bias else None
+    ws, n = _scratch(workspace, size_fn, ctypes.byref(prob), 1, device=x.device)
+    _run(fn, x.device, ctypes.byref(prob), dy.data_ptr(), x.data_ptr(), w.data_ptr(), _addr(pre), dx.data_ptr(),
+         dw.data_ptr(), _addr(dbias), _addr(ws), n)
+    return dx, dw, dbias
+
+
+def gated_linear(x: torch.Tensor, w_gate_up: torch.Tensor, bias: Optional[torch.Tensor] = None, act: int = ACT_SILU,
+                 save_pre: bool = False, workspace: Optional[torch.Tensor] = None):
+    """(a, pre): [gate | up] = x w_gate_up^T + bias, a = act(gate) * up [T,I], and pre = [gate |
+    up] [T,2I] when save_pre (else None).  x [T,H], w_gate_up [2I,H], bias [2I]; see moe_gated_linear."""
+    dt = _float_type("x", x)
+    if x.dim() != 2 or not isinstance(w_gate_up, torch.Tensor) or w_gate_up.dim() != 2 or w_gate_up.shape[0] % 2:
+        raise ValueError("x must be [T, H] and w_gate_up [2I, H]")
+    T, H = x.shape
+    I = w_gate_up.shape[0] // 2
+    prob = GatedProblem(T, H, I, dt, act, _rows("x", x, H, x.dtype), 0, 0, 0)
+    _vector("w_gate_up", w_gate_up, (2 * I, H), x.dtype)
+    if bias is not None:
+        _vector("bias", bias, (2 * I,), x.dtype)
+    _one_device(x=x, w_gate_up=w_gate_up, bias=bias, workspace=workspace)
+    a = torch.empty((T, I), dtype=x.dtype, device=x.device)
+    pre = torch.empty((T, 2 * I), dtype=x.dtype, device=x.device) if save_pre else None
+    L = lib()
+    ws, n = _scratch(workspace, L.moe_gated_linear_workspace_size, ctypes.byref(prob), 0, device=x.device)
+    _run(L.moe_gated_linear, x.device, ctypes.byref(prob), x.data_ptr(), w_gate_up.data_ptr(), _addr(bias),
+         a.data_ptr(), _addr(pre), _addr(ws), n)
+    return a, pre
+
+
+def gated_linear_backward(da: torch.Tensor, x: torch.Tensor, w_gate_up: torch.Tensor, pre: torch.Tensor,
+                          act: int = ACT_SILU, need_bias: bool = False, workspace: Optional[torch.Tensor] = None):
+    """(dx, dw, dbias) of gated_linear from da and the pre it saved; dbias None without need_bias.
+    See moe_gated_linear_backward."""
+    dt = _float_type("x", x)
+    if x.dim() != 2 or not isinstance(w_gate_up, torch.Tensor) or w_gate_up.dim() != 2 or w_gate_up.shape[0] % 2:
+        raise ValueError("x must be [T, H] and w_gate_up [2I, H]")
+    T, H = x.shape
+    I = w_gate_up.shape[0] // 2
+    prob = GatedProblem(T, H, I, dt, act, _rows("x", x, H, x.dtype), _rows("da", da, I, x.dtype, T),
+                        _rows("pre", pre, 2 * I, x.dtype, T), 0)
+    _vector("w_gate_up", w_gate_up, (2 * I, H), x.dtype)
+    _one_device(da=da, x=x, w_gate_up=w_gate_up, pre=pre, workspace=workspace)
+    L = lib()
+    return _backward(L.moe_gated_linear_backward, L.moe_gated_linear_workspace_size, prob, da, x, w_gate_up, pre, 2 * I,
+                     need_bias, workspace)

@@ -381,9 +381,10 @@ moe_status check_forward_args(const moe_problem* p, const void* hidden, const in
 // The forward's launches, arguments already checked (check_forward_args, T > 0) and the
 // workspace (16-byte aligned) holding at least make_layout(*p).total bytes.  Everything it
 // reads from the workspace is written first by its own kernels, so the workspace's
-// previous contents do not matter.
-moe_status forward_launch(const moe_problem* p, const void* hidden, const int32_t* topk_idx, const float* topk_w,
-                          const void* w_gate_up, const void* w_down, const void* w_gate_up_scale,
+// previous contents do not matter.  hidden_scale: null, or the scales of hidden rows that are
+// e4m3 codes already (fp8 and fp4 weights).
+moe_status forward_launch(const moe_problem* p, const void* hidden, const float* hidden_scale, const int32_t* topk_idx,
+                          const float* topk_w, const void* w_gate_up, const void* w_down, const void* w_gate_up_scale,
                           const void* w_down_scale, void* out, void* workspace, DeviceRecord* dev, void* stream) {
   const bool fp8 = quant_acts(*p);     // e4m3 activation rows (fp8 and fp4 weights)
   const bool fp4 = is_fp4(*p);
@@ -457,8 +458,9 @@ moe_status forward_launch(const moe_problem* p, const void* hidden, const int32_
 
   // gate_up + SwiGLU: rows = hidden rows gathered through perm (token = slot / k)
   GroupedArgs gu = g;
-  gu.a = fp8 ? (const void*)(ws + L.x_q) : hidden;
-  gu.a_scale = fp8 ? reinterpret_cast<const float*>(ws + L.x_s) : nullptr;
+  const bool quant_x = fp8 && !hidden_scale;
+  gu.a = quant_x ? (const void*)(ws + L.x_q) : hidden;
+  gu.a_scale = quant_x ? reinterpret_cast<const float*>(ws + L.x_s) : hidden_scale;
   gu.a_rows = perm;
   gu.a_row_div = p->k;
   gu.lda = p->H;
@@ -486,7 +488,7 @@ moe_status forward_launch(const moe_problem* p, const void* hidden, const int32_
   dn.b_expert_stride = (int64_t)p->H * p->I / (fp4 ? 2 : 1);
   dn.K = p->I;
 
-  if (fp8) {
+  if (quant_x) {
     MOE_HIP_CHECK(stage_mark(MOE_STAGE_QUANT_X, 0, s));
     MOE_HIP_CHECK(launch_quant_rows_bf16(hidden, p->T, p->H, reinterpret_cast<uint8_t*>(ws + L.x_q),
                                          reinterpret_cast<float*>(ws + L.x_s), s));
@@ -598,8 +600,26 @@ moe_status moe_experts_forward(const moe_problem* p, const void* hidden, const i
   if (workspace_bytes < make_layout(*p).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   DeviceRecord* dev = nullptr;
   if ((st = device_record(&dev)) != MOE_OK) return st;
-  return forward_launch(p, hidden, topk_idx, topk_w, w_gate_up, w_down, w_gate_up_scale, w_down_scale, out, workspace,
-                        dev, stream);
+  return forward_launch(p, hidden, nullptr, topk_idx, topk_w, w_gate_up, w_down, w_gate_up_scale, w_down_scale, out,
+                        workspace, dev, stream);
+}
+
+moe_status moe_experts_forward_quantized(const moe_problem* p, const uint8_t* hidden_q, const float* hidden_scale,
+                                         const int32_t* topk_idx, const float* topk_w, const void* w_gate_up,
+                                         const void* w_down, const void* w_gate_up_scale, const void* w_down_scale,
+                                         void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  moe_status st = check_forward_args(p, hidden_q, topk_idx, topk_w, w_gate_up, w_down, w_gate_up_scale, w_down_scale,
+                                     out);
+  if (st != MOE_OK) return st;
+  if (!quant_acts(*p)) return MOE_ERR_UNSUPPORTED;
+  if (p->T == 0) return MOE_OK;
+  if (!hidden_scale || !workspace) return MOE_ERR_NULL_ARG;
+  if (!aligned16(hidden_scale) || !aligned16(workspace)) return MOE_ERR_BAD_SHAPE;
+  if (workspace_bytes < make_layout(*p).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  DeviceRecord* dev = nullptr;
+  if ((st = device_record(&dev)) != MOE_OK) return st;
+  return forward_launch(p, hidden_q, hidden_scale, topk_idx, topk_w, w_gate_up, w_down, w_gate_up_scale, w_down_scale,
+                        out, workspace, dev, stream);
 }
 
 size_t moe_noalloc_scratch_bytes(void) { return kNoAllocScratchBytes; }
@@ -616,8 +636,8 @@ moe_status moe_experts_forward_noalloc(const moe_problem* p, const void* hidden,
   if ((st = device_record(&dev)) != MOE_OK) return st;
   void* ws = nullptr;
   if ((st = scratch_address(&ws)) != MOE_OK) return st;
-  return forward_launch(p, hidden, topk_idx, topk_w, w_gate_up, w_down, w_gate_up_scale, w_down_scale, out, ws, dev,
-                        stream);
+  return forward_launch(p, hidden, nullptr, topk_idx, topk_w, w_gate_up, w_down, w_gate_up_scale, w_down_scale, out, ws,
+                        dev, stream);
 }
 
 moe_status moe_set_stage_events(void* const* events, int n) {

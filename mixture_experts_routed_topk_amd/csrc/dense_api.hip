@@ -1,0 +1,354 @@
+// C ABI of the dense operators around the routed experts: argument validation (before any
+// HIP call), workspace layouts and launches.
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include "../../include/moe_experts.h"
+#include "dense_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxPitch = int64_t(1) << 22;   // tile offsets fit in 32 bits
+constexpr int kMaxWidth = 65536;                  // H, I, K
+constexpr int kMaxOutputs = 1 << 20;              // N
+
+bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
+bool aligned4(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0; }
+template <typename... P>
+bool all_aligned16(P... p) { return (aligned16(p) && ...); }
+bool type_ok(int t) { return t == MOE_F32 || t == MOE_BF16; }
+bool width_ok(int w) { return w >= 8 && w <= kMaxWidth && w % 8 == 0; }
+bool pitch_ok(int64_t ld, int64_t cols, bool vec) {
+  return ld == 0 || (ld >= cols && ld <= kMaxPitch && (!vec || ld % 8 == 0));
+}
+int64_t pitch(int64_t ld, int64_t cols) { return ld ? ld : cols; }
+size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+size_t esize(int t) { return t == MOE_F32 ? 4 : 2; }
+// a matrix ends inside a 48-bit address range whatever its pitch: T < 2^31, ld <= 2^22
+
+moe_status check(const moe_norm_problem* p) {
+  if (!p) return MOE_ERR_NULL_ARG;
+  if (!type_ok(p->dtype)) return MOE_ERR_UNSUPPORTED;
+  if (p->T < 0 || p->T > kMaxRows || !width_ok(p->H) || !(p->eps >= 0.f) || !isfinite(p->eps)) return MOE_ERR_BAD_SHAPE;
+  for (int64_t ld : {p->ldx, p->ldr, p->ldh, p->ldy})
+    if (!pitch_ok(ld, p->H, true)) return MOE_ERR_BAD_SHAPE;
+  return MOE_OK;
+}
+
+moe_status check(const moe_linear_problem* p) {
+  if (!p) return MOE_ERR_NULL_ARG;
+  if (!type_ok(p->dtype) || (p->out_dtype != p->dtype && p->out_dtype != MOE_F32)) return MOE_ERR_UNSUPPORTED;
+  if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_RELU) return MOE_ERR_UNSUPPORTED;
+  if (p->T < 0 || p->T > kMaxRows || !width_ok(p->K) || p->N < 1 || p->N > kMaxOutputs) return MOE_ERR_BAD_SHAPE;
+  if (!pitch_ok(p->ldx, p->K, true) || !pitch_ok(p->lddx, p->K, true)) return MOE_ERR_BAD_SHAPE;
+  for (int64_t ld : {p->ldy, p->ldr, p->ldp})
+    if (!pitch_ok(ld, p->N, false)) return MOE_ERR_BAD_SHAPE;
+  return MOE_OK;
+}
+
+moe_status check(const moe_gated_problem* p) {
+  if (!p) return MOE_ERR_NULL_ARG;
+  if (!type_ok(p->dtype)) return MOE_ERR_UNSUPPORTED;
+  if (p->act < MOE_ACT_SILU || p->act > MOE_ACT_RELU) return MOE_ERR_UNSUPPORTED;
+  if (p->T < 0 || p->T > kMaxRows || !width_ok(p->H) || !width_ok(p->I)) return MOE_ERR_BAD_SHAPE;
+  if (!pitch_ok(p->ldx, p->H, true) || !pitch_ok(p->lddx, p->H, true) || !pitch_ok(p->lda, p->I, true) ||
+      !pitch_ok(p->ldp, 2 * (int64_t)p->I, true))
+    return MOE_ERR_BAD_SHAPE;
+  return MOE_OK;
+}
+
+// The backward pass of a linear or gated projection in one form: dz has `cols` columns, the
+// products contract over T (dw) and over dz's columns (dx).
+struct Backward {
+  int64_t T;
+  int K;             // columns of x
+  int N;             // columns of dy
+  int64_t cols;      // columns of dz (gated: 2 N)
+  int dtype, dy_dtype, act, gated;
+  int64_t ldx, ldy, ldp, lddx;
+};
+Backward backward_of(const moe_linear_problem& p) {
+  return {p.T, p.K, p.N, p.N, p.dtype, p.out_dtype, p.act, 0,
+          pitch(p.ldx, p.K), pitch(p.ldy, p.N), pitch(p.ldp, p.N), pitch(p.lddx, p.K)};
+}
+Backward backward_of(const moe_gated_problem& p) {
+  return {p.T, p.H, p.I, 2 * (int64_t)p.I, p.dtype, p.dtype, p.act, 1,
+          pitch(p.ldx, p.H), pitch(p.lda, p.I), pitch(p.ldp, 2 * (int64_t)p.I), pitch(p.lddx, p.H)};
+}
+
+// dz is dy itself when nothing is to be done to it and the products can read its rows in
+// 16-byte pieces; otherwise it is written to the workspace.
+bool dz_is_dy(const Backward& b) {
+  return !b.gated && b.act == MOE_ACT_NONE && b.dy_dtype == b.dtype && b.N % 8 == 0 && b.ldy % 8 == 0;
+}
+int64_t dz_pitch(const Backward& b) { return (b.cols + 7) / 8 * 8; }
+
+struct BackwardLayout {
+  size_t dz, part, gemm, total;
+};
+BackwardLayout layout(const Backward& b) {
+  BackwardLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = up256(o + bytes);
+    return at;
+  };
+  const bool f32 = b.dtype == MOE_F32;
+  L.dz = take(dz_is_dy(b) ? 0 : (size_t)b.T * dz_pitch(b) * esize(b.dtype));
+  L.part = take((size_t)dz_parts(b.T) * b.cols * 4);
+  const size_t dx = dense_gemm_workspace(b.T, b.K, b.cols, 0, 0, 1, f32);
+  const size_t dw = dense_gemm_workspace(b.cols, b.K, b.T, 0, 1, 1, f32);
+  L.gemm = take(dx > dw ? dx : dw);
+  L.total = o;
+  return L;
+}
+
+#define MOE_HIP_CHECK(expr)                       \
+  do {                                            \
+    if ((expr) != hipSuccess) return MOE_ERR_HIP; \
+  } while (0)
+
+moe_status run_backward(const Backward& b, const void* dy, const void* x, const void* w, const void* pre, void* dx,
+                        void* dw, void* dbias, void* workspace, size_t workspace_bytes, hipStream_t s) {
+  const bool f32 = b.dtype == MOE_F32;
+  const bool need_pre = b.act != MOE_ACT_NONE;
+  if (b.T > 0 && (!dy || (need_pre && !pre) || (dx && !w) || (dw && !x))) return MOE_ERR_NULL_ARG;
+  if (!all_aligned16(dy, x, w, pre, dx, dw, dbias, workspace)) return MOE_ERR_BAD_SHAPE;
+  const BackwardLayout L = layout(b);
+  if (b.T > 0 && L.total > 0 && !workspace) return MOE_ERR_NULL_ARG;
+  if (b.T > 0 && workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  (void)hipGetLastError();   // an error left by an earlier, unrelated HIP call is not ours
+  if (b.T == 0) {
+    if (dw) MOE_HIP_CHECK(launch_zero_bytes(dw, b.cols * b.K * (int64_t)esize(b.dtype), s));
+    if (dbias) MOE_HIP_CHECK(launch_zero_bytes(dbias, b.cols * (int64_t)esize(b.dtype), s));
+    return MOE_OK;
+  }
+  char* ws = static_cast<char*>(workspace);
+  const bool direct = dz_is_dy(b);
+  const void* dz = direct ? dy : ws + L.dz;
+  const int64_t lddz = direct ? b.ldy : dz_pitch(b);
+  if (dbias || (!direct && (dx || dw))) {
+    DzArgs a{};
+    a.T = b.T;
+    a.N = b.N;
+    a.gated = b.gated;
+    a.act = b.act;
+    a.dy = dy;
+    a.ldy = b.ldy;
+    a.dy_f32 = b.dy_dtype == MOE_F32;
+    a.pre = need_pre ? pre : nullptr;
+    a.ldp = b.ldp;
+    a.dz = !direct && (dx || dw) ? ws + L.dz : nullptr;
+    a.ldz = dz_pitch(b);
+    a.part = dbias ? reinterpret_cast<float*>(ws + L.part) : nullptr;
+    a.dbias = dbias;
+    MOE_HIP_CHECK(launch_dz(a, f32, s));
+  }
+  auto product = [&](const void* r, int64_t ldr, int r_kmajor, const void* c, int64_t ldc, int64_t M, int64_t K, void* out,
+                     int64_t ldo) {
+    DenseGemm g{};
+    g.r = r;
+    g.ldr = ldr;
+    g.r_kmajor = r_kmajor;
+    g.c = c;
+    g.ldc = ldc;
+    g.c_kmajor = 1;
+    g.M = M;
+    g.K = K;
+    g.e.out = out;
+    g.e.ldo = ldo;
+    g.e.N = b.K;
+    g.e.vec = 1;
+    return launch_dense_gemm(g, ws + L.gemm, f32, s);
+  };
+  if (dx) MOE_HIP_CHECK(product(dz, lddz, 0, w, b.K, b.T, b.cols, dx, b.lddx));
+  if (dw) MOE_HIP_CHECK(product(dz, lddz, 1, x, b.ldx, b.cols, b.T, dw, b.K));
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_rms_norm(const moe_norm_problem* p, const void* x, const void* residual, const void* weight, void* y,
+                        void* h, float* rstd, uint8_t* q, float* q_scale, void* stream) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  if (q || q_scale) {
+    if (p->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (p->H % 128 != 0) return MOE_ERR_BAD_SHAPE;
+  }
+  if (p->T == 0) return MOE_OK;
+  if (!x || !weight || !rstd || (!y && !q) || !q != !q_scale || !residual != !h) return MOE_ERR_NULL_ARG;
+  if (!all_aligned16(x, residual, weight, y, h, q) || !aligned4(rstd) || !aligned4(q_scale)) return MOE_ERR_BAD_SHAPE;
+  (void)hipGetLastError();
+  NormArgs a{};
+  a.T = p->T;
+  a.H = p->H;
+  a.eps = p->eps;
+  a.ldx = pitch(p->ldx, p->H);
+  a.ldr = pitch(p->ldr, p->H);
+  a.ldh = pitch(p->ldh, p->H);
+  a.ldy = pitch(p->ldy, p->H);
+  a.x = x;
+  a.res = residual;
+  a.weight = weight;
+  a.y = y;
+  a.h = h;
+  a.rstd = rstd;
+  a.q = q;
+  a.q_scale = q_scale;
+  MOE_HIP_CHECK(launch_rms_norm(a, p->dtype == MOE_F32, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_rms_norm_workspace_size(const moe_norm_problem* p, size_t* bytes) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_NULL_ARG;
+  *bytes = up256((size_t)norm_backward_parts(p->T, p->H) * p->H * 4);
+  return MOE_OK;
+}
+
+moe_status moe_rms_norm_backward(const moe_norm_problem* p, const void* dy, const void* h, const void* weight,
+                                 const float* rstd, const void* dh, void* dx, void* dweight, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool f32 = p->dtype == MOE_F32;
+  if (!all_aligned16(dy, h, weight, dh, dx, dweight, workspace) || !aligned4(rstd)) return MOE_ERR_BAD_SHAPE;
+  if (p->T == 0) {
+    (void)hipGetLastError();
+    if (dweight) MOE_HIP_CHECK(launch_zero_bytes(dweight, (int64_t)p->H * (int64_t)esize(p->dtype), s));
+    return MOE_OK;
+  }
+  if (!dy || !h || !weight || !rstd || !dx || (dweight && !workspace)) return MOE_ERR_NULL_ARG;
+  if (dweight && workspace_bytes < up256((size_t)norm_backward_parts(p->T, p->H) * p->H * 4))
+    return MOE_ERR_WORKSPACE_TOO_SMALL;
+  (void)hipGetLastError();
+  NormArgs a{};
+  a.T = p->T;
+  a.H = p->H;
+  a.ldx = pitch(p->ldx, p->H);
+  a.ldr = pitch(p->ldr, p->H);
+  a.ldh = pitch(p->ldh, p->H);
+  a.ldy = pitch(p->ldy, p->H);
+  a.dy = dy;
+  a.hin = h;
+  a.weight = weight;
+  a.rstd_in = rstd;
+  a.res = dh;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  MOE_HIP_CHECK(launch_rms_norm_backward(a, f32, s));
+  return MOE_OK;
+}
+
+moe_status moe_linear_workspace_size(const moe_linear_problem* p, int backward, size_t* bytes) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_NULL_ARG;
+  *bytes = backward ? layout(backward_of(*p)).total : dense_gemm_workspace(p->T, p->N, p->K, 0, 0, 0, p->dtype == MOE_F32);
+  return MOE_OK;
+}
+
+moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w, const void* bias, const void* residual,
+                      void* y, void* pre, void* workspace, size_t workspace_bytes, void* stream) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  if (p->T == 0) return MOE_OK;
+  const bool f32 = p->dtype == MOE_F32;
+  const size_t need = dense_gemm_workspace(p->T, p->N, p->K, 0, 0, 0, f32);
+  if (!x || !w || !y || (need && !workspace)) return MOE_ERR_NULL_ARG;
+  if (!all_aligned16(x, w, bias, residual, y, pre, workspace)) return MOE_ERR_BAD_SHAPE;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  (void)hipGetLastError();
+  DenseGemm g{};
+  g.r = x;
+  g.ldr = pitch(p->ldx, p->K);
+  g.c = w;
+  g.ldc = p->K;
+  g.M = p->T;
+  g.K = p->K;
+  g.e.out = y;
+  g.e.ldo = pitch(p->ldy, p->N);
+  g.e.out_f32 = p->out_dtype == MOE_F32;
+  g.e.bias = bias;
+  g.e.res = residual;
+  g.e.ldr = pitch(p->ldr, p->N);
+  g.e.pre = pre;
+  g.e.ldp = pitch(p->ldp, p->N);
+  g.e.act = p->act;
+  g.e.N = p->N;
+  g.e.vec = p->N % 8 == 0 && g.e.ldo % 8 == 0 && (!residual || g.e.ldr % 8 == 0) && (!pre || g.e.ldp % 8 == 0);
+  MOE_HIP_CHECK(launch_dense_gemm(g, workspace, f32, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, const void* x, const void* w,
+                               const void* pre, void* dx, void* dw, void* dbias, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  return run_backward(backward_of(*p), dy, x, w, pre, dx, dw, dbias, workspace, workspace_bytes,
+                      static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_gated_linear_workspace_size(const moe_gated_problem* p, int backward, size_t* bytes) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_NULL_ARG;
+  *bytes = backward ? layout(backward_of(*p)).total : dense_gemm_workspace(p->T, p->I, p->H, 1, 0, 0, p->dtype == MOE_F32);
+  return MOE_OK;
+}
+
+moe_status moe_gated_linear(const moe_gated_problem* p, const void* x, const void* w_gate_up, const void* bias, void* a,
+                            void* pre, void* workspace, size_t workspace_bytes, void* stream) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  if (p->T == 0) return MOE_OK;
+  const bool f32 = p->dtype == MOE_F32;
+  const size_t need = dense_gemm_workspace(p->T, p->I, p->H, 1, 0, 0, f32);
+  if (!x || !w_gate_up || !a || (need && !workspace)) return MOE_ERR_NULL_ARG;
+  if (!all_aligned16(x, w_gate_up, bias, a, pre, workspace)) return MOE_ERR_BAD_SHAPE;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  (void)hipGetLastError();
+  DenseGemm g{};
+  g.r = x;
+  g.ldr = pitch(p->ldx, p->H);
+  g.c = w_gate_up;
+  g.ldc = p->H;
+  g.M = p->T;
+  g.K = p->H;
+  g.gated = 1;
+  g.e.out = a;
+  g.e.ldo = pitch(p->lda, p->I);
+  g.e.out_f32 = f32;
+  g.e.bias = bias;
+  g.e.pre = pre;
+  g.e.ldp = pitch(p->ldp, 2 * (int64_t)p->I);
+  g.e.act = p->act;
+  g.e.N = p->I;
+  g.e.vec = 1;
+  MOE_HIP_CHECK(launch_dense_gemm(g, workspace, f32, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_gated_linear_backward(const moe_gated_problem* p, const void* da, const void* x, const void* w_gate_up,
+                                     const void* pre, void* dx, void* dw, void* dbias, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  const moe_status st = check(p);
+  if (st != MOE_OK) return st;
+  return run_backward(backward_of(*p), da, x, w_gate_up, pre, dx, dw, dbias, workspace, workspace_bytes,
+                      static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,105 @@
+// Launch interfaces of the dense operators around the routed experts: RMS norm, linear
+// and gated projections, forward and backward (dense_api.hip checks the arguments).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+// ---------------------------------------------------------------------------- RMS norm
+struct NormArgs {
+  int64_t T;
+  int H;
+  float eps;
+  int64_t ldx, ldr, ldh, ldy;   // row pitches in elements
+  const void* x;                // backward: dx is written through xo
+  const void* res;              // residual (backward: dh), may be null
+  const void* weight;
+  void* y;                      // may be null (backward: dy is read through dy)
+  void* h;                      // x + residual (forward, when there is a residual)
+  float* rstd;
+  uint8_t* q;                   // e4m3 codes [T][H], may be null
+  float* q_scale;               // [T][H/128]
+  // backward
+  const void* dy;
+  const void* hin;
+  const float* rstd_in;
+  void* dx;
+  void* dweight;
+  float* part;                  // [norm_backward_parts(T, H)][H]
+};
+hipError_t launch_rms_norm(const NormArgs& a, bool f32, hipStream_t s);
+int64_t norm_backward_parts(int64_t T, int H);
+hipError_t launch_rms_norm_backward(const NormArgs& a, bool f32, hipStream_t s);
+
+// ---------------------------------------------------------------------------- matrix products
+enum { kActNone = 0, kActSilu = 1, kActGelu = 2, kActRelu = 3 };
+
+// What becomes of a product's element z = sum_k r[m][k] c[n][k]:
+//   z += bias[n]; pre[m][n] = z; out[m][n] = act(z) + res[m][n], or, gated,
+//   out[m][n] = act(z_gate) * z_up with the gate in rows [0, I) and the up projection in
+//   rows [I, 2I) of the second operand (pre holds both, [m][2I]).
+struct DenseEpi {
+  void* out;
+  int64_t ldo;
+  int out_f32;                  // out and res are float32 (else the operands' type)
+  const void* bias;             // operands' type, may be null
+  const void* res;              // may be null
+  int64_t ldr;
+  void* pre;                    // operands' type, may be null
+  int64_t ldp;
+  int act;
+  int N;                        // output columns (gated: I)
+  int vec;                      // rows of out, res and pre may be accessed in 16-byte pieces
+};
+
+// out[M][N] from r (M rows) and c (N rows, gated 2N): element (m, k) of r is r[m * ldr + k],
+// or r[k * ldr + m] with r_kmajor; c likewise.
+struct DenseGemm {
+  const void* r;
+  int64_t ldr;
+  int r_kmajor;
+  const void* c;
+  int64_t ldc;
+  int c_kmajor;
+  int64_t M;
+  int64_t K;
+  int gated;
+  DenseEpi e;
+};
+// Bytes of scratch the product takes (partial sums of a split contraction).
+size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32);
+hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s);
+
+// float32 products (any pitch, any alignment)
+hipError_t launch_dense_gemm_f32(const DenseGemm& g, hipStream_t s);
+
+// ---------------------------------------------------------------------------- backward
+// dz = dy * act'(pre) (gated: [da * up * act'(gate), da * act(gate)]) in the operands' type,
+// [T][ldz] with zeros in columns [cols, ldz), and its column sums.
+struct DzArgs {
+  int64_t T;
+  int N;                        // columns of dy (gated: I; dz has 2I)
+  int gated;
+  int act;
+  const void* dy;
+  int64_t ldy;
+  int dy_f32;                   // dy is float32 (else the operands' type)
+  const void* pre;
+  int64_t ldp;
+  void* dz;                     // may be null: column sums only
+  int64_t ldz;
+  float* part;                  // [dz_parts(T)][cols], null without dbias
+  void* dbias;                  // operands' type
+};
+int64_t dz_parts(int64_t T);
+hipError_t launch_dz(const DzArgs& a, bool f32, hipStream_t s);
+
+// out[j] = sum_i part[i][j] in the order of i, rounded to bf16 (or float32 with f32)
+hipError_t launch_column_sum(const float* part, int64_t rows, int64_t cols, void* out, bool f32, hipStream_t s);
+// zeros (T = 0: gradients of parameters)
+hipError_t launch_zero_bytes(void* p, int64_t bytes, hipStream_t s);
+
+}  // namespace moe

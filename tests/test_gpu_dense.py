@@ -1,0 +1,247 @@
+"""The dense operators around the routed experts (RMS norm, linear, gated projection) against
+their 64-bit plain forms (dense_ref.py, whose bounds are derived there), forward and backward."""
+
+import zlib
+
+import pytest
+import torch
+
+import dense_ref as ref
+import mixture_experts_routed_topk_amd as m
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+ACT = {"none": m.ACT_NONE, "silu": m.ACT_SILU, "gelu": m.ACT_GELU, "relu": m.ACT_RELU}
+EPS = 1e-6
+
+
+def rnd(name, shape, dtype, std=1.0, mean=0.0, pad=0):
+    """Seeded normal values; pad > 0: rows inside a wider buffer whose other columns are NaN."""
+    g = torch.Generator(device="cpu").manual_seed(zlib.crc32(repr((name, shape)).encode()))
+    t = (torch.randn(shape, generator=g) * std + mean).to(dtype).cuda()
+    if not pad:
+        return t
+    wide = torch.full((shape[0], shape[1] + pad), float("nan"), dtype=dtype, device="cuda")
+    wide[:, :shape[1]] = t
+    return wide[:, :shape[1]]
+
+
+# ----------------------------------------------------------------------------- norm
+
+NORM_SHAPES = [(1, 8), (3, 136), (16, 2048), (5, 2056), (130, 1024), (7, 4096), (33, 7168), (2, 8200), (3, 16384),
+               (2, 65536), (1100, 512), (5000, 40)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("residual", [False, True], ids=["plain", "residual"])
+@pytest.mark.parametrize("T,H", NORM_SHAPES)
+def test_norm(T, H, residual, dtype):
+    pad = 8 if T % 2 else 0
+    x = rnd("x", (T, H), dtype, 2.0, pad=pad)
+    w = rnd("w", (H,), dtype, 0.2, 1.0)
+    res = rnd("res", (T, H), dtype, pad=2 * pad) if residual else None
+    y, h, rstd = m.rms_norm(x, w, EPS, residual=res)
+    (ry, by), rh, (rr, br), _ = ref.norm(x, w, EPS, res, dtype)
+    assert torch.equal(h.double(), rh) and (residual or h is x)
+    ref.check(rstd, rr, br, "rstd")
+    ref.check(y, ry, by, "y")
+
+
+@pytest.mark.parametrize("T,H", [(1, 128), (17, 2048), (9, 2176), (64, 7168), (3, 40960)])
+@pytest.mark.parametrize("residual", [False, True], ids=["plain", "residual"])
+def test_norm_fp8(T, H, residual):
+    x = rnd("x", (T, H), BF16, 2.0)
+    x[0, :min(H, 128)] = 0                    # a group of zeros: scale 1
+    w = rnd("w", (H,), BF16, 0.2, 1.0)
+    res = rnd("res", (T, H), BF16) if residual else None
+    if residual:
+        res[0, :min(H, 128)] = 0
+    q, s, y, h, rstd = m.rms_norm_fp8(x, w, EPS, residual=res, with_y=True)
+    (ry, by), rh, (rr, br), (fy, fe) = ref.norm(x, w, EPS, res, BF16)
+    assert torch.equal(h.double(), rh)
+    ref.check(rstd, rr, br, "rstd")
+    ref.check(y, ry, by, "y")
+    groups, eg = fy.view(T, -1, 128), fe.view(T, -1, 128)
+    amax = groups.abs().amax(2)
+    want = torch.where(amax > 0, amax / 448, torch.ones_like(amax))
+    ref.check(s, want, eg.amax(2) / 448 + 2 * ref.U32 * want, "scale")
+    # a code is the e4m3 value nearest to y / s: half a step is at most 2^-4 of it, or 2^-10 among the subnormal values
+    val = q.view(torch.float8_e4m3fn).double().view(T, -1, 128)
+    sd = s.double()[:, :, None]
+    assert ((val * sd - groups).abs() <= (groups.abs() * 2.0 ** -4).clamp(min=2.0 ** -10 * sd) * (1 + 2.0 ** -20) + eg).all()
+    assert (q.view(T, -1, 128)[0, 0] == 0).all() and s[0, 0] == 1
+    q2, s2, y2, _, _ = m.rms_norm_fp8(x, w, EPS, residual=res)
+    assert y2 is None and torch.equal(q, q2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("with_dh", [False, True], ids=["plain", "dh"])
+@pytest.mark.parametrize("T,H", NORM_SHAPES)
+def test_norm_backward(T, H, with_dh, dtype):
+    pad = 8 if T % 2 else 0
+    h = rnd("h", (T, H), dtype, 2.0, pad=pad)
+    w = rnd("w", (H,), dtype, 0.2, 1.0)
+    dy = rnd("dy", (T, H), dtype, pad=pad)
+    dh = rnd("dh", (T, H), dtype) if with_dh else None
+    rstd = (h.double().square().mean(1) + EPS).rsqrt().float()
+    dx, dw = m.rms_norm_backward(dy, h, w, rstd, dh=dh)
+    (rx, bx), (rw, bw) = ref.norm_backward(dy, h, w, rstd, dh, dtype)
+    ref.check(dx, rx, bx, "dx")
+    ref.check(dw, rw, bw, "dweight")
+
+
+# ----------------------------------------------------------------------------- linear
+
+# (T, K, N): single tokens, few tokens, every tile shape, ragged in each direction, long contractions
+LINEAR_SHAPES = [(1, 8, 1), (1, 2048, 60), (2, 72, 16), (16, 1408, 2048), (17, 520, 257), (31, 7168, 256), (33, 64, 8),
+                 (64, 264, 136), (65, 1032, 100), (127, 128, 384), (129, 2048, 60), (200, 4104, 520), (300, 136, 1000),
+                 (512, 1000, 640), (700, 2048, 2050), (1111, 328, 2304), (2100, 512, 1030), (3000, 200, 24),
+                 (4097, 64, 264)]
+
+
+def linear_case(T, K, N, dtype, odt, bias, residual, pad=0):
+    x = rnd("x", (T, K), dtype, pad=8 * pad)
+    w = rnd("w", (N, K), dtype, K ** -0.5)
+    b = rnd("b", (N,), dtype, 0.5) if bias else None
+    r = rnd("r", (T, N), odt, pad=8 * pad) if residual else None
+    return x, w, b, r
+
+
+@pytest.mark.parametrize("dtype,odt", [(BF16, BF16), (BF16, F32), (F32, F32)], ids=["bf16", "bf16_f32", "f32"])
+@pytest.mark.parametrize("T,K,N", LINEAR_SHAPES)
+def test_linear(T, K, N, dtype, odt):
+    i = (T + N) % 4
+    bias, residual, name = i != 0, i != 1, ref.ACTS[i]
+    x, w, b, r = linear_case(T, K, N, dtype, odt, bias, residual, pad=T % 3)
+    y, pre = m.linear(x, w, b, r, ACT[name], odt, save_pre=i >= 2)
+    (ry, by), (rz, bz) = ref.linear(x, w, b, r, name, dtype, odt)
+    ref.check(y, ry, by, "y")
+    if i >= 2:
+        ref.check(pre, rz, bz, "pre")
+    else:
+        assert pre is None
+
+
+@pytest.mark.parametrize("name", ref.ACTS)
+@pytest.mark.parametrize("T", [3, 200, 1300])
+def test_linear_every_epilogue(T, name):
+    for bias in (False, True):
+        for residual in (False, True):
+            x, w, b, r = linear_case(T, 256, 264, BF16, BF16, bias, residual)
+            y, pre = m.linear(x, w, b, r, ACT[name], save_pre=True)
+            (ry, by), (rz, bz) = ref.linear(x, w, b, r, name, BF16, BF16)
+            ref.check(y, ry, by, f"y bias={bias} residual={residual}")
+            ref.check(pre, rz, bz, f"pre bias={bias} residual={residual}")
+
+
+BACKWARD_SHAPES = [(1, 8, 1), (1, 2048, 60), (2, 72, 16), (16, 1408, 2048), (17, 520, 257), (33, 64, 8), (64, 264, 136),
+                   (65, 1032, 100), (129, 2048, 60), (200, 4104, 520), (300, 136, 1000), (700, 2048, 2050),
+                   (1111, 328, 2304), (2100, 512, 1030), (3000, 200, 24), (4097, 64, 264)]
+
+
+@pytest.mark.parametrize("dtype,odt", [(BF16, BF16), (BF16, F32), (F32, F32)], ids=["bf16", "bf16_f32", "f32"])
+@pytest.mark.parametrize("T,K,N", BACKWARD_SHAPES)
+def test_linear_backward(T, K, N, dtype, odt):
+    i = (T + N) % 4
+    name, bias = ref.ACTS[i], T % 2 == 1
+    x = rnd("x", (T, K), dtype, pad=8 * (T % 3))
+    w = rnd("w", (N, K), dtype, K ** -0.5)
+    pre = rnd("z", (T, N), dtype, 1.5, pad=8 * (T % 2)) if i else None
+    dy = rnd("dy", (T, N), odt, pad=8 * (T % 2))
+    dx, dw, db = m.linear_backward(dy, x, w, pre=pre, act=ACT[name], need_bias=bias)
+    grads = ref.backward(*ref.dz_linear(dy, pre, name), x, w, dtype)
+    for got, (r, b), what in zip((dx, dw, db), grads, ("dx", "dw", "db")):
+        if got is None:
+            assert what == "db" and not bias
+        else:
+            ref.check(got, r, b, what)
+
+
+# ----------------------------------------------------------------------------- gated
+
+GATED_SHAPES = [(1, 8, 8), (1, 2048, 1408), (3, 72, 40), (16, 2048, 360), (40, 1032, 264), (64, 512, 128), (100, 136, 200),
+                (130, 2048, 1408), (513, 264, 520), (1025, 640, 1032), (2100, 328, 136)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H,I", GATED_SHAPES)
+def test_gated(T, H, I, dtype):
+    name, bias, save = ref.ACTS[1 + T % 3], I % 16 == 8, T % 4 != 1
+    x = rnd("x", (T, H), dtype, pad=8 * (T % 2))
+    w = rnd("w", (2 * I, H), dtype, H ** -0.5)
+    b = rnd("b", (2 * I,), dtype, 0.5) if bias else None
+    a, pre = m.gated_linear(x, w, b, ACT[name], save_pre=save)
+    (ra, ba), (rz, bz) = ref.gated(x, w, b, name, dtype)
+    ref.check(a, ra, ba, "a")
+    if save:
+        ref.check(pre, rz, bz, "pre")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H,I", GATED_SHAPES)
+def test_gated_backward(T, H, I, dtype):
+    name, bias = ref.ACTS[1 + T % 3], T % 2 == 1
+    x = rnd("x", (T, H), dtype, pad=8 * (T % 2))
+    w = rnd("w", (2 * I, H), dtype, H ** -0.5)
+    pre = rnd("z", (T, 2 * I), dtype, 1.5, pad=8 * (T % 2))
+    da = rnd("da", (T, I), dtype, pad=8 * (T % 3))
+    dx, dw, db = m.gated_linear_backward(da, x, w, pre, ACT[name], need_bias=bias)
+    grads = ref.backward(*ref.dz_gated(da, pre, name), x, w, dtype)
+    for got, (r, b), what in zip((dx, dw, db), grads, ("dx", "dw", "db")):
+        if got is None:
+            assert what == "db" and not bias
+        else:
+            ref.check(got, r, b, what)
+
+
+# ----------------------------------------------------------------------------- gradients against differences
+
+def directional(f, args, k, direction, step=1e-6):
+    up, down = list(args), list(args)
+    up[k], down[k] = args[k] + step * direction, args[k] - step * direction
+    return ((f(*up) - f(*down)) / (2 * step)).item()
+
+
+@pytest.mark.parametrize("name", ref.ACTS[:3])
+def test_gradients_match_differences(name):
+    """float32 kernels' gradients along random directions against central differences of the
+    64-bit forward: off by the float32 bounds (1e-5 of the norms covers 40-long sums) and the
+    differences' own step^2."""
+    T, K, N = 11, 40, 32
+    x, w, b = rnd("x", (T, K), F32), rnd("w", (N, K), F32, 0.2), rnd("b", (N,), F32)
+    dy = rnd("dy", (T, N), F32)
+    args = [t.double() for t in (x, w, b)]
+
+    def lin(x, w, b):
+        return (dy.double() * ref.act(name, x @ w.t() + b)).sum()
+
+    _, pre = m.linear(x, w, b, act=ACT[name], save_pre=True)
+    grads = m.linear_backward(dy, x, w, pre=pre, act=ACT[name], need_bias=True)
+    for k, g in enumerate(grads):
+        v = rnd(f"v{k}", tuple(g.shape), F32).double()
+        assert abs(directional(lin, args, k, v) - (g.double() * v).sum().item()) <= 1e-5 * (g.norm() * v.norm()).item()
+
+    if name == "none":
+        nw, nx = rnd("nw", (K,), F32, 0.2, 1.0), x
+        ndy, dh = rnd("ndy", (T, K), F32), rnd("dh", (T, K), F32)
+
+        def nrm(x, w):
+            return (ndy.double() * (x * (x.square().mean(1, keepdim=True) + EPS) ** -0.5 * w) + dh.double() * x).sum()
+
+        _, h, rstd = m.rms_norm(nx, nw, EPS)
+        for k, g in enumerate(m.rms_norm_backward(ndy, h, nw, rstd, dh=dh)):
+            v = rnd(f"nv{k}", tuple(g.shape), F32).double()
+            diff = directional(nrm, [nx.double(), nw.double()], k, v)
+            assert abs(diff - (g.double() * v).sum().item()) <= 1e-5 * (g.norm() * v.norm()).item()
+        return
+
+    def gat(x, w, b):
+        g, u = (x @ w.t() + b).chunk(2, 1)
+        return (dy[:, :N // 2].double().contiguous() * ref.act(name, g) * u).sum()
+
+    da = dy[:, :N // 2].contiguous()
+    _, pre = m.gated_linear(x, w, b[:N].contiguous(), ACT[name], save_pre=True)
+    for k, g in enumerate(m.gated_linear_backward(da, x, w, pre, ACT[name], need_bias=True)):
+        v = rnd(f"gv{k}", tuple(g.shape), F32).double()
+        assert abs(directional(gat, args, k, v) - (g.double() * v).sum().item()) <= 1e-5 * (g.norm() * v.norm()).item()
