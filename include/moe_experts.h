@@ -343,7 +343,7 @@ moe_status moe_set_stage_events(void* const* events, int n);
  *
  * They keep the conventions above with one addition: activations have a row pitch.  A
  * pitch is in elements, 0 stands for packed rows, and otherwise it is at least the row's
- * length and at most 2^22.  Weights are packed.  Types are MOE_F32 or MOE_BF16; sums,
+ * length and at most 2^22.  Weights are packed.  No matrix has more than 2^40 elements.  Types are MOE_F32 or MOE_BF16; sums,
  * statistics and activations are computed in float32 and every output is rounded once to
  * its type (bf16: nearest even).  Results do not depend on timing: sums over workgroups
  * are added in a fixed order, without atomics.  Calls launch kernels only (no host wait, no

@@ -13,6 +13,7 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxPitch = int64_t(1) << 22;   // tile offsets fit in 32 bits
 constexpr int kMaxWidth = 65536;                  // H, I, K
 constexpr int kMaxOutputs = 1 << 20;              // N
+constexpr int64_t kMaxElements = int64_t(1) << 40;  // of any activation: tile counts fit in 31 bits
 
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
 bool aligned4(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0; }
@@ -26,7 +27,6 @@ bool pitch_ok(int64_t ld, int64_t cols, bool vec) {
 int64_t pitch(int64_t ld, int64_t cols) { return ld ? ld : cols; }
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 size_t esize(int t) { return t == MOE_F32 ? 4 : 2; }
-// a matrix ends inside a 48-bit address range whatever its pitch: T < 2^31, ld <= 2^22
 
 moe_status check(const moe_norm_problem* p) {
   if (!p) return MOE_ERR_NULL_ARG;
@@ -41,7 +41,9 @@ moe_status check(const moe_linear_problem* p) {
   if (!p) return MOE_ERR_NULL_ARG;
   if (!type_ok(p->dtype) || (p->out_dtype != p->dtype && p->out_dtype != MOE_F32)) return MOE_ERR_UNSUPPORTED;
   if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_RELU) return MOE_ERR_UNSUPPORTED;
-  if (p->T < 0 || p->T > kMaxRows || !width_ok(p->K) || p->N < 1 || p->N > kMaxOutputs) return MOE_ERR_BAD_SHAPE;
+  if (p->T < 0 || p->T > kMaxRows || !width_ok(p->K) || p->N < 1 || p->N > kMaxOutputs ||
+      p->T * p->N > kMaxElements || p->T * p->K > kMaxElements)
+    return MOE_ERR_BAD_SHAPE;
   if (!pitch_ok(p->ldx, p->K, true) || !pitch_ok(p->lddx, p->K, true)) return MOE_ERR_BAD_SHAPE;
   for (int64_t ld : {p->ldy, p->ldr, p->ldp})
     if (!pitch_ok(ld, p->N, false)) return MOE_ERR_BAD_SHAPE;
@@ -52,7 +54,9 @@ moe_status check(const moe_gated_problem* p) {
   if (!p) return MOE_ERR_NULL_ARG;
   if (!type_ok(p->dtype)) return MOE_ERR_UNSUPPORTED;
   if (p->act < MOE_ACT_SILU || p->act > MOE_ACT_RELU) return MOE_ERR_UNSUPPORTED;
-  if (p->T < 0 || p->T > kMaxRows || !width_ok(p->H) || !width_ok(p->I)) return MOE_ERR_BAD_SHAPE;
+  if (p->T < 0 || p->T > kMaxRows || !width_ok(p->H) || !width_ok(p->I) || p->T * p->H > kMaxElements ||
+      2 * p->T * p->I > kMaxElements)
+    return MOE_ERR_BAD_SHAPE;
   if (!pitch_ok(p->ldx, p->H, true) || !pitch_ok(p->lddx, p->H, true) || !pitch_ok(p->lda, p->I, true) ||
       !pitch_ok(p->ldp, 2 * (int64_t)p->I, true))
     return MOE_ERR_BAD_SHAPE;

@@ -1,0 +1,602 @@
+// Matrix products of the dense operators in bf16 on MFMA (gfx950).
+//
+// out[m][n] = epilogue(sum_k r[m][k] c[n][k]) (DenseGemm), float32 sums.  Three forms occur:
+// forward (both operands stored along k), dx (c stored along n) and dw (both stored along
+// their rows).  One pair of operand readers serves all of them:
+//
+//   along k    : a tile row is 128 bytes of LDS per slice of 64 k, its eight 16-byte chunks
+//                XOR-permuted by the row, so the 16 rows of a fragment read hit distinct banks;
+//                a fragment is one 16-byte read per lane.
+//   along rows : a k row is 256 bytes of LDS (128 rows of the tile), its eight 32-byte units
+//                XOR-permuted by k; a fragment is two transposing 8-byte reads per lane
+//                (ds_read_tr16_b64: each group of 16 lanes reads four k rows of 16 elements and
+//                every lane gets one column), so neither form needs a transposed copy in HBM.
+//
+// Both arrive by global->LDS DMA; the permutation is applied to the global addresses.  The
+// last slice of a contraction that ends inside it takes its missing chunks from a zero
+// chunk in memory, so both operands are zero there.  Rows past the matrix repeat its last one
+// and are not stored.
+//
+// c sits on the MFMA's row side with its rows permuted (fragment j, row q: column 8 (q / 4) +
+// 4 j + q % 4), so two fragments of a lane are eight consecutive columns of one output row:
+// results leave the registers in 16-byte pieces without a pass through LDS.
+#include <type_traits>
+
+#include "dense_device.h"
+
+namespace moe {
+namespace {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int KS = 64;                    // k per slice
+constexpr int REGION = 128 * KS * 2;      // bytes of 128 operand rows in a slice (16 KB)
+
+__device__ const i32x4 zero_chunk[1] = {{0, 0, 0, 0}};
+
+__device__ __forceinline__ void dma_lds_x4_at(const void* p, uint32_t m0) {   // address per lane
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(m0) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
+__device__ __forceinline__ void barrier() {
+  fence();
+  __builtin_amdgcn_s_barrier();
+  fence();
+}
+
+enum { kLinear = 0, kGated = 1, kPartial = 2 };
+
+// ---------------------------------------------------------------------------- DMA
+// Where instruction `ins` (1 KB) of a 128-row region takes lane `lane`'s 16 bytes from.
+struct Chunk {
+  int row;    // tile row within the region (along k) or first of eight rows (along rows)
+  int k;      // first k of the chunk (along k) or the k row (along rows)
+};
+template <bool KM, bool CSIDE>
+__device__ __forceinline__ Chunk chunk_of(int ins, int lane) {
+  Chunk c;
+  if constexpr (!KM) {
+    c.row = ins * 8 + (lane >> 3);
+    const int swz = CSIDE ? (((c.row >> 1) & 1) | (((c.row >> 3) & 3) << 1)) : ((c.row >> 1) & 7);
+    c.k = ((lane & 7) ^ swz) * 8;
+  } else {
+    c.k = ins * 4 + (lane >> 4);
+    const int f = CSIDE ? 2 * (c.k & 3) : ((c.k & 3) | (((c.k >> 3) & 1) << 2));
+    const int pos = lane & 15;
+    c.row = (((pos >> 1) ^ f) * 2 + (pos & 1)) * 8;
+  }
+  return c;
+}
+
+// ---------------------------------------------------------------------------- fragments
+// 16 rows x 32 k (k step s) of a region from row r0 (a multiple of 16)
+template <bool KM>
+struct RowFrag {
+  uint32_t off[2];
+  int f;
+  __device__ __forceinline__ RowFrag(int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    if constexpr (!KM) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) off[s] = (uint32_t)(i * 128 + (((4 * s + g) ^ (i >> 1)) << 4));
+    } else {
+      off[0] = (uint32_t)((8 * g + (i >> 2)) * 256 + (i & 3) * 8);
+      f = (i >> 2) | ((g & 1) << 2);
+    }
+  }
+  __device__ __forceinline__ bf16x8 load(const char* region, int r0, int s) const {
+    if constexpr (!KM) {
+      return *reinterpret_cast<const bf16x8*>(region + r0 * 128 + off[s]);
+    } else {
+      const char* p = region + off[0] + (((r0 >> 4) ^ f) << 5) + s * 32 * 256;
+      return tr_pair(p, p + 4 * 256);
+    }
+  }
+  static __device__ __forceinline__ bf16x8 tr_pair(const char* p, const char* q) {
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)lds_addr(p));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)lds_addr(q));
+    const s16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, v);
+  }
+};
+// fragment j of the 32 columns from c0 (a multiple of 32): row q is column c0 + 8 (q / 4) + 4 j + q % 4
+template <bool KM>
+struct ColFrag {
+  uint32_t off[2];
+  int f, half;
+  __device__ __forceinline__ ColFrag(int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    if constexpr (!KM) {
+      const int swz = ((i >> 1) & 1) | ((i >> 2) << 1);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        off[s] = (uint32_t)((8 * (i >> 2) + (i & 3)) * 128 + (((4 * s + g) ^ swz) << 4));
+    } else {
+      off[0] = (uint32_t)((8 * g + (i >> 2)) * 256 + (i & 1) * 16);
+      f = 2 * ((i >> 2) & 3);
+      half = (i & 3) >> 1;
+    }
+  }
+  __device__ __forceinline__ bf16x8 load(const char* region, int c0, int j, int s) const {
+    if constexpr (!KM) {
+      return *reinterpret_cast<const bf16x8*>(region + (c0 + 4 * j) * 128 + off[s]);
+    } else {
+      const char* p = region + off[0] + ((((c0 >> 4) + half) ^ f) << 5) + 8 * j + s * 32 * 256;
+      return RowFrag<true>::tr_pair(p, p + 4 * 256);
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------- operand streams
+struct Job {
+  DenseGemm g;
+  int mt, nt;          // tiles
+  int splits;          // contraction split over blockIdx.y
+  int slices;          // slices of one split
+  int crows;           // rows of c (gated: 2 I)
+  float* part;         // [splits][M][ldpart] partial sums (splits > 1)
+  int64_t ldpart;
+};
+
+// This lane's DMA sources for NI instructions (first, first + 1, ...) of one region whose
+// rows are tile rows base_row .. base_row + 127
+template <bool KM, bool CSIDE, int NI>
+struct Stream {
+  uint32_t off[NI];
+  // row_of(tile row) gives the row's distance from the operand's tile origin, clamped
+  template <typename F>
+  __device__ __forceinline__ void init(int first, int lane, int64_t ld, F&& row_of) {
+#pragma unroll
+    for (int q = 0; q < NI; ++q) {
+      const Chunk c = chunk_of<KM, CSIDE>(first + q, lane);
+      off[q] = KM ? (uint32_t)(c.k * ld * 2 + row_of(c.row) * 2) : (uint32_t)(row_of(c.row) * ld * 2 + c.k * 2);
+    }
+  }
+  // full slice: base = operand tile origin advanced to the slice
+  __device__ __forceinline__ void issue(const char* base, uint32_t lds, int q) const { dma_lds_x4(base, off[q], lds); }
+  // last slice with `left` k in it
+  __device__ __forceinline__ void issue_tail(const char* base, uint32_t lds, int q, int first, int lane, int left) const {
+    const Chunk c = chunk_of<KM, CSIDE>(first + q, lane);
+    const char* p = c.k < left ? base + off[q] : reinterpret_cast<const char*>(zero_chunk);
+    dma_lds_x4_at(p, lds);
+  }
+};
+
+// Tile (mt, nt) of workgroup b.  Consecutive workgroups go to the eight XCDs in turn; each XCD
+// takes a contiguous run of tiles, ordered in groups of 8 tile rows with the row fastest, so
+// the 32 tiles that run together on an XCD are 8 x 4 and share their operands in its L2.
+__device__ __forceinline__ bool tile_of(const Job& job, int b, int& mt, int& nt) {
+  const int total = job.mt * job.nt;
+  const int per = (total + 7) >> 3;
+  const int t = (b & 7) * per + (b >> 3);
+  if ((b >> 3) >= per || t >= total) return false;
+  const int grp = t / (8 * job.nt);
+  const int rows = min(8, job.mt - grp * 8);
+  const int l = t - grp * 8 * job.nt;
+  mt = grp * 8 + l % rows;
+  nt = l / rows;
+  return true;
+}
+
+template <int EPI>
+__device__ __forceinline__ void store8(const Job& job, int split, int64_t m, int n, const f32x4 z0, const f32x4 z1,
+                                       const f32x4 u0, const f32x4 u1) {
+  if (m >= job.g.M) return;
+  float z[8], u[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = z0[i], z[4 + i] = z1[i], u[i] = u0[i], u[4 + i] = u1[i];
+  if constexpr (EPI == kPartial) {
+    if (n < job.crows) Piece<float>::store(job.part, ((int64_t)split * job.g.M + m) * job.ldpart + n, z);
+  } else {
+    epi_store<uint16_t, EPI == kGated>(job.g.e, m, n, z, u);
+  }
+}
+
+// ---------------------------------------------------------------------------- 256 x 256 tiles
+// Eight waves (two per SIMD) in a 2 x 4 grid, each 128 x 64 of the tile as four quadrants (64
+// rows of row half 0 or 1 x 32 columns of column half 0 or 1).  A slice is four phases, one
+// quadrant each: fragment reads and DMA issue, barrier, 16 MFMAs, barrier.  The two waves of a
+// SIMD are half a phase apart (one extra barrier before the loop for the second row of waves),
+// so one reads LDS while the other multiplies.  Two slices live in LDS; a region is refilled
+// with slice kt + 2 as soon as both waves' rows have read it, which keeps 10 to 14 DMAs per wave in
+// flight and gives each about five phases to land.  Phase by phase (slice kt):
+//   0: read R0            multiply R0 x C0   issue R1(kt+1)   wait for C1(kt)
+//   1: read C1            multiply R0 x C1   issue R0(kt+2)   wait for R1(kt)
+//   2: read R1            multiply R1 x C0   issue C0(kt+2)   wait for R0, C0(kt+1)
+//   3: read C0(kt+1)      multiply R1 x C1   issue C1(kt+2)
+// DMAs retire in issue order (R0 C0 C1 | R1 of the next slice in turn), two per region and
+// wave, which gives the vmcnt of each wait.
+template <bool RK, bool CK, int EPI>
+__global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
+  __shared__ __attribute__((aligned(1024))) char lds[2][4][REGION];   // [slice parity][R0 R1 C0 C1]
+  int mt, nt;
+  if (!tile_of(job, blockIdx.x, mt, nt)) return;
+  const DenseGemm& g = job.g;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int64_t m0 = (int64_t)mt * 256;
+  const int n0 = nt * (EPI == kGated ? 128 : 256);
+  const int split = blockIdx.y;
+  const int64_t k0 = (int64_t)split * job.slices * KS;
+  const int KT = (int)min((int64_t)job.slices, (g.K - k0 + KS - 1) / KS);
+  const int left = (int)min((int64_t)KS, g.K - k0 - (int64_t)(KT - 1) * KS);   // k in the last slice
+
+  // operand tile origins and the bytes from one slice to the next
+  const char* rbase = static_cast<const char*>(g.r) + (RK ? k0 * g.ldr + m0 : m0 * g.ldr + k0) * 2;
+  const char* cbase = static_cast<const char*>(g.c) + (CK ? k0 * g.ldc + n0 : (int64_t)n0 * g.ldc + k0) * 2;
+  const int64_t rstep = RK ? (int64_t)KS * g.ldr * 2 : KS * 2, cstep = CK ? (int64_t)KS * g.ldc * 2 : KS * 2;
+  Stream<RK, false, 2> sr[2];
+  Stream<CK, true, 2> sc[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    sr[h].init(wave * 2, lane, g.ldr, [&](int row) -> int64_t {
+      // (along rows: whole chunks of eight)
+      const int64_t last = RK ? (g.M - 1 - m0) / 8 * 8 : g.M - 1 - m0;
+      return min((int64_t)(h * 128 + row), last);
+    });
+    sc[h].init(wave * 2, lane, g.ldc, [&](int row) -> int64_t {
+      if constexpr (EPI == kGated) return (int64_t)h * g.e.N + min(row, g.e.N - 1 - n0);
+      const int last = CK ? (job.crows - 1 - n0) / 8 * 8 : job.crows - 1 - n0;
+      return min(h * 128 + row, last);
+    });
+  }
+  const uint32_t lds0 = lds_addr(&lds[0][0][0]);
+  auto issue_r = [&](int h, int kt) __attribute__((always_inline)) {
+    const char* base = rbase + kt * rstep;
+    const uint32_t dst = lds0 + (uint32_t)(((kt & 1) * 4 + h) * REGION + wave * 2048);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (kt == KT - 1 && left < KS) sr[h].issue_tail(base, dst + q * 1024, q, wave * 2, lane, left);
+      else sr[h].issue(base, dst + q * 1024, q);
+    }
+  };
+  auto issue_c = [&](int h, int kt) __attribute__((always_inline)) {
+    const char* base = cbase + kt * cstep;
+    const uint32_t dst = lds0 + (uint32_t)(((kt & 1) * 4 + 2 + h) * REGION + wave * 2048);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (kt == KT - 1 && left < KS) sc[h].issue_tail(base, dst + q * 1024, q, wave * 2, lane, left);
+      else sc[h].issue(base, dst + q * 1024, q);
+    }
+  };
+
+  const RowFrag<RK> fr(lane);
+  const ColFrag<CK> fc(lane);
+  f32x4 acc[2][2][4][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[a][b][i][j] = f32x4{};
+  bf16x8 r[4][2], c0[2][2], c1[2][2];
+  auto read_r = [&](int h, int kt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) r[i][s] = fr.load(&lds[kt & 1][h][0], wm * 64 + i * 16, s);
+  };
+  auto read_c = [&](bf16x8 (&c)[2][2], int h, int kt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) c[j][s] = fc.load(&lds[kt & 1][2 + h][0], wn * 32, j, s);
+  };
+  auto multiply = [&](f32x4 (&a)[4][2], const bf16x8 (&c)[2][2]) __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) a[i][j] = mfma_16x16x32_bf16(c[j][s], r[i][s], a[i][j]);
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+  };
+  // end of a phase's reads: this wave's fragments are in registers, its part of the awaited
+  // regions has landed, and the barrier makes both hold for the workgroup
+  auto ready = [&]() __attribute__((always_inline)) {
+    wait_lds();
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+  };
+
+  issue_r(0, 0), issue_c(0, 0), issue_c(1, 0), issue_r(1, 0);
+  if (KT > 1) {
+    issue_r(0, 1), issue_c(0, 1), issue_c(1, 1);
+    wait_vmcnt<10>();
+  } else {
+    wait_vmcnt<4>();
+  }
+  barrier();
+  read_c(c0, 0, 0);
+  if (wm == 1) barrier();
+  for (int kt = 0; kt < KT; ++kt) {
+    const bool more = kt + 2 < KT;
+    read_r(0, kt);
+    if (kt + 1 < KT) {
+      issue_r(1, kt + 1);
+      wait_vmcnt<10>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    ready();
+    multiply(acc[0][0], c0);
+
+    read_c(c1, 1, kt);
+    if (more) {
+      issue_r(0, kt + 2);
+      wait_vmcnt<10>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    ready();
+    multiply(acc[0][1], c1);
+
+    read_r(1, kt);
+    if (more) {
+      issue_c(0, kt + 2);
+      wait_vmcnt<8>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    ready();
+    multiply(acc[1][0], c0);
+
+    if (kt + 1 < KT) read_c(c0, 0, kt + 1);
+    if (more) issue_c(1, kt + 2);
+    ready();
+    multiply(acc[1][1], c1);
+  }
+  if (wm == 0) barrier();
+
+  const int row = lane & 15, col = 8 * (lane >> 4);
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t m = m0 + a * 128 + wm * 64 + i * 16 + row;
+      if constexpr (EPI == kGated) {
+        store8<EPI>(job, split, m, n0 + wn * 32 + col, acc[a][0][i][0], acc[a][0][i][1], acc[a][1][i][0],
+                    acc[a][1][i][1]);
+      } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          store8<EPI>(job, split, m, n0 + b * 128 + wn * 32 + col, acc[a][b][i][0], acc[a][b][i][1], f32x4{}, f32x4{});
+      }
+    }
+}
+
+// ---------------------------------------------------------------------------- RR x 128 tiles
+// Four waves (2 x 2), two slices in LDS, one barrier per slice; two (RR = 128) or three (RR =
+// 64) workgroups share a CU, so one's waits are covered by the others' MFMAs.  A wave's
+// columns are 32 of each half of the tile (gated: 32 gate and the matching 32 up columns).
+template <int RR, bool RK, bool CK, int EPI>
+__global__ __launch_bounds__(256, 2) void dense_128_kernel(Job job) {
+  constexpr int FM = RR / 32;                              // 16-row fragments per wave
+  constexpr int RBYTES = RR * KS * 2, STAGE = RBYTES + REGION;
+  constexpr int NR = RBYTES / 4096, NC = REGION / 4096;    // DMA instructions per wave and slice
+  static_assert(RR == 128 || !RK, "rows stored along k come in regions of 128");
+  __shared__ __attribute__((aligned(1024))) char lds[2][STAGE];
+  int mt, nt;
+  if (!tile_of(job, blockIdx.x, mt, nt)) return;
+  const DenseGemm& g = job.g;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t m0 = (int64_t)mt * RR;
+  const int n0 = nt * (EPI == kGated ? 64 : 128);
+  const int split = blockIdx.y;
+  const int64_t k0 = (int64_t)split * job.slices * KS;
+  const int KT = (int)min((int64_t)job.slices, (g.K - k0 + KS - 1) / KS);
+  const int left = (int)min((int64_t)KS, g.K - k0 - (int64_t)(KT - 1) * KS);
+  const char* rbase = static_cast<const char*>(g.r) + (RK ? k0 * g.ldr + m0 : m0 * g.ldr + k0) * 2;
+  const char* cbase = static_cast<const char*>(g.c) + (CK ? k0 * g.ldc + n0 : (int64_t)n0 * g.ldc + k0) * 2;
+  const int64_t rstep = RK ? (int64_t)KS * g.ldr * 2 : KS * 2, cstep = CK ? (int64_t)KS * g.ldc * 2 : KS * 2;
+  Stream<RK, false, NR> sr;
+  Stream<CK, true, NC> sc;
+  sr.init(wave * NR, lane, g.ldr, [&](int row) -> int64_t {
+    const int64_t last = RK ? (g.M - 1 - m0) / 8 * 8 : g.M - 1 - m0;
+    return min((int64_t)row, last);
+  });
+  sc.init(wave * NC, lane, g.ldc, [&](int row) -> int64_t {
+    if constexpr (EPI == kGated) return (int64_t)(row >> 6) * g.e.N + min(row & 63, g.e.N - 1 - n0);
+    const int last = CK ? (job.crows - 1 - n0) / 8 * 8 : job.crows - 1 - n0;
+    return min(row, last);
+  });
+  const uint32_t lds0 = lds_addr(&lds[0][0]);
+  auto issue = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + (uint32_t)((kt & 1) * STAGE);
+    const char* rb = rbase + kt * rstep;
+    const char* cb = cbase + kt * cstep;
+    if (kt == KT - 1 && left < KS) {
+#pragma unroll
+      for (int q = 0; q < NR; ++q) sr.issue_tail(rb, dst + (wave * NR + q) * 1024, q, wave * NR, lane, left);
+#pragma unroll
+      for (int q = 0; q < NC; ++q) sc.issue_tail(cb, dst + RBYTES + (wave * NC + q) * 1024, q, wave * NC, lane, left);
+    } else {
+#pragma unroll
+      for (int q = 0; q < NR; ++q) sr.issue(rb, dst + (wave * NR + q) * 1024, q);
+#pragma unroll
+      for (int q = 0; q < NC; ++q) sc.issue(cb, dst + RBYTES + (wave * NC + q) * 1024, q);
+    }
+  };
+  const RowFrag<RK> fr(lane);
+  const ColFrag<CK> fc(lane);
+  f32x4 acc[2][FM][2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[b][i][j] = f32x4{};
+
+  issue(0);
+  for (int kt = 0; kt < KT; ++kt) {
+    wait_vmcnt<0>();     // slice kt has landed
+    wait_lds();          // (and the reads of slice kt - 1 are done: its buffer is refilled next)
+    barrier();
+    if (kt + 1 < KT) issue(kt + 1);
+    const char* R = &lds[kt & 1][0];
+    const char* C = R + RBYTES;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8 r[FM], c[2][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) c[b][j] = fc.load(C, b * 64 + wn * 32, j, s);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) r[i] = fr.load(R, wm * (RR / 2) + i * 16, s);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[b][i][j] = mfma_16x16x32_bf16(c[b][j], r[i], acc[b][i][j]);
+    }
+  }
+  const int row = lane & 15, col = 8 * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + wm * (RR / 2) + i * 16 + row;
+    if constexpr (EPI == kGated) {
+      store8<EPI>(job, split, m, n0 + wn * 32 + col, acc[0][i][0], acc[0][i][1], acc[1][i][0], acc[1][i][1]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        store8<EPI>(job, split, m, n0 + b * 64 + wn * 32 + col, acc[b][i][0], acc[b][i][1], f32x4{}, f32x4{});
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- sum of the splits
+// Adds the splits' partial sums in their order and applies the epilogue; one thread per eight columns.
+template <bool GATED>
+__global__ __launch_bounds__(256) void dense_join_kernel(Job job) {
+  const int n8 = (job.g.e.N + 7) / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= job.g.M * n8) return;
+  const int64_t m = i / n8;
+  const int n = (int)(i - m * n8) * 8;
+  float z[8] = {}, u[8] = {};
+  for (int s = 0; s < job.splits; ++s) {
+    float v[8];
+    const int64_t at = ((int64_t)s * job.g.M + m) * job.ldpart + n;
+    Piece<float>::load(job.part, at, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] += v[j];
+    if constexpr (GATED) {
+      Piece<float>::load(job.part, at + job.g.e.N, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += v[j];
+    }
+  }
+  epi_store<uint16_t, GATED>(job.g.e, m, n, z, u);
+}
+
+// ---------------------------------------------------------------------------- plan
+struct Plan {
+  int tile;      // 256, 128 or 64 (rows of a tile)
+  int splits;
+  int slices;    // per split
+};
+
+// The tile and split with the least estimated time.  A tile costs its slices plus a fixed part
+// (first DMA, epilogue); tiles run in rounds of the workgroups that fit the 256 CUs; a split
+// adds a pass over its partial sums.
+Plan plan(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor) {
+  const int64_t cols = gated ? 2 * N : N;
+  const int64_t KT = (K + KS - 1) / KS;
+  Plan best{128, 1, (int)KT};
+  double best_us = 1e30;
+  for (int tile : {256, 128, 64}) {
+    if (tile == 64 && r_kmajor) continue;
+    const int tn = tile == 256 ? 256 : 128;
+    const int64_t tiles = ((M + tile - 1) / tile) * ((cols + tn - 1) / tn);
+    const int slots = tile == 256 ? 256 : (tile == 128 ? 512 : 768);
+    const double slice_us = tile == 256 ? 1.1 : (tile == 128 ? 0.8 : 0.75), fixed_us = tile == 256 ? 5.0 : 3.0;
+    const double alone_us = tile == 256 ? 1.1 : (tile == 128 ? 0.5 : 0.35);   // a CU with one workgroup
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && KT / s < 4) break;
+      const int64_t per = (KT + s - 1) / s;
+      if ((KT + per - 1) / per != s) continue;        // (every split has slices)
+      const int64_t wgs = tiles * s;
+      const int64_t rounds = (wgs + slots - 1) / slots;
+      const double us = rounds * (per * (wgs <= 256 ? alone_us : slice_us) + fixed_us) +
+                        (s > 1 ? 3.0 + (double)M * cols * 4 * 2 * s / 3e6 : 0.0);
+      if (us < best_us) best_us = us, best = Plan{tile, s, (int)per};
+    }
+  }
+  return best;
+}
+int64_t part_pitch(int64_t N, int gated) { return ((gated ? 2 * N : N) + 7) / 8 * 8; }
+
+template <int EPI>
+hipError_t launch_tiles(const Job& job, int tile, hipStream_t s) {
+  const int total = job.mt * job.nt;
+  const dim3 grid((unsigned)((total + 7) / 8 * 8), (unsigned)job.splits);
+  const bool rk = job.g.r_kmajor, ck = job.g.c_kmajor;
+  if (tile == 256) {
+    if (!rk && !ck) hipLaunchKernelGGL((dense_256_kernel<false, false, EPI>), grid, dim3(512), 0, s, job);
+    if constexpr (EPI != kGated) {
+      if (!rk && ck) hipLaunchKernelGGL((dense_256_kernel<false, true, EPI>), grid, dim3(512), 0, s, job);
+      if (rk && ck) hipLaunchKernelGGL((dense_256_kernel<true, true, EPI>), grid, dim3(512), 0, s, job);
+    }
+  } else if (tile == 128) {
+    if (!rk && !ck) hipLaunchKernelGGL((dense_128_kernel<128, false, false, EPI>), grid, dim3(256), 0, s, job);
+    if constexpr (EPI != kGated) {
+      if (!rk && ck) hipLaunchKernelGGL((dense_128_kernel<128, false, true, EPI>), grid, dim3(256), 0, s, job);
+      if (rk && ck) hipLaunchKernelGGL((dense_128_kernel<128, true, true, EPI>), grid, dim3(256), 0, s, job);
+    }
+  } else {
+    if (!ck) hipLaunchKernelGGL((dense_128_kernel<64, false, false, EPI>), grid, dim3(256), 0, s, job);
+    if constexpr (EPI != kGated) {
+      if (ck) hipLaunchKernelGGL((dense_128_kernel<64, false, true, EPI>), grid, dim3(256), 0, s, job);
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32) {
+  (void)c_kmajor;
+  if (f32 || M == 0 || K == 0) return 0;
+  const Plan p = plan(M, N, K, gated, r_kmajor);
+  return p.splits > 1 ? (size_t)p.splits * M * part_pitch(N, gated) * 4 : 0;
+}
+
+hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s) {
+  if (f32) return launch_dense_gemm_f32(g, s);
+  const Plan p = plan(g.M, g.e.N, g.K, g.gated, g.r_kmajor);
+  Job job{};
+  job.g = g;
+  job.splits = p.splits;
+  job.slices = p.slices;
+  job.crows = g.gated ? 2 * g.e.N : g.e.N;
+  job.mt = (int)((g.M + p.tile - 1) / p.tile);
+  const bool fused_gate = g.gated && p.splits == 1;
+  const int tn = (p.tile == 256 ? 256 : 128) / (fused_gate ? 2 : 1);
+  job.nt = ((fused_gate ? g.e.N : job.crows) + tn - 1) / tn;
+  if (p.splits == 1) return g.gated ? launch_tiles<kGated>(job, p.tile, s) : launch_tiles<kLinear>(job, p.tile, s);
+  job.part = static_cast<float*>(ws);
+  job.ldpart = part_pitch(g.e.N, g.gated);
+  hipError_t err = launch_tiles<kPartial>(job, p.tile, s);
+  if (err != hipSuccess) return err;
+  const int64_t pieces = g.M * ((g.e.N + 7) / 8);
+  const dim3 grid((unsigned)((pieces + 255) / 256));
+  if (g.gated) hipLaunchKernelGGL(dense_join_kernel<true>, grid, dim3(256), 0, s, job);
+  else hipLaunchKernelGGL(dense_join_kernel<false>, grid, dim3(256), 0, s, job);
+  return hipGetLastError();
+}
+
+}  // namespace moe

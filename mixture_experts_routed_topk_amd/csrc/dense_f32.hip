@@ -105,9 +105,4 @@ hipError_t launch(const DenseGemm& g, hipStream_t s) {
 
 hipError_t launch_dense_gemm_f32(const DenseGemm& g, hipStream_t s) { return launch<float>(g, s); }
 
-size_t dense_gemm_workspace(int64_t, int64_t, int64_t, int, int, int, bool) { return 0; }
-hipError_t launch_dense_gemm(const DenseGemm& g, void*, bool f32, hipStream_t s) {
-  return f32 ? launch<float>(g, s) : launch<uint16_t>(g, s);
-}
-
 }  // namespace moe
