@@ -14,7 +14,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kDzRows = 64;      // rows of one workgroup: partial rows cost 1/64 of dz at most twice over
+constexpr int kDzRows = 16;      // rows of one workgroup: four per wave, all in flight at once
 
 // Eight columns starting at n of a row whose columns end at N (zeros past it)
 template <typename T>
@@ -27,65 +27,91 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int n, int N, b
   }
 }
 
-// Workgroup (x, y): columns 8 * (256 y + tid) .. + 7 of rows 64 x .. 64 x + 63
-template <typename T, bool GATED>
+// Workgroup (x, y): columns 512 y .. 512 y + 511 (eight a lane) of rows 16 x .. 16 x + 15; wave w takes rows
+// w, w + 4, w + 8, w + 12.  The four waves' column sums meet in LDS.
+template <typename T, typename D, bool GATED>
 __global__ __launch_bounds__(kThreads) void dz_kernel(DzArgs a, int vec) {
   constexpr bool FAST = sizeof(T) == 2;
-  const int n = (blockIdx.y * kThreads + threadIdx.x) * 8;
+  constexpr int ROWS = kDzRows / 4;
+  __shared__ float red[GATED ? 2 : 1][4][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = blockIdx.y * 512 + lane * 8;
   const int width = GATED ? a.N : (int)a.ldz;        // columns written (with the pitch's zeros)
-  if (n >= width) return;
-  const int64_t r0 = (int64_t)blockIdx.x * kDzRows, r1 = min(a.T, r0 + kDzRows);
   float s0[8] = {}, s1[8] = {};
-  for (int64_t t = r0; t < r1; ++t) {
-    float d[8], z[8], u[8];
-    if (a.dy_f32) load8<float>(a.dy, t * a.ldy, n, a.N, vec, d);
-    else load8<T>(a.dy, t * a.ldy, n, a.N, vec, d);
-    if (a.pre) load8<T>(a.pre, t * a.ldp, n, a.N, vec, z);
-    if constexpr (GATED) {
-      load8<T>(a.pre, t * a.ldp + a.N, n, a.N, vec, u);
+  if (n < width) {
+    float d[ROWS][8], z[ROWS][8], u[ROWS][8];
+    const int64_t t0 = (int64_t)blockIdx.x * kDzRows + wave;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float da = d[i];
-        d[i] = da * u[i] * act_slope<FAST>(a.act, z[i]);
-        u[i] = da * act_fn<FAST>(a.act, z[i]);
-        s1[i] += u[i];
-      }
-    } else if (a.pre) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = n + i < a.N ? d[i] * act_slope<FAST>(a.act, z[i]) : 0.f;
+    for (int r = 0; r < ROWS; ++r) {
+      const int64_t t = min(t0 + 4 * r, a.T - 1);    // (rows past the end repeat the last and are dropped below)
+      load8<D>(a.dy, t * a.ldy, n, a.N, vec, d[r]);
+      if (a.pre) load8<T>(a.pre, t * a.ldp, n, a.N, vec, z[r]);
+      if (GATED) load8<T>(a.pre, t * a.ldp + a.N, n, a.N, vec, u[r]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s0[i] += d[i];
-    if (a.dz) {
-      Piece<T>::store(a.dz, t * a.ldz + n, d);
-      if constexpr (GATED) Piece<T>::store(a.dz, t * a.ldz + a.N + n, u);
+    for (int r = 0; r < ROWS; ++r) {
+      const int64_t t = t0 + 4 * r;
+      if (t >= a.T) continue;
+      if constexpr (GATED) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const ActPair p = act_pair<FAST>(a.act, z[r][i]);
+          const float da = d[r][i];
+          d[r][i] = da * u[r][i] * p.slope;
+          u[r][i] = da * p.value;
+          s1[i] += u[r][i];
+        }
+      } else if (a.pre) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[r][i] = n + i < a.N ? d[r][i] * act_pair<FAST>(a.act, z[r][i]).slope : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s0[i] += d[r][i];
+      if (a.dz) {
+        Piece<T>::store(a.dz, t * a.ldz + n, d[r]);
+        if constexpr (GATED) Piece<T>::store(a.dz, t * a.ldz + a.N + n, u[r]);
+      }
     }
   }
-  if (a.part) {
-    const int64_t cols = GATED ? 2 * (int64_t)a.N : a.N;
-    float* out = a.part + blockIdx.x * cols;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (n + i < a.N) {
-        out[n + i] = s0[i];
-        if (GATED) out[a.N + n + i] = s1[i];
-      }
+  if (!a.part) return;
+  Piece<float>::store(red[0][wave], lane * 8, s0);
+  if constexpr (GATED) Piece<float>::store(red[1][wave], lane * 8, s1);
+  __syncthreads();
+  const int64_t cols = GATED ? 2 * (int64_t)a.N : a.N;
+  float* out = a.part + blockIdx.x * cols;
+  for (int c = threadIdx.x; c < 512; c += kThreads) {
+    const int col = blockIdx.y * 512 + c;
+    if (col >= a.N) break;
+    out[col] = ((red[0][0][c] + red[0][1][c]) + red[0][2][c]) + red[0][3][c];
+    if constexpr (GATED) out[a.N + col] = ((red[1][0][c] + red[1][1][c]) + red[1][2][c]) + red[1][3][c];
   }
 }
 
-// 64 columns a workgroup; wave w adds rows w, w + 4, ... and the four sums are added in order
-__global__ __launch_bounds__(kThreads) void column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t cols,
-                                                              void* __restrict__ out, int f32) {
-  __shared__ float red[4][kWave];
+// 64 columns a workgroup; wave w adds rows w, w + 16, ... and the sixteen sums are added in order
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(kSumWaves * kWave) void column_sum_kernel(const float* __restrict__ part, int64_t rows,
+                                                                       int64_t cols, void* __restrict__ out, int f32) {
+  __shared__ float red[kSumWaves][kWave];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * kWave + lane;
   float s = 0.f;
-  if (c < cols)
-    for (int64_t r = wave; r < rows; r += 4) s += part[r * cols + c];
+  if (c < cols) {
+    int64_t r = wave;
+    for (; r + 7 * kSumWaves < rows; r += 8 * kSumWaves) {   // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = part[(r + i * kSumWaves) * cols + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; r < rows; r += kSumWaves) s += part[r * cols + c];
+  }
   red[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < cols) {
-    s = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSumWaves; ++w) s += red[w][lane];
     if (f32) Piece<float>::put(out, c, s);
     else Piece<uint16_t>::put(out, c, s);
   }
@@ -95,12 +121,12 @@ __global__ __launch_bounds__(kThreads) void zero_bytes_kernel(uint8_t* p, int64_
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) p[i] = 0;
 }
 
-template <typename T>
+template <typename T, typename D>
 hipError_t launch(const DzArgs& a, int vec, hipStream_t s) {
   const int64_t width = a.gated ? a.N : a.ldz;
-  const dim3 grid((unsigned)dz_parts(a.T), (unsigned)((width + 8 * kThreads - 1) / (8 * kThreads)));
-  if (a.gated) hipLaunchKernelGGL((dz_kernel<T, true>), grid, dim3(kThreads), 0, s, a, vec);
-  else hipLaunchKernelGGL((dz_kernel<T, false>), grid, dim3(kThreads), 0, s, a, vec);
+  const dim3 grid((unsigned)dz_parts(a.T), (unsigned)((width + 511) / 512));
+  if (a.gated) hipLaunchKernelGGL((dz_kernel<T, T, true>), grid, dim3(kThreads), 0, s, a, vec);
+  else hipLaunchKernelGGL((dz_kernel<T, D, false>), grid, dim3(kThreads), 0, s, a, vec);
   return hipGetLastError();
 }
 
@@ -114,14 +140,16 @@ hipError_t launch_dz(const DzArgs& a, bool f32, hipStream_t s) {
   };
   const int esz = f32 ? 4 : 2;
   const int vec = ok(a.dy, a.ldy, a.dy_f32 ? 4 : esz) && (!a.pre || ok(a.pre, a.ldp, esz));
-  hipError_t err = f32 ? launch<float>(a, vec, s) : launch<uint16_t>(a, vec, s);
+  hipError_t err = f32         ? launch<float, float>(a, vec, s)
+                   : a.dy_f32 ? launch<uint16_t, float>(a, vec, s)
+                              : launch<uint16_t, uint16_t>(a, vec, s);
   if (err != hipSuccess || !a.dbias) return err;
   return launch_column_sum(a.part, dz_parts(a.T), a.gated ? 2 * (int64_t)a.N : a.N, a.dbias, f32, s);
 }
 
 hipError_t launch_column_sum(const float* part, int64_t rows, int64_t cols, void* out, bool f32, hipStream_t s) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((cols + kWave - 1) / kWave)), dim3(kThreads), 0, s, part, rows,
-                     cols, out, f32 ? 1 : 0);
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((cols + kWave - 1) / kWave)), dim3(kSumWaves * kWave), 0, s, part,
+                     rows, cols, out, f32 ? 1 : 0);
   return hipGetLastError();
 }
 

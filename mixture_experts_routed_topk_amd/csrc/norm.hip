@@ -181,7 +181,7 @@ int rows_of_block(int H) { return H / 8 <= 256 ? rows_per_block<1>() : 1; }
 
 int64_t backward_blocks(int64_t T, int H) {
   const int64_t need = (T + rows_of_block(H) - 1) / rows_of_block(H);
-  const int64_t most = H / 8 <= 1024 ? 1024 : 256;   // four blocks of four waves, or one of sixteen, per CU
+  const int64_t most = H / 8 <= 1024 ? 512 : 256;   // two blocks of four waves, or one of sixteen, per CU
   return need < most ? need : most;
 }
 
