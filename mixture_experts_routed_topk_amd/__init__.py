@@ -10,6 +10,7 @@ not on the GPU, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -447,89 +448,122 @@ def check_mfma_blocks(a: torch.Tensor, b: torch.Tensor, b_scale: Optional[torch.
 
 
 # ----------------------------------------------------------------------------- dense operators
+# (Decode steps make these calls by the thousand, each a few microseconds of GPU time: the checks
+# below take the common case in one comparison and say what is wrong only after it fails.)
 
-def _rows(name: str, t: torch.Tensor, cols: int, dtype, T: Optional[int] = None) -> int:
-    """Checks a [T, cols] activation matrix on the GPU; returns its row pitch in elements."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _rows(name: str, t: torch.Tensor, T: int, cols: int, dtype: torch.dtype, dev: int) -> int:
+    """Checks a [T, cols] activation matrix on GPU `dev`; returns its row pitch in elements."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-    if t.dim() != 2 or t.shape[1] != cols or (T is not None and t.shape[0] != T):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'T' if T is None else T}, {cols}]")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.shape != (T, cols) or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, (T, cols), dtype, dev)
     ld, inner = t.stride()
-    if t.shape[0] <= 1:
+    if T <= 1:
         ld = cols
     if (inner != 1 and cols > 1) or ld < cols:
         raise ValueError(f"{name} must have unit stride along its rows and rows that do not overlap")
     return ld
 
 
-def _vector(name: str, t: torch.Tensor, shape, dtype) -> None:
-    _need_gpu(name, t)
-    if tuple(t.shape) != shape or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+def _packed(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: int) -> None:
+    """Checks a packed tensor on GPU `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, shape, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _float_type(name: str, t: torch.Tensor) -> int:
+def _refuse(name, t, shape, dtype, dev):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _matrix(name: str, t: torch.Tensor):
+    """(moe_dtype, GPU index) of the 2-D bf16 or float32 GPU tensor that a call's types follow."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _ACT:
         raise ValueError(f"{name} must be a bf16 or float32 tensor")
-    return _ACT[t.dtype]
+    dev = t.get_device() if t.device.type == "cuda" else -1
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {list(t.shape)}")
+    return _ACT[t.dtype], dev
 
 
-def _one_device(**tensors) -> None:
-    devices = {t.device for t in tensors.values() if t is not None}
-    if len(devices) > 1:
-        raise ValueError(f"tensors are on different devices: {sorted(str(d) for d in devices)}")
-
-
-def _run(fn, device: torch.device, *args) -> None:
-    """Calls fn(*args, current stream of `device`) with `device` current."""
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+def _outputs(name: str, w: torch.Tensor) -> int:
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError(f"{name} must be a tensor of two dimensions")
+    return w.shape[0]
 
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(workspace: Optional[torch.Tensor], size_fn, *args, device):
-    """(tensor or None, bytes): the caller's workspace, or one of the size the library asks for."""
+def _run(fn, dev: int, *args) -> None:
+    """Calls fn(*args, current stream of GPU `dev`) with that GPU current."""
+    if _current_device() == dev:
+        status = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev))
+    if status:
+        _check(status)
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, x: torch.Tensor, dev: int):
+    """(tensor or None, bytes): the caller's workspace, or one of `need` bytes next to x."""
     if workspace is not None:
         _need_gpu("workspace", workspace)
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.device}, the call's other tensors on cuda:{dev}")
         return workspace, workspace.numel() * workspace.element_size()
-    n = ctypes.c_size_t(0)
-    _check(size_fn(*args, ctypes.byref(n)))
-    if n.value == 0:
+    if need == 0:
         return None, 0
-    return torch.empty(n.value, dtype=torch.uint8, device=device), n.value
+    return x.new_empty(need, dtype=torch.uint8), need
+
+
+@functools.lru_cache(maxsize=4096)
+def _problem(kind, fields: tuple, size_fn: Optional[str] = None, *args):
+    """(reference to the C problem, its workspace bytes): both follow from the fields alone, so
+    they are made once per problem.  The library only reads the struct."""
+    ref = ctypes.byref(kind(*fields))
+    n = ctypes.c_size_t(0)
+    if size_fn is not None:
+        _check(getattr(lib(), size_fn)(ref, *args, ctypes.byref(n)))
+    return ref, n.value
 
 
 def _rms_norm(x, weight, eps, residual, fp8, with_y):
-    dt = _float_type("x", x)
-    if x.dim() != 2:
-        raise ValueError("x must be [T, H]")
+    dt, dev = _matrix("x", x)
     T, H = x.shape
-    prob = NormProblem(T, H, dt, eps, _rows("x", x, H, x.dtype), 0, 0, 0)
-    _vector("weight", weight, (H,), x.dtype)
-    h = x
-    if residual is not None:
-        prob.ldr = _rows("residual", residual, H, x.dtype, T)
-        h = torch.empty((T, H), dtype=x.dtype, device=x.device)
-    _one_device(x=x, weight=weight, residual=residual)
-    y = torch.empty((T, H), dtype=x.dtype, device=x.device) if with_y else None
-    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    dtype = x.dtype
+    ldr = 0
+    _packed("weight", weight, (H,), dtype, dev)
+    if residual is None:
+        h = x
+    else:
+        ldr = _rows("residual", residual, T, H, dtype, dev)
+        h = torch.empty_like(x)
+    prob, _ = _problem(NormProblem, (T, H, dt, eps, _rows("x", x, T, H, dtype, dev), ldr, 0, 0))
+    y = torch.empty_like(x) if with_y else None
+    rstd = x.new_empty(T, dtype=torch.float32)
     q = scale = None
     if fp8:
-        if x.dtype != torch.bfloat16 or H % 128:
+        if dtype is not torch.bfloat16 or H % 128:
             raise ValueError("the 8-bit output takes bf16 rows with H a multiple of 128")
-        q = torch.empty((T, H), dtype=torch.uint8, device=x.device)
-        scale = torch.empty((T, H // 128), dtype=torch.float32, device=x.device)
-    _run(lib().moe_rms_norm, x.device, ctypes.byref(prob), x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(y),
+        q = x.new_empty((T, H), dtype=torch.uint8)
+        scale = x.new_empty((T, H // 128), dtype=torch.float32)
+    _run(lib().moe_rms_norm, dev, prob, x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(y),
          None if residual is None else h.data_ptr(), rstd.data_ptr(), _addr(q), _addr(scale))
     return q, scale, y, h, rstd
 
@@ -553,22 +587,19 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, r
                       dh: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """(dx, dweight) of rms_norm, from dy and dh, the gradient that reaches h along the residual
     stream; dx is the gradient of x and of the residual.  See moe_rms_norm_backward."""
-    dt = _float_type("h", h)
-    if h.dim() != 2:
-        raise ValueError("h must be [T, H]")
+    dt, dev = _matrix("h", h)
     T, H = h.shape
-    prob = NormProblem(T, H, dt, 0.0, 0, 0, _rows("h", h, H, h.dtype), _rows("dy", dy, H, h.dtype, T))
-    _vector("weight", weight, (H,), h.dtype)
-    _vector("rstd", rstd, (T,), torch.float32)
-    if dh is not None:
-        prob.ldr = _rows("dh", dh, H, h.dtype, T)
-    _one_device(dy=dy, h=h, weight=weight, rstd=rstd, dh=dh, workspace=workspace)
-    dx = torch.empty((T, H), dtype=h.dtype, device=h.device)
-    dweight = torch.empty(H, dtype=h.dtype, device=h.device)
-    L = lib()
-    ws, n = _scratch(workspace, L.moe_rms_norm_workspace_size, ctypes.byref(prob), device=h.device)
-    _run(L.moe_rms_norm_backward, h.device, ctypes.byref(prob), dy.data_ptr(), h.data_ptr(), weight.data_ptr(),
-         rstd.data_ptr(), _addr(dh), dx.data_ptr(), dweight.data_ptr(), _addr(ws), n)
+    dtype = h.dtype
+    ldr = 0 if dh is None else _rows("dh", dh, T, H, dtype, dev)
+    fields = (T, H, dt, 0.0, 0, ldr, _rows("h", h, T, H, dtype, dev), _rows("dy", dy, T, H, dtype, dev))
+    _packed("weight", weight, (H,), dtype, dev)
+    _packed("rstd", rstd, (T,), torch.float32, dev)
+    prob, need = _problem(NormProblem, fields, "moe_rms_norm_workspace_size")
+    ws, n = _scratch(workspace, need, h, dev)
+    dx = torch.empty_like(h)
+    dweight = torch.empty_like(weight)
+    _run(lib().moe_rms_norm_backward, dev, prob, dy.data_ptr(), h.data_ptr(),
+         weight.data_ptr(), rstd.data_ptr(), _addr(dh), dx.data_ptr(), dweight.data_ptr(), _addr(ws), n)
     return dx, dweight
 
 
@@ -578,27 +609,24 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     """(y, pre): y = act(x w^T + bias) + residual in out_dtype (x's, or float32), and pre = x w^T +
     bias when save_pre (else None).  x [T,K], w [N,K], bias [N], residual [T,N] in
     out_dtype; see moe_linear."""
-    dt = _float_type("x", x)
-    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
-        raise ValueError("x must be [T, K] and w [N, K]")
+    dt, dev = _matrix("x", x)
     T, K = x.shape
-    N = w.shape[0]
-    odt = x.dtype if out_dtype is None else out_dtype
+    N = _outputs("w", w)
+    dtype = x.dtype
+    odt = dtype if out_dtype is None else out_dtype
     if odt not in _ACT:
         raise ValueError("out_dtype must be bf16 or float32")
-    prob = LinearProblem(T, K, N, dt, _ACT[odt], act, _rows("x", x, K, x.dtype), 0, 0, 0, 0)
-    _vector("w", w, (N, K), x.dtype)
+    _packed("w", w, (N, K), dtype, dev)
     if bias is not None:
-        _vector("bias", bias, (N,), x.dtype)
-    if residual is not None:
-        prob.ldr = _rows("residual", residual, N, odt, T)
-    _one_device(x=x, w=w, bias=bias, residual=residual, workspace=workspace)
-    y = torch.empty((T, N), dtype=odt, device=x.device)
-    pre = torch.empty((T, N), dtype=x.dtype, device=x.device) if save_pre else None
-    L = lib()
-    ws, n = _scratch(workspace, L.moe_linear_workspace_size, ctypes.byref(prob), 0, device=x.device)
-    _run(L.moe_linear, x.device, ctypes.byref(prob), x.data_ptr(), w.data_ptr(), _addr(bias), _addr(residual),
-         y.data_ptr(), _addr(pre), _addr(ws), n)
+        _packed("bias", bias, (N,), dtype, dev)
+    ldr = 0 if residual is None else _rows("residual", residual, T, N, odt, dev)
+    fields = (T, K, N, dt, _ACT[odt], act, _rows("x", x, T, K, dtype, dev), 0, ldr, 0, 0)
+    prob, need = _problem(LinearProblem, fields, "moe_linear_workspace_size", 0)
+    ws, n = _scratch(workspace, need, x, dev)
+    y = x.new_empty((T, N), dtype=odt)
+    pre = x.new_empty((T, N)) if save_pre else None
+    _run(lib().moe_linear, dev, prob, x.data_ptr(), w.data_ptr(), _addr(bias),
+         _addr(residual), y.data_ptr(), _addr(pre), _addr(ws), n)
     return y, pre
 
 
@@ -606,55 +634,56 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre: Opt
                     act: int = ACT_NONE, need_bias: bool = False, workspace: Optional[torch.Tensor] = None):
     """(dx, dw, dbias) of linear, dbias None without need_bias; pre is what linear saved (needed
     with an activation).  See moe_linear_backward."""
-    dt = _float_type("x", x)
-    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
-        raise ValueError("x must be [T, K] and w [N, K]")
+    dt, dev = _matrix("x", x)
     T, K = x.shape
-    N = w.shape[0]
-    ody = _float_type("dy", dy)
-    prob = LinearProblem(T, K, N, dt, ody, act, _rows("x", x, K, x.dtype), _rows("dy", dy, N, dy.dtype, T), 0, 0, 0)
-    _vector("w", w, (N, K), x.dtype)
-    if act != ACT_NONE:
-        if pre is None:
-            raise ValueError("an activation's gradient needs pre")
-        prob.ldp = _rows("pre", pre, N, x.dtype, T)
-    else:
+    N = _outputs("w", w)
+    dtype = x.dtype
+    ody, _ = _matrix("dy", dy)
+    _packed("w", w, (N, K), dtype, dev)
+    ldp = 0
+    if act == ACT_NONE:
         pre = None
-    _one_device(dy=dy, x=x, w=w, pre=pre, workspace=workspace)
-    L = lib()
-    return _backward(L.moe_linear_backward, L.moe_linear_workspace_size, prob, dy, x, w, pre, N, need_bias, workspace)
+    elif pre is None:
+        raise ValueError("an activation's gradient needs pre")
+    else:
+        ldp = _rows("pre", pre, T, N, dtype, dev)
+    fields = (T, K, N, dt, ody, act, _rows("x", x, T, K, dtype, dev), _rows("dy", dy, T, N, dy.dtype, dev), 0, ldp, 0)
+    return _backward("moe_linear_backward", LinearProblem, fields, dy, x, w, pre, N, need_bias, workspace, dev)
 
 
-def _backward(fn, size_fn, prob, dy, x, w, pre, cols, need_bias, workspace):
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+def _backward(fn_name, kind, fields, dy, x, w, pre, cols, need_bias, workspace, dev):
+    prob, need = _problem(kind, fields, fn_name.replace("_backward", "_workspace_size"), 1)
+    ws, n = _scratch(workspace, need, x, dev)
+    dx = torch.empty_like(x)
     dw = torch.empty_like(w)
-    dbias = torch.empty(cols, dtype=x.dtype, device=x.device) if need_bias else None
-    ws, n = _scratch(workspace, size_fn, ctypes.byref(prob), 1, device=x.device)
-    _run(fn, x.device, ctypes.byref(prob), dy.data_ptr(), x.data_ptr(), w.data_ptr(), _addr(pre), dx.data_ptr(),
-         dw.data_ptr(), _addr(dbias), _addr(ws), n)
+    dbias = x.new_empty(cols) if need_bias else None
+    _run(getattr(lib(), fn_name), dev, prob, dy.data_ptr(), x.data_ptr(), w.data_ptr(),
+         _addr(pre), dx.data_ptr(), dw.data_ptr(), _addr(dbias), _addr(ws), n)
     return dx, dw, dbias
+
+
+def _gated_sizes(x, w_gate_up):
+    dt, dev = _matrix("x", x)
+    T, H = x.shape
+    I = _outputs("w_gate_up", w_gate_up) // 2
+    _packed("w_gate_up", w_gate_up, (2 * I, H), x.dtype, dev)
+    return dt, dev, T, H, I
 
 
 def gated_linear(x: torch.Tensor, w_gate_up: torch.Tensor, bias: Optional[torch.Tensor] = None, act: int = ACT_SILU,
                  save_pre: bool = False, workspace: Optional[torch.Tensor] = None):
     """(a, pre): [gate | up] = x w_gate_up^T + bias, a = act(gate) * up [T,I], and pre = [gate |
     up] [T,2I] when save_pre (else None).  x [T,H], w_gate_up [2I,H], bias [2I]; see moe_gated_linear."""
-    dt = _float_type("x", x)
-    if x.dim() != 2 or not isinstance(w_gate_up, torch.Tensor) or w_gate_up.dim() != 2 or w_gate_up.shape[0] % 2:
-        raise ValueError("x must be [T, H] and w_gate_up [2I, H]")
-    T, H = x.shape
-    I = w_gate_up.shape[0] // 2
-    prob = GatedProblem(T, H, I, dt, act, _rows("x", x, H, x.dtype), 0, 0, 0)
-    _vector("w_gate_up", w_gate_up, (2 * I, H), x.dtype)
+    dt, dev, T, H, I = _gated_sizes(x, w_gate_up)
     if bias is not None:
-        _vector("bias", bias, (2 * I,), x.dtype)
-    _one_device(x=x, w_gate_up=w_gate_up, bias=bias, workspace=workspace)
-    a = torch.empty((T, I), dtype=x.dtype, device=x.device)
-    pre = torch.empty((T, 2 * I), dtype=x.dtype, device=x.device) if save_pre else None
-    L = lib()
-    ws, n = _scratch(workspace, L.moe_gated_linear_workspace_size, ctypes.byref(prob), 0, device=x.device)
-    _run(L.moe_gated_linear, x.device, ctypes.byref(prob), x.data_ptr(), w_gate_up.data_ptr(), _addr(bias),
-         a.data_ptr(), _addr(pre), _addr(ws), n)
+        _packed("bias", bias, (2 * I,), x.dtype, dev)
+    fields = (T, H, I, dt, act, _rows("x", x, T, H, x.dtype, dev), 0, 0, 0)
+    prob, need = _problem(GatedProblem, fields, "moe_gated_linear_workspace_size", 0)
+    ws, n = _scratch(workspace, need, x, dev)
+    a = x.new_empty((T, I))
+    pre = x.new_empty((T, 2 * I)) if save_pre else None
+    _run(lib().moe_gated_linear, dev, prob, x.data_ptr(), w_gate_up.data_ptr(),
+         _addr(bias), a.data_ptr(), _addr(pre), _addr(ws), n)
     return a, pre
 
 
@@ -662,15 +691,8 @@ def gated_linear_backward(da: torch.Tensor, x: torch.Tensor, w_gate_up: torch.Te
                           act: int = ACT_SILU, need_bias: bool = False, workspace: Optional[torch.Tensor] = None):
     """(dx, dw, dbias) of gated_linear from da and the pre it saved; dbias None without need_bias.
     See moe_gated_linear_backward."""
-    dt = _float_type("x", x)
-    if x.dim() != 2 or not isinstance(w_gate_up, torch.Tensor) or w_gate_up.dim() != 2 or w_gate_up.shape[0] % 2:
-        raise ValueError("x must be [T, H] and w_gate_up [2I, H]")
-    T, H = x.shape
-    I = w_gate_up.shape[0] // 2
-    prob = GatedProblem(T, H, I, dt, act, _rows("x", x, H, x.dtype), _rows("da", da, I, x.dtype, T),
-                        _rows("pre", pre, 2 * I, x.dtype, T), 0)
-    _vector("w_gate_up", w_gate_up, (2 * I, H), x.dtype)
-    _one_device(da=da, x=x, w_gate_up=w_gate_up, pre=pre, workspace=workspace)
-    L = lib()
-    return _backward(L.moe_gated_linear_backward, L.moe_gated_linear_workspace_size, prob, da, x, w_gate_up, pre, 2 * I,
-                     need_bias, workspace)
+    dt, dev, T, H, I = _gated_sizes(x, w_gate_up)
+    fields = (T, H, I, dt, act, _rows("x", x, T, H, x.dtype, dev), _rows("da", da, T, I, x.dtype, dev),
+              _rows("pre", pre, T, 2 * I, x.dtype, dev), 0)
+    return _backward("moe_gated_linear_backward", GatedProblem, fields, da, x, w_gate_up, pre, 2 * I, need_bias,
+                     workspace, dev)

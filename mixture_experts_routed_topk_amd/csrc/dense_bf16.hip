@@ -538,6 +538,10 @@ Plan plan(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor) {
   }
   return best;
 }
+// Products of few rows with both operands stored along k (the forward ones) have kernels of their own.
+bool few_rows(int64_t M, int64_t K, int r_kmajor, int c_kmajor) {
+  return !r_kmajor && !c_kmajor && dense_rows_take(M, K);
+}
 int64_t part_pitch(int64_t N, int gated) { return ((gated ? 2 * N : N) + 7) / 8 * 8; }
 
 template <int EPI>
@@ -569,14 +573,14 @@ hipError_t launch_tiles(const Job& job, int tile, hipStream_t s) {
 }  // namespace
 
 size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32) {
-  (void)c_kmajor;
-  if (f32 || M == 0 || K == 0) return 0;
+  if (f32 || M == 0 || K == 0 || few_rows(M, K, r_kmajor, c_kmajor)) return 0;
   const Plan p = plan(M, N, K, gated, r_kmajor);
   return p.splits > 1 ? (size_t)p.splits * M * part_pitch(N, gated) * 4 : 0;
 }
 
 hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s) {
   if (f32) return launch_dense_gemm_f32(g, s);
+  if (few_rows(g.M, g.K, g.r_kmajor, g.c_kmajor)) return launch_dense_rows(g, s);
   const Plan p = plan(g.M, g.e.N, g.K, g.gated, g.r_kmajor);
   Job job{};
   job.g = g;

@@ -88,6 +88,20 @@ __device__ __forceinline__ float act_fn(int act, float z) {
 static_assert(kActGelu - kActSilu + kGateSilu == kGateGelu && kActRelu - kActSilu + kGateSilu == kGateRelu,
               "activations keep the gates' order");
 
+template <bool FAST>
+__device__ __forceinline__ void act8(int act, float z[8]) {
+  if (act == kActSilu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_fn<FAST>(kActSilu, z[i]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_fn<FAST>(kActGelu, z[i]);
+  } else if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = act_fn<FAST>(kActRelu, z[i]);
+  }
+}
+
 // act(z) and act'(z) together (they share the exponential)
 struct ActPair {
   float value, slope;
@@ -152,8 +166,11 @@ __device__ __forceinline__ void epi_store(const DenseEpi& e, int64_t m, int n, f
         }
     }
   }
+  act8<FAST>(e.act, z);
+  if (GATED) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = act_fn<FAST>(e.act, z[i]) * (GATED ? u[i] : 1.0f);
+    for (int i = 0; i < 8; ++i) z[i] *= u[i];
+  }
   const int64_t at = m * e.ldo + n, rat = m * e.ldr + n;
   if (e.vec) {
     if (e.res) {
@@ -175,6 +192,24 @@ __device__ __forceinline__ void epi_store(const DenseEpi& e, int64_t m, int n, f
         else Piece<T>::put(e.out, at + i, v);
       }
   }
+}
+
+// One element (m, n) of the output.
+template <typename T, bool GATED>
+__device__ __forceinline__ void epi_store1(const DenseEpi& e, int64_t m, int n, float z, float u) {
+  if (e.bias) {
+    z += Piece<T>::get(e.bias, n);
+    if (GATED) u += Piece<T>::get(e.bias, e.N + n);
+  }
+  if (e.pre) {
+    Piece<T>::put(e.pre, m * e.ldp + n, z);
+    if (GATED) Piece<T>::put(e.pre, m * e.ldp + e.N + n, u);
+  }
+  z = act_fn<sizeof(T) == 2>(e.act, z);
+  if (GATED) z *= u;
+  if (e.res) z += e.out_f32 ? Piece<float>::get(e.res, m * e.ldr + n) : Piece<T>::get(e.res, m * e.ldr + n);
+  if (e.out_f32) Piece<float>::put(e.out, m * e.ldo + n, z);
+  else Piece<T>::put(e.out, m * e.ldo + n, z);
 }
 
 }  // namespace moe

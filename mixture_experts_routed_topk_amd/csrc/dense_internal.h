@@ -76,6 +76,10 @@ hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t
 // float32 products (any pitch, any alignment)
 hipError_t launch_dense_gemm_f32(const DenseGemm& g, hipStream_t s);
 
+// bf16 products of few rows with both operands stored along k
+bool dense_rows_take(int64_t M, int64_t K);
+hipError_t launch_dense_rows(const DenseGemm& g, hipStream_t s);
+
 // ---------------------------------------------------------------------------- backward
 // dz = dy * act'(pre) (gated: [da * up * act'(gate), da * act(gate)]) in the operands' type,
 // [T][ldz] with zeros in columns [cols, ldz), and its column sums.

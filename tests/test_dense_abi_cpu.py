@@ -179,5 +179,5 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         m.rms_norm(x.half(), w[0])
     with pytest.raises(ValueError, match="bf16 or float32"):
         m.linear(x.half(), w)
-    with pytest.raises(ValueError, match=r"\[T, K\]"):
-        m.linear(x[0], w)
+    with pytest.raises(ValueError, match="torch tensor|bf16"):
+        m.linear([[1.0]], w)

@@ -297,3 +297,40 @@ def test_calls_on_several_streams_at_once():
                 for t, r in zip(out, ref_out):
                     ok = same(t, r)
                 assert ok
+
+
+# ----------------------------------------------------------------------------- refusals of the binding
+
+def test_binding_refuses():
+    x, w, b = rnd("rx", (4, 64), BF16), rnd("rw", (32, 64), BF16), rnd("rb", (32,), BF16)
+    nw, z, dy = rnd("rn", (64,), BF16), rnd("rz", (4, 32), BF16), rnd("rdy", (4, 32), BF16)
+    bad = [lambda: m.linear(x[0], w), lambda: m.linear(x, w[0]), lambda: m.linear(x, w[:, :56].contiguous()),
+           lambda: m.linear(x, w.float()), lambda: m.linear(x, w, bias=b[:31]), lambda: m.linear(x, w, bias=b.float()),
+           lambda: m.linear(x, w, residual=dy.float()), lambda: m.linear(x, w, residual=dy[:3]),
+           lambda: m.linear(x, w, out_dtype=torch.float16), lambda: m.linear(x, w, act=4),
+           lambda: m.linear(x.t().contiguous().t(), w), lambda: m.linear(x, w.t().contiguous().t()),
+           lambda: m.linear(x[:1].expand(4, 64), w), lambda: m.linear(x[:, :60], w[:, :60].contiguous()),
+           lambda: m.linear(torch.empty((4, 65), dtype=BF16, device="cuda")[:, :64], w),        # rows not 16-byte aligned
+           lambda: m.linear(torch.empty((4, 72), dtype=BF16, device="cuda")[:, 4:68], w),       # nor the first
+           lambda: m.linear(x.cpu(), w), lambda: m.linear(x, w.cpu()), lambda: m.linear(x, w, residual=dy.cpu()),
+           lambda: m.linear(x, w, workspace=torch.empty(16, dtype=torch.uint8)),
+           lambda: m.linear_backward(dy, x, w, act=m.ACT_GELU), lambda: m.linear_backward(dy[:, :31], x, w),
+           lambda: m.linear_backward(dy, x, w, pre=z[:3], act=m.ACT_GELU),
+           lambda: m.linear_backward(dy, x, w, pre=z, act=m.ACT_GELU,
+                                     workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+           lambda: m.gated_linear(x, w[:31].contiguous()), lambda: m.gated_linear(x, w, act=m.ACT_NONE),
+           lambda: m.gated_linear(x, w[:24].contiguous()), lambda: m.gated_linear(x, w, bias=b[:16]),
+           lambda: m.gated_linear_backward(dy, x, w, z), lambda: m.gated_linear_backward(dy[:, :16], x, w, z[:, :16]),
+           lambda: m.rms_norm(x, nw[:63]), lambda: m.rms_norm(x, nw.float()), lambda: m.rms_norm(x, nw, residual=x[:3]),
+           lambda: m.rms_norm(x, nw, -1.0), lambda: m.rms_norm(x, nw, float("nan")), lambda: m.rms_norm_fp8(x, nw),
+           lambda: m.rms_norm_fp8(x.float(), nw.float()),
+           lambda: m.rms_norm_backward(x, x, nw, torch.ones(3, device="cuda")),
+           lambda: m.rms_norm_backward(x, x, nw, torch.ones(4, device="cuda").double()),
+           lambda: m.rms_norm_backward(x, x, nw, torch.ones(4, device="cuda"),
+                                       workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))]
+    for i, f in enumerate(bad):
+        try:
+            f()
+        except ValueError:
+            continue
+        raise AssertionError(f"call {i} was taken")
