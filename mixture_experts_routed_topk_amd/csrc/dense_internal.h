@@ -56,7 +56,8 @@ struct DenseEpi {
 };
 
 // out[M][N] from r (M rows) and c (N rows, gated 2N): element (m, k) of r is r[m * ldr + k],
-// or r[k * ldr + m] with r_kmajor; c likewise.
+// or r[k * ldr + m] with r_kmajor; c likewise.  Rows start on 16 bytes, and their last 16-byte
+// piece may be read whole: past K it holds zeros, past the rows of a k-major operand anything.
 struct DenseGemm {
   const void* r;
   int64_t ldr;
@@ -73,7 +74,7 @@ struct DenseGemm {
 size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32);
 hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s);
 
-// float32 products (any pitch, any alignment)
+// float32 products
 hipError_t launch_dense_gemm_f32(const DenseGemm& g, hipStream_t s);
 
 // bf16 products of few rows with both operands stored along k
