@@ -13,12 +13,18 @@ struct Piece;   // eight consecutive elements of a row as float32
 
 template <>
 struct Piece<float> {
-  static __device__ __forceinline__ void load(const void* p, int64_t at, float v[8]) {
+  struct Raw {
+    f32x4 a, b;
+  };
+  static __device__ __forceinline__ Raw raw(const void* p, int64_t at) {
     const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
-    const f32x4 a = q[0], b = q[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+    return {q[0], q[1]};
   }
+  static __device__ __forceinline__ void widen(const Raw& r, float v[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = r.a[i], v[4 + i] = r.b[i];
+  }
+  static __device__ __forceinline__ void load(const void* p, int64_t at, float v[8]) { widen(raw(p, at), v); }
   static __device__ __forceinline__ void store(void* p, int64_t at, const float v[8]) {
     f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + at);
     q[0] = f32x4{v[0], v[1], v[2], v[3]};
@@ -31,11 +37,15 @@ struct Piece<float> {
 
 template <>
 struct Piece<uint16_t> {   // bf16 bits
-  static __device__ __forceinline__ void load(const void* p, int64_t at, float v[8]) {
-    const i32x4 a = *reinterpret_cast<const i32x4*>(static_cast<const uint16_t*>(p) + at);
+  typedef i32x4 Raw;
+  static __device__ __forceinline__ Raw raw(const void* p, int64_t at) {
+    return *reinterpret_cast<const i32x4*>(static_cast<const uint16_t*>(p) + at);
+  }
+  static __device__ __forceinline__ void widen(const Raw& a, float v[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo((uint32_t)a[i]), v[2 * i + 1] = bf16_hi((uint32_t)a[i]);
   }
+  static __device__ __forceinline__ void load(const void* p, int64_t at, float v[8]) { widen(raw(p, at), v); }
   static __device__ __forceinline__ void store(void* p, int64_t at, const float v[8]) {
     i32x4 a;
 #pragma unroll

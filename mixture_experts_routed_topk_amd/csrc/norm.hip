@@ -51,18 +51,29 @@ __global__ __launch_bounds__(block_threads<WPR>()) void rms_norm_kernel(NormArgs
   const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
   if (row >= a.T) return;                        // (whole rows: the lanes of a row agree; WPR > 1 has one row)
   const int np = a.H / 8;
+  using Raw = typename Piece<T>::Raw;
+  Raw x[NV], r[NV], w[NV];
+  // every load of the row before the first use (lanes past the row repeat its first piece)
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int p = i * LPR + lane < np ? i * LPR + lane : 0;
+    x[i] = Piece<T>::raw(a.x, row * a.ldx + p * 8);
+    if (a.res) r[i] = Piece<T>::raw(a.res, row * a.ldr + p * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) w[i] = Piece<T>::raw(a.weight, (i * LPR + lane < np ? i * LPR + lane : 0) * 8);
   float v[NV][8];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int p = i * LPR + lane;
     if (p < np) {
-      Piece<T>::load(a.x, row * a.ldx + p * 8, v[i]);
+      Piece<T>::widen(x[i], v[i]);
       if (a.res) {
-        float r[8];
-        Piece<T>::load(a.res, row * a.ldr + p * 8, r);
+        float d[8];
+        Piece<T>::widen(r[i], d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = Piece<T>::round(v[i][j] + r[j]);
+        for (int j = 0; j < 8; ++j) v[i][j] = Piece<T>::round(v[i][j] + d[j]);
         Piece<T>::store(a.h, row * a.ldh + p * 8, v[i]);
       }
 #pragma unroll
@@ -76,10 +87,10 @@ __global__ __launch_bounds__(block_threads<WPR>()) void rms_norm_kernel(NormArgs
   for (int i = 0; i < NV; ++i) {
     const int p = i * LPR + lane;
     if (p < np) {
-      float w[8];
-      Piece<T>::load(a.weight, p * 8, w);
+      float wf[8];
+      Piece<T>::widen(w[i], wf);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
+      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * wf[j];
       if (!QUANT || a.y) Piece<T>::store(a.y, row * a.ldy + p * 8, v[i]);
       if constexpr (QUANT) {   // 16 lanes hold a group of 128 columns (H % 128 == 0: whole groups)
         float amax = 0.f;
@@ -88,12 +99,26 @@ __global__ __launch_bounds__(block_threads<WPR>()) void rms_norm_kernel(NormArgs
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 16));
         const float s = amax > 0.f ? amax / 448.0f : 1.0f;
-        uint32_t lo = 0, hi = 0;
+        // v / s from one reciprocal: the quotient's error is taken back once, which rounds as the
+        // division does (eight IEEE divisions and the e4m3 rounding in integer steps take as long as
+        // the row's memory traffic)
+        float d[8];
+        if (s > 0x1p-96f && s < 0x1p96f) {
+          const float inv = 1.0f / s;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          lo |= f32_to_e4m3(v[i][j] / s) << (8 * j);
-          hi |= f32_to_e4m3(v[i][4 + j] / s) << (8 * j);
+          for (int j = 0; j < 8; ++j) {
+            const float quo = v[i][j] * inv;
+            d[j] = fmaf(fmaf(-quo, s, v[i][j]), inv, quo);
+          }
+        } else {   // (1 / s or the correction may leave float32's range)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = v[i][j] / s;
         }
+        uint32_t lo = 0, hi = 0;
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], lo, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], lo, true);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[4], d[5], hi, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[6], d[7], hi, true);
         *reinterpret_cast<uint2*>(a.q + row * a.H + p * 8) = make_uint2(lo, hi);
         if ((lane & 15) == 0) a.q_scale[row * (a.H / 128) + p / 16] = s;
       }
@@ -112,25 +137,51 @@ __global__ __launch_bounds__(block_threads<WPR>()) void rms_norm_backward_kernel
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  using Raw = typename Piece<T>::Raw;
+  struct Row {
+    Raw dy[NV], h[NV], dh[NV];
+    float rstd;
+  } next;
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {   // (lanes past the row repeat its first piece)
+    next.rstd = a.rstd_in[row];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = i * LPR + lane < np ? i * LPR + lane : 0;
+      next.dy[i] = Piece<T>::raw(a.dy, row * a.ldy + p * 8);
+      next.h[i] = Piece<T>::raw(a.hin, row * a.ldh + p * 8);
+      if (a.res) next.dh[i] = Piece<T>::raw(a.res, row * a.ldr + p * 8);
+    }
+  };
+  // sixteen waves leave a lane 128 registers: no room for a second row, nor for g and n beside dy and h
+  constexpr bool kAhead = WPR < 16;
   int slot = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < a.T; row += (int64_t)gridDim.x * RPB) {
-    const float rstd = a.rstd_in[row];
-    float g[NV][8], n[NV][8];
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + sub;
+  if (row < a.T) fetch(row);
+  for (; row < a.T; row += step) {
+    const Row cur = next;
+    if (kAhead && row + step < a.T) fetch(row + step);   // the next row's loads cover this row's reduction
+    // g = dy w and n = h rstd of piece i; kept over the reduction, or formed again after it
+    float gk[NV][8], nk[NV][8];
+    auto form = [&](int i, int p, float (&dy)[8], float (&g)[8], float (&n)[8]) __attribute__((always_inline)) {
+      float w[8];
+      Piece<T>::widen(cur.dy[i], dy);
+      Piece<T>::widen(cur.h[i], n);
+      Piece<T>::load(a.weight, p * 8, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) n[j] *= cur.rstd, g[j] = dy[j] * w[j];
+    };
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int p = i * LPR + lane;
       if (p < np) {
-        float w[8];
-        Piece<T>::load(a.dy, row * a.ldy + p * 8, g[i]);
-        Piece<T>::load(a.hin, row * a.ldh + p * 8, n[i]);
-        Piece<T>::load(a.weight, p * 8, w);
+        float dy[8];
+        form(i, p, dy, gk[i], nk[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          n[i][j] *= rstd;
-          dw[i][j] += g[i][j] * n[i][j];
-          g[i][j] *= w[j];
-          dot += g[i][j] * n[i][j];
+          dw[i][j] += dy[j] * nk[i][j];
+          dot += gk[i][j] * nk[i][j];
         }
       }
     }
@@ -141,17 +192,19 @@ __global__ __launch_bounds__(block_threads<WPR>()) void rms_norm_backward_kernel
       const int p = i * LPR + lane;
       if (p < np) {
         float d[8];
+        if (!kAhead) form(i, p, d, gk[i], nk[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = rstd * (g[i][j] - n[i][j] * dot);
+        for (int j = 0; j < 8; ++j) d[j] = cur.rstd * (gk[i][j] - nk[i][j] * dot);
         if (a.res) {
           float r[8];
-          Piece<T>::load(a.res, row * a.ldr + p * 8, r);
+          Piece<T>::widen(cur.dh[i], r);
 #pragma unroll
           for (int j = 0; j < 8; ++j) d[j] += r[j];
         }
         Piece<T>::store(a.dx, row * a.ldx + p * 8, d);
       }
     }
+    if (!kAhead && row + step < a.T) fetch(row + step);
   }
   if (a.part) {   // one partial row per row slot of the grid
     float* out = a.part + ((int64_t)blockIdx.x * RPB + sub) * a.H;

@@ -75,6 +75,21 @@ def test_norm_fp8(T, H, residual):
     assert y2 is None and torch.equal(q, q2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("exponent", [-122, -110, 0, 110])
+def test_norm_fp8_far_scales(exponent):
+    """Weights that put the scales below, inside and above the range of a float32 reciprocal: the
+    codes are those of the values at exponent 0, whose scales differ by the power of two alone."""
+    x, w = rnd("fx", (9, 256), BF16), rnd("fw", (256,), BF16, 0.2, 1.0)
+    q0, s0, *_ = m.rms_norm_fp8(x, w, EPS)
+    q, s, *_ = m.rms_norm_fp8(x, (w.double() * 2.0 ** exponent).to(BF16), EPS)
+    assert torch.equal(s.double(), (s0.double() * 2.0 ** exponent).float().double())
+    if exponent > -122:                  # (there the scale has lost bits below the smallest normal value)
+        assert torch.equal(q, q0)
+    else:
+        v, v0 = (t.view(torch.float8_e4m3fn).double() for t in (q, q0))
+        assert torch.isfinite(v).all() and ((v - v0).abs() <= 2.0 ** -3 * v0.abs() + 2.0 ** -9).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("with_dh", [False, True], ids=["plain", "dh"])
 @pytest.mark.parametrize("T,H", NORM_SHAPES)
