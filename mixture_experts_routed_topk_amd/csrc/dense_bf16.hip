@@ -197,18 +197,18 @@ __device__ __forceinline__ void store8(const Job& job, int split, int64_t m, int
 
 // ---------------------------------------------------------------------------- 256 x 256 tiles
 // Eight waves (two per SIMD) in a 2 x 4 grid, each 128 x 64 of the tile as four quadrants (64
-// rows of row half 0 or 1 x 32 columns of column half 0 or 1).  A slice is four phases, one
-// quadrant each: fragment reads and DMA issue, barrier, 16 MFMAs, barrier.  The two waves of a
-// SIMD are half a phase apart (one extra barrier before the loop for the second row of waves),
-// so one reads LDS while the other multiplies.  Two slices live in LDS; a region is refilled
-// with slice kt + 2 as soon as both waves' rows have read it, which keeps 10 to 14 DMAs per wave in
-// flight and gives each about five phases to land.  Phase by phase (slice kt):
-//   0: read R0            multiply R0 x C0   issue R1(kt+1)   wait for C1(kt)
-//   1: read C1            multiply R0 x C1   issue R0(kt+2)   wait for R1(kt)
-//   2: read R1            multiply R1 x C0   issue C0(kt+2)   wait for R0, C0(kt+1)
-//   3: read C0(kt+1)      multiply R1 x C1   issue C1(kt+2)
-// DMAs retire in issue order (R0 C0 C1 | R1 of the next slice in turn), two per region and
-// wave, which gives the vmcnt of each wait.
+// rows of row half 0 or 1 x 32 columns of column half 0 or 1).  A slice is four phases of one
+// quadrant, 16 MFMAs; the fragments of a phase are read from LDS one phase ahead, so a wave's MFMAs
+// never wait for its own reads, and the SIMD's other wave fills what is left:
+//   phase   multiplies   reads            issues (DMA)
+//   0       R0 x C0      C1(kt)           R0(kt+2)
+//   1       R0 x C1      R1(kt)           C0(kt+2)     then: wait for R0, C0(kt+1); barrier
+//   2       R1 x C0      R0(kt+1)         C1(kt+2)
+//   3       R1 x C1      C0(kt+1)         R1(kt+2)     then: wait for C1, R1(kt+1); barrier
+// Two slices live in LDS.  Each barrier publishes the regions read in the next two phases and frees
+// those read in the last two, which the next two phases refill: a DMA has four to six phases
+// (more than a slice's MFMA time) to land.  DMAs retire in issue order, two per region
+// and wave, which gives the vmcnt of each wait.
 template <bool RK, bool CK, int EPI>
 __global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
   __shared__ __attribute__((aligned(1024))) char lds[2][4][REGION];   // [slice parity][R0 R1 C0 C1]
@@ -275,8 +275,8 @@ __global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[a][b][i][j] = f32x4{};
-  bf16x8 r[4][2], c0[2][2], c1[2][2];
-  auto read_r = [&](int h, int kt) __attribute__((always_inline)) {
+  bf16x8 r0[4][2], r1[4][2], c0[2][2], c1[2][2];
+  auto read_r = [&](bf16x8 (&r)[4][2], int h, int kt) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -288,75 +288,52 @@ __global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) c[j][s] = fc.load(&lds[kt & 1][2 + h][0], wn * 32, j, s);
   };
-  auto multiply = [&](f32x4 (&a)[4][2], const bf16x8 (&c)[2][2]) __attribute__((always_inline)) {
+  auto multiply = [&](f32x4 (&a)[4][2], const bf16x8 (&r)[4][2], const bf16x8 (&c)[2][2]) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) a[i][j] = mfma_16x16x32_bf16(c[j][s], r[i][s], a[i][j]);
-    __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
-    barrier();
   };
-  // end of a phase's reads: this wave's fragments are in registers, its part of the awaited
-  // regions has landed, and the barrier makes both hold for the workgroup
-  auto ready = [&]() __attribute__((always_inline)) {
+  // this wave's reads are done and (but for the youngest `more` regions) its DMAs have landed; the
+  // barrier makes both hold for the workgroup
+  auto publish = [&](bool more) __attribute__((always_inline)) {
+    if (more) wait_vmcnt<8>();
+    else wait_vmcnt<0>();
     wait_lds();
-    __builtin_amdgcn_sched_barrier(0);
     barrier();
   };
 
   issue_r(0, 0), issue_c(0, 0), issue_c(1, 0), issue_r(1, 0);
-  if (KT > 1) {
-    issue_r(0, 1), issue_c(0, 1), issue_c(1, 1);
-    wait_vmcnt<10>();
-  } else {
-    wait_vmcnt<4>();
-  }
-  barrier();
+  if (KT > 1) issue_r(0, 1), issue_c(0, 1), issue_c(1, 1), issue_r(1, 1);
+  publish(KT > 1);
+  read_r(r0, 0, 0);
   read_c(c0, 0, 0);
-  if (wm == 1) barrier();
+  wait_lds();
+  barrier();       // (phase 0 refills what was just read)
   for (int kt = 0; kt < KT; ++kt) {
-    const bool more = kt + 2 < KT;
-    read_r(0, kt);
-    if (kt + 1 < KT) {
-      issue_r(1, kt + 1);
-      wait_vmcnt<10>();
-    } else {
-      wait_vmcnt<0>();
-    }
-    ready();
-    multiply(acc[0][0], c0);
-
+    const bool more = kt + 2 < KT, next = kt + 1 < KT;
     read_c(c1, 1, kt);
-    if (more) {
-      issue_r(0, kt + 2);
-      wait_vmcnt<10>();
-    } else {
-      wait_vmcnt<0>();
-    }
-    ready();
-    multiply(acc[0][1], c1);
+    if (more) issue_r(0, kt + 2);
+    multiply(acc[0][0], r0, c0);
 
-    read_r(1, kt);
-    if (more) {
-      issue_c(0, kt + 2);
-      wait_vmcnt<8>();
-    } else {
-      wait_vmcnt<0>();
-    }
-    ready();
-    multiply(acc[1][0], c0);
+    read_r(r1, 1, kt);
+    if (more) issue_c(0, kt + 2);
+    multiply(acc[0][1], r0, c1);
+    publish(more);
 
-    if (kt + 1 < KT) read_c(c0, 0, kt + 1);
+    if (next) read_r(r0, 0, kt + 1);
     if (more) issue_c(1, kt + 2);
-    ready();
-    multiply(acc[1][1], c1);
+    multiply(acc[1][0], r1, c0);
+
+    if (next) read_c(c0, 0, kt + 1);
+    if (more) issue_r(1, kt + 2);
+    multiply(acc[1][1], r1, c1);
+    publish(more);
   }
-  if (wm == 0) barrier();
 
   const int row = lane & 15, col = 8 * (lane >> 4);
 #pragma unroll
