@@ -181,17 +181,33 @@ __device__ __forceinline__ bool tile_of(const Job& job, int b, int& mt, int& nt)
   return true;
 }
 
-template <int EPI>
-__device__ __forceinline__ void store8(const Job& job, int split, int64_t m, int n, const f32x4 z0, const f32x4 z1,
-                                       const f32x4 u0, const f32x4 u1) {
-  if (m >= job.g.M) return;
-  float z[8], u[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = z0[i], z[4 + i] = z1[i], u[i] = u0[i], u[4 + i] = u1[i];
+// Stores FM pieces of eight columns from n on: piece i is row m + 16 i, its sums acc[i] (and, gated, up[i])
+template <int EPI, int FM>
+__device__ __forceinline__ void store_rows(const Job& job, int split, int64_t m, int n, const f32x4 (&acc)[FM][2],
+                                           const f32x4 (&up)[FM][2]) {
+  const DenseEpi& e = job.g.e;
   if constexpr (EPI == kPartial) {
-    if (n < job.crows) Piece<float>::store(job.part, ((int64_t)split * job.g.M + m) * job.ldpart + n, z);
+    if (n >= job.crows) return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (m + 16 * i >= job.g.M) continue;
+      f32x4* out = reinterpret_cast<f32x4*>(job.part + ((int64_t)split * job.g.M + m + 16 * i) * job.ldpart + n);
+      out[0] = acc[i][0];
+      out[1] = acc[i][1];
+    }
   } else {
-    epi_store<uint16_t, EPI == kGated>(job.g.e, m, n, z, u);
+    const EpiBias<uint16_t, EPI == kGated> bias(e, n);
+    EpiRes res[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) res[i] = epi_res<uint16_t>(e, m + 16 * i, job.g.M, n);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (m + 16 * i >= job.g.M) continue;
+      float z[8], u[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) z[v] = acc[i][v >> 2][v & 3], u[v] = up[i][v >> 2][v & 3];
+      epi_store<uint16_t, EPI == kGated>(e, m + 16 * i, n, z, u, bias, res[i]);
+    }
   }
 }
 
@@ -337,19 +353,15 @@ __global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
 
   const int row = lane & 15, col = 8 * (lane >> 4);
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+  for (int a = 0; a < 2; ++a) {
+    const int64_t m = m0 + a * 128 + wm * 64 + row;
+    if constexpr (EPI == kGated) {
+      store_rows<EPI>(job, split, m, n0 + wn * 32 + col, acc[a][0], acc[a][1]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + a * 128 + wm * 64 + i * 16 + row;
-      if constexpr (EPI == kGated) {
-        store8<EPI>(job, split, m, n0 + wn * 32 + col, acc[a][0][i][0], acc[a][0][i][1], acc[a][1][i][0],
-                    acc[a][1][i][1]);
-      } else {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          store8<EPI>(job, split, m, n0 + b * 128 + wn * 32 + col, acc[a][b][i][0], acc[a][b][i][1], f32x4{}, f32x4{});
-      }
+      for (int b = 0; b < 2; ++b) store_rows<EPI>(job, split, m, n0 + b * 128 + wn * 32 + col, acc[a][b], acc[a][b]);
     }
+  }
 }
 
 // ---------------------------------------------------------------------------- RR x 128 tiles
@@ -441,17 +453,13 @@ __global__ __launch_bounds__(256, 2) void dense_128_kernel(Job job) {
           for (int j = 0; j < 2; ++j) acc[b][i][j] = mfma_16x16x32_bf16(c[b][j], r[i], acc[b][i][j]);
     }
   }
-  const int row = lane & 15, col = 8 * (lane >> 4);
+  const int col = n0 + wn * 32 + 8 * (lane >> 4);
+  const int64_t m = m0 + wm * (RR / 2) + (lane & 15);
+  if constexpr (EPI == kGated) {
+    store_rows<EPI>(job, split, m, col, acc[0], acc[1]);
+  } else {
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t m = m0 + wm * (RR / 2) + i * 16 + row;
-    if constexpr (EPI == kGated) {
-      store8<EPI>(job, split, m, n0 + wn * 32 + col, acc[0][i][0], acc[0][i][1], acc[1][i][0], acc[1][i][1]);
-    } else {
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        store8<EPI>(job, split, m, n0 + b * 64 + wn * 32 + col, acc[b][i][0], acc[b][i][1], f32x4{}, f32x4{});
-    }
+    for (int b = 0; b < 2; ++b) store_rows<EPI>(job, split, m, col + b * 64, acc[b], acc[b]);
   }
 }
 
@@ -464,6 +472,8 @@ __global__ __launch_bounds__(256) void dense_join_kernel(Job job) {
   if (i >= job.g.M * n8) return;
   const int64_t m = i / n8;
   const int n = (int)(i - m * n8) * 8;
+  const EpiBias<uint16_t, GATED> bias(job.g.e, n);
+  const EpiRes res = epi_res<uint16_t>(job.g.e, m, job.g.M, n);
   float z[8] = {}, u[8] = {};
   for (int s = 0; s < job.splits; ++s) {
     float v[8];
@@ -477,7 +487,7 @@ __global__ __launch_bounds__(256) void dense_join_kernel(Job job) {
       for (int j = 0; j < 8; ++j) u[j] += v[j];
     }
   }
-  epi_store<uint16_t, GATED>(job.g.e, m, n, z, u);
+  epi_store<uint16_t, GATED>(job.g.e, m, n, z, u, bias, res);
 }
 
 // ---------------------------------------------------------------------------- plan

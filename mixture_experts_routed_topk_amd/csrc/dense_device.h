@@ -135,21 +135,47 @@ __device__ __forceinline__ ActPair act_pair(int act, float z) {
 }
 
 // ---------------------------------------------------------------------------- element store
-// Eight columns n .. n + 7 (n a multiple of 8) of output row m; z (and, gated, u) are the
-// float32 sums.  T is the operands' type.  Columns past e.N are not touched.
+// What the store of eight columns n .. n + 7 (n a multiple of 8) reads besides the sums: the
+// bias (the same for every row) and the residual.  Kernels load them for several pieces
+// before the first store: a load behind a store waits for it, since the two may alias.
 template <typename T, bool GATED>
-__device__ __forceinline__ void epi_store(const DenseEpi& e, int64_t m, int n, float z[8], float u[8]) {
+struct EpiBias {
+  typename Piece<T>::Raw z, u;
+  __device__ __forceinline__ EpiBias(const DenseEpi& e, int n) : z(), u() {
+    if (!e.bias || !e.vec || n >= e.N) return;
+    z = Piece<T>::raw(e.bias, n);
+    if (GATED) u = Piece<T>::raw(e.bias, e.N + n);
+  }
+};
+struct EpiRes {
+  i32x4 lo, hi;   // 16 bytes of bf16, or 32 of float32
+};
+template <typename T>
+__device__ __forceinline__ EpiRes epi_res(const DenseEpi& e, int64_t m, int64_t M, int n) {
+  EpiRes r = {};
+  if (!e.res || !e.vec || n >= e.N || m >= M) return r;
+  const char* p = static_cast<const char*>(e.res) + (m * e.ldr + n) * (e.out_f32 ? 4 : (int)sizeof(T));
+  r.lo = *reinterpret_cast<const i32x4*>(p);
+  if (e.out_f32) r.hi = *reinterpret_cast<const i32x4*>(p + 16);
+  return r;
+}
+
+// Stores eight columns of output row m; z (and, gated, u) are the float32 sums.  T is the
+// operands' type.  Columns past e.N are not touched.
+template <typename T, bool GATED>
+__device__ __forceinline__ void epi_store(const DenseEpi& e, int64_t m, int n, float z[8], float u[8],
+                                          const EpiBias<T, GATED>& bias, const EpiRes& res) {
   constexpr bool FAST = sizeof(T) == 2;
   if (n >= e.N) return;
   const int cnt = min(8, e.N - n);
   if (e.bias) {
-    if (e.vec) {   // (bias shares the alignment rule)
+    if (e.vec) {
       float b[8];
-      Piece<T>::load(e.bias, n, b);
+      Piece<T>::widen(bias.z, b);
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] += b[i];
       if (GATED) {
-        Piece<T>::load(e.bias, e.N + n, b);
+        Piece<T>::widen(bias.u, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] += b[i];
       }
@@ -185,8 +211,8 @@ __device__ __forceinline__ void epi_store(const DenseEpi& e, int64_t m, int n, f
   if (e.vec) {
     if (e.res) {
       float r[8];
-      if (e.out_f32) Piece<float>::load(e.res, rat, r);
-      else Piece<T>::load(e.res, rat, r);
+      if (e.out_f32) Piece<float>::widen({__builtin_bit_cast(f32x4, res.lo), __builtin_bit_cast(f32x4, res.hi)}, r);
+      else Piece<uint16_t>::widen(res.lo, r);    // (float32 operands have float32 outputs)
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] += r[i];
     }

@@ -170,6 +170,11 @@ __global__ __launch_bounds__(G * 256) void dense_f32_kernel(DenseGemm g) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) acc[b][i][j] += sums[((o * 4 * NB + (b * 2 + i) * 2 + j) * 256) + t];
   }
+  const int n = n0 + wn * 32 + 8 * grp;
+  const EpiBias<float, GATED> bias(g.e, n);
+  EpiRes res[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) res[i] = epi_res<float>(g.e, m0 + wm * 32 + i * 16 + r16, g.M, n);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t m = m0 + wm * 32 + i * 16 + r16;
@@ -180,7 +185,7 @@ __global__ __launch_bounds__(G * 256) void dense_f32_kernel(DenseGemm g) {
       z[v] = acc[0][i][v >> 2][v & 3];
       u[v] = acc[NB - 1][i][v >> 2][v & 3];
     }
-    epi_store<float, GATED>(g.e, m, n0 + wn * 32 + 8 * grp, z, u);
+    epi_store<float, GATED>(g.e, m, n, z, u, bias, res[i]);
   }
 }
 
