@@ -103,11 +103,19 @@ BackwardLayout layout(const Backward& b) {
   const bool f32 = b.dtype == MOE_F32;
   L.dz = take(dz_is_dy(b) ? 0 : (size_t)b.T * dz_pitch(b) * esize(b.dtype));
   L.part = take((size_t)dz_parts(b.T) * b.cols * 4);
-  const size_t dx = dense_gemm_workspace(b.T, b.K, b.cols, 0, 0, 1, f32);
-  const size_t dw = dense_gemm_workspace(b.cols, b.K, b.T, 0, 1, 1, f32);
+  const size_t dx = dense_gemm_workspace(b.T, b.K, b.cols, 0, 0, 1, f32, 1);
+  const size_t dw = dense_gemm_workspace(b.cols, b.K, b.T, 0, 1, 1, f32, 1);
   L.gemm = take(dx > dw ? dx : dw);
   L.total = o;
   return L;
+}
+
+// rows of y, residual and pre start on 16 bytes and end on whole pieces of eight
+bool stores_pieces(const moe_linear_problem& p) {
+  return p.N % 8 == 0 && pitch(p.ldy, p.N) % 8 == 0 && pitch(p.ldr, p.N) % 8 == 0 && pitch(p.ldp, p.N) % 8 == 0;
+}
+size_t forward_bytes(const moe_linear_problem& p) {
+  return dense_gemm_workspace(p.T, p.N, p.K, 0, 0, 0, p.dtype == MOE_F32, stores_pieces(p));
 }
 
 #define MOE_HIP_CHECK(expr)                       \
@@ -260,7 +268,7 @@ moe_status moe_linear_workspace_size(const moe_linear_problem* p, int backward, 
   const moe_status st = check(p);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_NULL_ARG;
-  *bytes = backward ? layout(backward_of(*p)).total : dense_gemm_workspace(p->T, p->N, p->K, 0, 0, 0, p->dtype == MOE_F32);
+  *bytes = backward ? layout(backward_of(*p)).total : forward_bytes(*p);
   return MOE_OK;
 }
 
@@ -270,7 +278,7 @@ moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w,
   if (st != MOE_OK) return st;
   if (p->T == 0) return MOE_OK;
   const bool f32 = p->dtype == MOE_F32;
-  const size_t need = dense_gemm_workspace(p->T, p->N, p->K, 0, 0, 0, f32);
+  const size_t need = forward_bytes(*p);
   if (!x || !w || !y || (need && !workspace)) return MOE_ERR_NULL_ARG;
   if (!all_aligned16(x, w, bias, residual, y, pre, workspace)) return MOE_ERR_BAD_SHAPE;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
@@ -292,7 +300,7 @@ moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w,
   g.e.ldp = pitch(p->ldp, p->N);
   g.e.act = p->act;
   g.e.N = p->N;
-  g.e.vec = p->N % 8 == 0 && g.e.ldo % 8 == 0 && (!residual || g.e.ldr % 8 == 0) && (!pre || g.e.ldp % 8 == 0);
+  g.e.vec = stores_pieces(*p);
   MOE_HIP_CHECK(launch_dense_gemm(g, workspace, f32, static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
@@ -310,7 +318,7 @@ moe_status moe_gated_linear_workspace_size(const moe_gated_problem* p, int backw
   const moe_status st = check(p);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_NULL_ARG;
-  *bytes = backward ? layout(backward_of(*p)).total : dense_gemm_workspace(p->T, p->I, p->H, 1, 0, 0, p->dtype == MOE_F32);
+  *bytes = backward ? layout(backward_of(*p)).total : dense_gemm_workspace(p->T, p->I, p->H, 1, 0, 0, p->dtype == MOE_F32, 1);
   return MOE_OK;
 }
 
@@ -320,7 +328,7 @@ moe_status moe_gated_linear(const moe_gated_problem* p, const void* x, const voi
   if (st != MOE_OK) return st;
   if (p->T == 0) return MOE_OK;
   const bool f32 = p->dtype == MOE_F32;
-  const size_t need = dense_gemm_workspace(p->T, p->I, p->H, 1, 0, 0, f32);
+  const size_t need = dense_gemm_workspace(p->T, p->I, p->H, 1, 0, 0, f32, 1);
   if (!x || !w_gate_up || !a || (need && !workspace)) return MOE_ERR_NULL_ARG;
   if (!all_aligned16(x, w_gate_up, bias, a, pre, workspace)) return MOE_ERR_BAD_SHAPE;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;

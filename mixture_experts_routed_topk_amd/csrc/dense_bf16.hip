@@ -20,7 +20,7 @@
 // c sits on the MFMA's row side with its rows permuted (fragment j, row q: column 8 (q / 4) +
 // 4 j + q % 4), so two fragments of a lane are eight consecutive columns of one output row:
 // results leave the registers in 16-byte pieces without a pass through LDS.
-#include <type_traits>
+#include <math.h>
 
 #include "dense_device.h"
 
@@ -196,6 +196,7 @@ __device__ __forceinline__ void store_rows(const Job& job, int split, int64_t m,
       out[1] = acc[i][1];
     }
   } else {
+    if (n >= e.N) return;
     const EpiBias<uint16_t, EPI == kGated> bias(e, n);
     EpiRes res[FM];
 #pragma unroll
@@ -206,7 +207,7 @@ __device__ __forceinline__ void store_rows(const Job& job, int split, int64_t m,
       float z[8], u[8];
 #pragma unroll
       for (int v = 0; v < 8; ++v) z[v] = acc[i][v >> 2][v & 3], u[v] = up[i][v >> 2][v & 3];
-      epi_store<uint16_t, EPI == kGated>(e, m + 16 * i, n, z, u, bias, res[i]);
+      epi_store_vec<uint16_t, EPI == kGated>(e, m + 16 * i, n, z, u, bias, res[i]);
     }
   }
 }
@@ -497,30 +498,37 @@ struct Plan {
   int slices;    // per split
 };
 
-// The tile and split with the least estimated time.  A tile costs its slices plus a fixed part
-// (first DMA, epilogue); tiles run in rounds of the workgroups that fit the 256 CUs; a split
-// adds a pass over its partial sums.
+// The tile and split with the least estimated time.  Tiles go over the 256 CUs in rounds of the
+// workgroups that a CU holds; a slice takes a workgroup at least `alone` us, and `shared` us of its CU;
+// `fixed` us go to a tile's first DMA and epilogue, and a split adds a second launch and a pass over its
+// partial sums.  The constants are a least-squares fit to 43 products of 60 to 8192 rows, each
+// measured with every tile and split (rms error 11%; the choices take 2.5% longer than the best ones).
+struct TileCost {
+  int rows, cols, per_cu;
+  double alone, shared, fixed;
+};
+constexpr TileCost kTiles[] = {{256, 256, 1, 1.33, 1.33, 4.9}, {128, 128, 2, 0.56, 0.42, 1.3}, {64, 128, 3, 0.41, 0.28, 0.0}};
+constexpr double kJoinUs = 4.0, kJoinBytesPerUs = 4e6;
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+
 Plan plan(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor) {
   const int64_t cols = gated ? 2 * N : N;
   const int64_t KT = (K + KS - 1) / KS;
   Plan best{128, 1, (int)KT};
   double best_us = 1e30;
-  for (int tile : {256, 128, 64}) {
-    if (tile == 64 && r_kmajor) continue;
-    const int tn = tile == 256 ? 256 : 128;
-    const int64_t tiles = ((M + tile - 1) / tile) * ((cols + tn - 1) / tn);
-    const int slots = tile == 256 ? 256 : (tile == 128 ? 512 : 768);
-    const double slice_us = tile == 256 ? 1.1 : (tile == 128 ? 0.8 : 0.75), fixed_us = tile == 256 ? 5.0 : 3.0;
-    const double alone_us = tile == 256 ? 1.1 : (tile == 128 ? 0.5 : 0.35);   // a CU with one workgroup
-    for (int s = 1; s <= 16; ++s) {
-      if (s > 1 && KT / s < 4) break;
-      const int64_t per = (KT + s - 1) / s;
-      if ((KT + per - 1) / per != s) continue;        // (every split has slices)
-      const int64_t wgs = tiles * s;
-      const int64_t rounds = (wgs + slots - 1) / slots;
-      const double us = rounds * (per * (wgs <= 256 ? alone_us : slice_us) + fixed_us) +
-                        (s > 1 ? 3.0 + (double)M * cols * 4 * 2 * s / 3e6 : 0.0);
-      if (us < best_us) best_us = us, best = Plan{tile, s, (int)per};
+  for (const TileCost& t : kTiles) {
+    if (t.rows == 64 && r_kmajor) continue;
+    const int64_t tiles = ((M + t.rows - 1) / t.rows) * ((cols + t.cols - 1) / t.cols);
+    for (int want : kSplits) {
+      if (want > 1 && KT / want < 3) break;
+      const int64_t per = (KT + want - 1) / want;
+      const int s = (int)((KT + per - 1) / per);      // (every split has slices)
+      const int64_t queue = (tiles * s + 255) / 256;  // workgroups of one CU
+      const int64_t rest = queue % t.per_cu;
+      double us = (queue / t.per_cu) * (per * fmax(t.alone, t.per_cu * t.shared) + t.fixed);
+      if (rest) us += per * fmax(t.alone, rest * t.shared) + t.fixed;
+      if (s > 1) us += kJoinUs + (double)M * cols * 4 * (s + 1) / kJoinBytesPerUs;
+      if (us < best_us) best_us = us, best = Plan{t.rows, s, (int)per};
     }
   }
   return best;
@@ -559,10 +567,10 @@ hipError_t launch_tiles(const Job& job, int tile, hipStream_t s) {
 
 }  // namespace
 
-size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32) {
+size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32, int vec) {
   if (f32 || M == 0 || K == 0 || few_rows(M, K, r_kmajor, c_kmajor)) return 0;
   const Plan p = plan(M, N, K, gated, r_kmajor);
-  return p.splits > 1 ? (size_t)p.splits * M * part_pitch(N, gated) * 4 : 0;
+  return p.splits > 1 || !vec ? (size_t)p.splits * M * part_pitch(N, gated) * 4 : 0;
 }
 
 hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s) {
@@ -575,10 +583,11 @@ hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t
   job.slices = p.slices;
   job.crows = g.gated ? 2 * g.e.N : g.e.N;
   job.mt = (int)((g.M + p.tile - 1) / p.tile);
-  const bool fused_gate = g.gated && p.splits == 1;
+  const bool join = p.splits > 1 || !g.e.vec;      // the tiles store partial sums
+  const bool fused_gate = g.gated && !join;
   const int tn = (p.tile == 256 ? 256 : 128) / (fused_gate ? 2 : 1);
   job.nt = ((fused_gate ? g.e.N : job.crows) + tn - 1) / tn;
-  if (p.splits == 1) return g.gated ? launch_tiles<kGated>(job, p.tile, s) : launch_tiles<kLinear>(job, p.tile, s);
+  if (!join) return g.gated ? launch_tiles<kGated>(job, p.tile, s) : launch_tiles<kLinear>(job, p.tile, s);
   job.part = static_cast<float*>(ws);
   job.ldpart = part_pitch(g.e.N, g.gated);
   hipError_t err = launch_tiles<kPartial>(job, p.tile, s);

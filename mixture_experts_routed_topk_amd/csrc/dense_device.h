@@ -161,73 +161,39 @@ __device__ __forceinline__ EpiRes epi_res(const DenseEpi& e, int64_t m, int64_t 
 }
 
 // Stores eight columns of output row m; z (and, gated, u) are the float32 sums.  T is the
-// operands' type.  Columns past e.N are not touched.
+// operands' type.  e.vec and n < e.N.
 template <typename T, bool GATED>
-__device__ __forceinline__ void epi_store(const DenseEpi& e, int64_t m, int n, float z[8], float u[8],
-                                          const EpiBias<T, GATED>& bias, const EpiRes& res) {
-  constexpr bool FAST = sizeof(T) == 2;
-  if (n >= e.N) return;
-  const int cnt = min(8, e.N - n);
+__device__ __forceinline__ void epi_store_vec(const DenseEpi& e, int64_t m, int n, float z[8], float u[8],
+                                              const EpiBias<T, GATED>& bias, const EpiRes& res) {
   if (e.bias) {
-    if (e.vec) {
-      float b[8];
-      Piece<T>::widen(bias.z, b);
+    float b[8];
+    Piece<T>::widen(bias.z, b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] += b[i];
-      if (GATED) {
-        Piece<T>::widen(bias.u, b);
+    for (int i = 0; i < 8; ++i) z[i] += b[i];
+    if (GATED) {
+      Piece<T>::widen(bias.u, b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] += b[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < cnt) {
-          z[i] += Piece<T>::get(e.bias, n + i);
-          if (GATED) u[i] += Piece<T>::get(e.bias, e.N + n + i);
-        }
+      for (int i = 0; i < 8; ++i) u[i] += b[i];
     }
   }
   if (e.pre) {
-    const int64_t at = m * e.ldp + n;
-    if (e.vec) {
-      Piece<T>::store(e.pre, at, z);
-      if (GATED) Piece<T>::store(e.pre, at + e.N, u);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < cnt) {
-          Piece<T>::put(e.pre, at + i, z[i]);
-          if (GATED) Piece<T>::put(e.pre, at + e.N + i, u[i]);
-        }
-    }
+    Piece<T>::store(e.pre, m * e.ldp + n, z);
+    if (GATED) Piece<T>::store(e.pre, m * e.ldp + e.N + n, u);
   }
-  act8<FAST>(e.act, z);
+  act8<sizeof(T) == 2>(e.act, z);
   if (GATED) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= u[i];
   }
-  const int64_t at = m * e.ldo + n, rat = m * e.ldr + n;
-  if (e.vec) {
-    if (e.res) {
-      float r[8];
-      if (e.out_f32) Piece<float>::widen({__builtin_bit_cast(f32x4, res.lo), __builtin_bit_cast(f32x4, res.hi)}, r);
-      else Piece<uint16_t>::widen(res.lo, r);    // (float32 operands have float32 outputs)
+  if (e.res) {
+    float r[8];
+    if (e.out_f32) Piece<float>::widen({__builtin_bit_cast(f32x4, res.lo), __builtin_bit_cast(f32x4, res.hi)}, r);
+    else Piece<uint16_t>::widen(res.lo, r);    // (float32 operands have float32 outputs)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] += r[i];
-    }
-    if (e.out_f32) Piece<float>::store(e.out, at, z);
-    else Piece<T>::store(e.out, at, z);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < cnt) {
-        float v = z[i];
-        if (e.res) v += e.out_f32 ? Piece<float>::get(e.res, rat + i) : Piece<T>::get(e.res, rat + i);
-        if (e.out_f32) Piece<float>::put(e.out, at + i, v);
-        else Piece<T>::put(e.out, at + i, v);
-      }
+    for (int i = 0; i < 8; ++i) z[i] += r[i];
   }
+  if (e.out_f32) Piece<float>::store(e.out, m * e.ldo + n, z);
+  else Piece<T>::store(e.out, m * e.ldo + n, z);
 }
 
 // One element (m, n) of the output.
@@ -246,6 +212,20 @@ __device__ __forceinline__ void epi_store1(const DenseEpi& e, int64_t m, int n, 
   if (e.res) z += e.out_f32 ? Piece<float>::get(e.res, m * e.ldr + n) : Piece<T>::get(e.res, m * e.ldr + n);
   if (e.out_f32) Piece<float>::put(e.out, m * e.ldo + n, z);
   else Piece<T>::put(e.out, m * e.ldo + n, z);
+}
+
+// Eight columns in either way; columns past e.N are not touched.
+template <typename T, bool GATED>
+__device__ __forceinline__ void epi_store(const DenseEpi& e, int64_t m, int n, float z[8], float u[8],
+                                          const EpiBias<T, GATED>& bias, const EpiRes& res) {
+  if (n >= e.N) return;
+  if (e.vec) {
+    epi_store_vec<T, GATED>(e, m, n, z, u, bias, res);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (n + i < e.N) epi_store1<T, GATED>(e, m, n + i, z[i], u[i]);
 }
 
 }  // namespace moe

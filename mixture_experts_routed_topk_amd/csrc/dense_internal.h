@@ -70,8 +70,9 @@ struct DenseGemm {
   int gated;
   DenseEpi e;
 };
-// Bytes of scratch the product takes (partial sums of a split contraction).
-size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32);
+// Bytes of scratch the product takes: the partial sums of a split contraction, and of an output
+// that cannot be stored in 16-byte pieces (vec == 0: a second kernel stores it by the element).
+size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32, int vec);
 hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s);
 
 // float32 products
