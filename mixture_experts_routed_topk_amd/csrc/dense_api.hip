@@ -103,9 +103,7 @@ BackwardLayout layout(const Backward& b) {
   const bool f32 = b.dtype == MOE_F32;
   L.dz = take(dz_is_dy(b) ? 0 : (size_t)b.T * dz_pitch(b) * esize(b.dtype));
   L.part = take((size_t)dz_parts(b.T) * b.cols * 4);
-  const size_t dx = dense_gemm_workspace(b.T, b.K, b.cols, 0, 0, 1, f32, 1);
-  const size_t dw = dense_gemm_workspace(b.cols, b.K, b.T, 0, 1, 1, f32, 1);
-  L.gemm = take(dx > dw ? dx : dw);
+  L.gemm = take(dense_gradients_workspace(b.T, b.K, b.cols, f32));
   L.total = o;
   return L;
 }
@@ -115,7 +113,7 @@ bool stores_pieces(const moe_linear_problem& p) {
   return p.N % 8 == 0 && pitch(p.ldy, p.N) % 8 == 0 && pitch(p.ldr, p.N) % 8 == 0 && pitch(p.ldp, p.N) % 8 == 0;
 }
 size_t forward_bytes(const moe_linear_problem& p) {
-  return dense_gemm_workspace(p.T, p.N, p.K, 0, 0, 0, p.dtype == MOE_F32, stores_pieces(p));
+  return dense_gemm_workspace(p.T, p.N, p.K, 0, p.dtype == MOE_F32, stores_pieces(p));
 }
 
 #define MOE_HIP_CHECK(expr)                       \
@@ -159,11 +157,10 @@ moe_status run_backward(const Backward& b, const void* dy, const void* x, const 
     a.dbias = dbias;
     MOE_HIP_CHECK(launch_dz(a, f32, s));
   }
-  auto product = [&](const void* r, int64_t ldr, int r_kmajor, const void* c, int64_t ldc, int64_t M, int64_t K, void* out,
-                     int64_t ldo) {
+  auto product = [&](int r_kmajor, const void* c, int64_t ldc, int64_t M, int64_t K, void* out, int64_t ldo) {
     DenseGemm g{};
-    g.r = r;
-    g.ldr = ldr;
+    g.r = dz;
+    g.ldr = lddz;
     g.r_kmajor = r_kmajor;
     g.c = c;
     g.ldc = ldc;
@@ -174,10 +171,12 @@ moe_status run_backward(const Backward& b, const void* dy, const void* x, const 
     g.e.ldo = ldo;
     g.e.N = b.K;
     g.e.vec = 1;
-    return launch_dense_gemm(g, ws + L.gemm, f32, s);
+    return g;
   };
-  if (dx) MOE_HIP_CHECK(product(dz, lddz, 0, w, b.K, b.T, b.cols, dx, b.lddx));
-  if (dw) MOE_HIP_CHECK(product(dz, lddz, 1, x, b.ldx, b.cols, b.T, dw, b.K));
+  if (dx || dw) {
+    const DenseGemm gx = product(0, w, b.K, b.T, b.cols, dx, b.lddx), gw = product(1, x, b.ldx, b.cols, b.T, dw, b.K);
+    MOE_HIP_CHECK(launch_dense_gradients(dx ? &gx : nullptr, dw ? &gw : nullptr, ws + L.gemm, f32, s));
+  }
   return MOE_OK;
 }
 
@@ -318,7 +317,7 @@ moe_status moe_gated_linear_workspace_size(const moe_gated_problem* p, int backw
   const moe_status st = check(p);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_NULL_ARG;
-  *bytes = backward ? layout(backward_of(*p)).total : dense_gemm_workspace(p->T, p->I, p->H, 1, 0, 0, p->dtype == MOE_F32, 1);
+  *bytes = backward ? layout(backward_of(*p)).total : dense_gemm_workspace(p->T, p->I, p->H, 1, p->dtype == MOE_F32, 1);
   return MOE_OK;
 }
 
@@ -328,7 +327,7 @@ moe_status moe_gated_linear(const moe_gated_problem* p, const void* x, const voi
   if (st != MOE_OK) return st;
   if (p->T == 0) return MOE_OK;
   const bool f32 = p->dtype == MOE_F32;
-  const size_t need = dense_gemm_workspace(p->T, p->I, p->H, 1, 0, 0, f32, 1);
+  const size_t need = dense_gemm_workspace(p->T, p->I, p->H, 1, f32, 1);
   if (!x || !w_gate_up || !a || (need && !workspace)) return MOE_ERR_NULL_ARG;
   if (!all_aligned16(x, w_gate_up, bias, a, pre, workspace)) return MOE_ERR_BAD_SHAPE;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;

@@ -46,7 +46,8 @@ __device__ __forceinline__ void barrier() {
   fence();
 }
 
-enum { kLinear = 0, kGated = 1, kPartial = 2 };
+// kPartial: float32 sums to job.part; kGrad: those, or with one split the plain bf16 result
+enum { kLinear = 0, kGated = 1, kPartial = 2, kGrad = 3 };
 
 // ---------------------------------------------------------------------------- DMA
 // Where instruction `ins` (1 KB) of a 128-row region takes lane `lane`'s 16 bytes from.
@@ -186,7 +187,17 @@ template <int EPI, int FM>
 __device__ __forceinline__ void store_rows(const Job& job, int split, int64_t m, int n, const f32x4 (&acc)[FM][2],
                                            const f32x4 (&up)[FM][2]) {
   const DenseEpi& e = job.g.e;
-  if constexpr (EPI == kPartial) {
+  if (EPI == kGrad && !job.part) {
+    if (n >= e.N) return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (m + 16 * i >= job.g.M) continue;
+      float z[8];
+#pragma unroll
+      for (int v = 0; v < 8; ++v) z[v] = acc[i][v >> 2][v & 3];
+      Piece<uint16_t>::store(e.out, (m + 16 * i) * e.ldo + n, z);
+    }
+  } else if constexpr (EPI == kPartial || EPI == kGrad) {
     if (n >= job.crows) return;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -226,18 +237,17 @@ __device__ __forceinline__ void store_rows(const Job& job, int split, int64_t m,
 // those read in the last two, which the next two phases refill: a DMA has four to six phases
 // (more than a slice's MFMA time) to land.  DMAs retire in issue order, two per region
 // and wave, which gives the vmcnt of each wait.
+constexpr int kLds256 = 2 * 4 * REGION;   // [slice parity][R0 R1 C0 C1]
 template <bool RK, bool CK, int EPI>
-__global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
-  __shared__ __attribute__((aligned(1024))) char lds[2][4][REGION];   // [slice parity][R0 R1 C0 C1]
+__device__ __forceinline__ void tile_256(const Job& job, int block, int split, char* lds) {
   int mt, nt;
-  if (!tile_of(job, blockIdx.x, mt, nt)) return;
+  if (!tile_of(job, block, mt, nt)) return;
   const DenseGemm& g = job.g;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int64_t m0 = (int64_t)mt * 256;
   const int n0 = nt * (EPI == kGated ? 128 : 256);
-  const int split = blockIdx.y;
   const int64_t k0 = (int64_t)split * job.slices * KS;
   const int KT = (int)min((int64_t)job.slices, (g.K - k0 + KS - 1) / KS);
   const int left = (int)min((int64_t)KS, g.K - k0 - (int64_t)(KT - 1) * KS);   // k in the last slice
@@ -261,7 +271,7 @@ __global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
       return min(h * 128 + row, last);
     });
   }
-  const uint32_t lds0 = lds_addr(&lds[0][0][0]);
+  const uint32_t lds0 = lds_addr(lds);
   auto issue_r = [&](int h, int kt) __attribute__((always_inline)) {
     const char* base = rbase + kt * rstep;
     const uint32_t dst = lds0 + (uint32_t)(((kt & 1) * 4 + h) * REGION + wave * 2048);
@@ -297,13 +307,13 @@ __global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) r[i][s] = fr.load(&lds[kt & 1][h][0], wm * 64 + i * 16, s);
+      for (int s = 0; s < 2; ++s) r[i][s] = fr.load(lds + ((kt & 1) * 4 + h) * REGION, wm * 64 + i * 16, s);
   };
   auto read_c = [&](bf16x8 (&c)[2][2], int h, int kt) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) c[j][s] = fc.load(&lds[kt & 1][2 + h][0], wn * 32, j, s);
+      for (int s = 0; s < 2; ++s) c[j][s] = fc.load(lds + ((kt & 1) * 4 + 2 + h) * REGION, wn * 32, j, s);
   };
   auto multiply = [&](f32x4 (&a)[4][2], const bf16x8 (&r)[4][2], const bf16x8 (&c)[2][2]) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
@@ -365,26 +375,32 @@ __global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
   }
 }
 
+template <bool RK, bool CK, int EPI>
+__global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
+  __shared__ __attribute__((aligned(1024))) char lds[kLds256];
+  tile_256<RK, CK, EPI>(job, blockIdx.x, blockIdx.y, lds);
+}
+
 // ---------------------------------------------------------------------------- RR x 128 tiles
 // Four waves (2 x 2), two slices in LDS, one barrier per slice; two (RR = 128) or three (RR =
 // 64) workgroups share a CU, so one's waits are covered by the others' MFMAs.  A wave's
 // columns are 32 of each half of the tile (gated: 32 gate and the matching 32 up columns).
+template <int RR>
+constexpr int lds_128() { return 2 * (RR * KS * 2 + REGION); }
 template <int RR, bool RK, bool CK, int EPI>
-__global__ __launch_bounds__(256, 2) void dense_128_kernel(Job job) {
+__device__ __forceinline__ void tile_128(const Job& job, int block, int split, char* lds) {
   constexpr int FM = RR / 32;                              // 16-row fragments per wave
   constexpr int RBYTES = RR * KS * 2, STAGE = RBYTES + REGION;
   constexpr int NR = RBYTES / 4096, NC = REGION / 4096;    // DMA instructions per wave and slice
   static_assert(RR == 128 || !RK, "rows stored along k come in regions of 128");
-  __shared__ __attribute__((aligned(1024))) char lds[2][STAGE];
   int mt, nt;
-  if (!tile_of(job, blockIdx.x, mt, nt)) return;
+  if (!tile_of(job, block, mt, nt)) return;
   const DenseGemm& g = job.g;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int64_t m0 = (int64_t)mt * RR;
   const int n0 = nt * (EPI == kGated ? 64 : 128);
-  const int split = blockIdx.y;
   const int64_t k0 = (int64_t)split * job.slices * KS;
   const int KT = (int)min((int64_t)job.slices, (g.K - k0 + KS - 1) / KS);
   const int left = (int)min((int64_t)KS, g.K - k0 - (int64_t)(KT - 1) * KS);
@@ -402,7 +418,7 @@ __global__ __launch_bounds__(256, 2) void dense_128_kernel(Job job) {
     const int last = CK ? (job.crows - 1 - n0) / 8 * 8 : job.crows - 1 - n0;
     return min(row, last);
   });
-  const uint32_t lds0 = lds_addr(&lds[0][0]);
+  const uint32_t lds0 = lds_addr(lds);
   auto issue = [&](int kt) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + (uint32_t)((kt & 1) * STAGE);
     const char* rb = rbase + kt * rstep;
@@ -435,7 +451,7 @@ __global__ __launch_bounds__(256, 2) void dense_128_kernel(Job job) {
     wait_lds();          // (and the reads of slice kt - 1 are done: its buffer is refilled next)
     barrier();
     if (kt + 1 < KT) issue(kt + 1);
-    const char* R = &lds[kt & 1][0];
+    const char* R = lds + (kt & 1) * STAGE;
     const char* C = R + RBYTES;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -464,12 +480,41 @@ __global__ __launch_bounds__(256, 2) void dense_128_kernel(Job job) {
   }
 }
 
+template <int RR, bool RK, bool CK, int EPI>
+__global__ __launch_bounds__(256, 2) void dense_128_kernel(Job job) {
+  __shared__ __attribute__((aligned(1024))) char lds[lds_128<RR>()];
+  tile_128<RR, RK, CK, EPI>(job, blockIdx.x, blockIdx.y, lds);
+}
+
+// ---------------------------------------------------------------------------- both gradients in one launch
+// dx (r along k) in tiles of TA rows and dw (both operands along their rows) in tiles of TB: two
+// products that do not depend on each other share the CUs, so one's last tiles are
+// covered by the other's (2731 x 2048 x 5632: 352 and 704 tiles of 128 x 128 on 512 places, 75 us
+// and 70 us one after the other).  The product with the longer tiles comes first.  Blocks
+// [0, n_first) belong to the first one; a split's blocks follow one another.
+template <int TA, int TB>
+__global__ __launch_bounds__(TA == 256 ? 512 : 256, TA == 256 ? 1 : 2) void dense_pair_kernel(Job dx, Job dw, int n_first,
+                                                                                             int dw_first) {
+  constexpr int L = TA == 256 ? kLds256 : lds_128<128>();
+  __shared__ __attribute__((aligned(1024))) char lds[L];
+  const bool first = (int)blockIdx.x < n_first;
+  const int b = first ? blockIdx.x : blockIdx.x - n_first;
+  if (first == (dw_first != 0)) {
+    const int n = (dw.mt * dw.nt + 7) / 8 * 8;
+    if constexpr (TB == 256) tile_256<true, true, kGrad>(dw, b % n, b / n, lds);
+    else tile_128<TB, true, true, kGrad>(dw, b % n, b / n, lds);
+  } else {
+    const int n = (dx.mt * dx.nt + 7) / 8 * 8;
+    if constexpr (TA == 256) tile_256<false, true, kGrad>(dx, b % n, b / n, lds);
+    else tile_128<TA, false, true, kGrad>(dx, b % n, b / n, lds);
+  }
+}
+
 // ---------------------------------------------------------------------------- sum of the splits
 // Adds the splits' partial sums in their order and applies the epilogue; one thread per eight columns.
 template <bool GATED>
-__global__ __launch_bounds__(256) void dense_join_kernel(Job job) {
+__device__ __forceinline__ void join(const Job& job, int64_t i) {
   const int n8 = (job.g.e.N + 7) / 8;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= job.g.M * n8) return;
   const int64_t m = i / n8;
   const int n = (int)(i - m * n8) * 8;
@@ -491,6 +536,15 @@ __global__ __launch_bounds__(256) void dense_join_kernel(Job job) {
   epi_store<uint16_t, GATED>(job.g.e, m, n, z, u, bias, res);
 }
 
+template <bool GATED>
+__global__ __launch_bounds__(256) void dense_join_kernel(Job job) {
+  join<GATED>(job, (int64_t)blockIdx.x * 256 + threadIdx.x);
+}
+__global__ __launch_bounds__(256) void dense_join_pair_kernel(Job a, Job b, int n_first) {
+  if ((int)blockIdx.x < n_first) join<false>(a, (int64_t)blockIdx.x * 256 + threadIdx.x);
+  else join<false>(b, (int64_t)(blockIdx.x - n_first) * 256 + threadIdx.x);
+}
+
 // ---------------------------------------------------------------------------- plan
 struct Plan {
   int tile;      // 256, 128 or 64 (rows of a tile)
@@ -501,23 +555,22 @@ struct Plan {
 // The tile and split with the least estimated time.  Tiles go over the 256 CUs in rounds of the
 // workgroups that a CU holds; a slice takes a workgroup at least `alone` us, and `shared` us of its CU;
 // `fixed` us go to a tile's first DMA and epilogue, and a split adds a second launch and a pass over its
-// partial sums.  The constants are a least-squares fit to 43 products of 60 to 8192 rows, each
-// measured with every tile and split (rms error 11%; the choices take 2.5% longer than the best ones).
+// partial sums.  The constants are fitted to 43 products of 60 to 8192 rows, each measured with every
+// tile and split (rms error of the estimate 13%; the choices take 1.6% longer than the best ones).
 struct TileCost {
   int rows, cols, per_cu;
   double alone, shared, fixed;
 };
-constexpr TileCost kTiles[] = {{256, 256, 1, 1.33, 1.33, 4.9}, {128, 128, 2, 0.56, 0.42, 1.3}, {64, 128, 3, 0.41, 0.28, 0.0}};
-constexpr double kJoinUs = 4.0, kJoinBytesPerUs = 4e6;
+constexpr TileCost kTiles[] = {{256, 256, 1, 1.115, 1.115, 7.0}, {128, 128, 2, 0.549, 0.353, 0.57}, {64, 128, 3, 0.328, 0.251, 0.02}};
+constexpr double kJoinUs = 2.8, kJoinBytesPerUs = 3.36e6;
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 
-Plan plan(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor) {
+Plan plan(int64_t M, int64_t N, int64_t K, int gated) {
   const int64_t cols = gated ? 2 * N : N;
   const int64_t KT = (K + KS - 1) / KS;
   Plan best{128, 1, (int)KT};
   double best_us = 1e30;
   for (const TileCost& t : kTiles) {
-    if (t.rows == 64 && r_kmajor) continue;
     const int64_t tiles = ((M + t.rows - 1) / t.rows) * ((cols + t.cols - 1) / t.cols);
     for (int want : kSplits) {
       if (want > 1 && KT / want < 3) break;
@@ -533,50 +586,88 @@ Plan plan(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor) {
   }
   return best;
 }
-// Products of few rows with both operands stored along k (the forward ones) have kernels of their own.
-bool few_rows(int64_t M, int64_t K, int r_kmajor, int c_kmajor) {
-  return !r_kmajor && !c_kmajor && dense_rows_take(M, K);
-}
 int64_t part_pitch(int64_t N, int gated) { return ((gated ? 2 * N : N) + 7) / 8 * 8; }
 
 template <int EPI>
 hipError_t launch_tiles(const Job& job, int tile, hipStream_t s) {
   const int total = job.mt * job.nt;
   const dim3 grid((unsigned)((total + 7) / 8 * 8), (unsigned)job.splits);
-  const bool rk = job.g.r_kmajor, ck = job.g.c_kmajor;
-  if (tile == 256) {
-    if (!rk && !ck) hipLaunchKernelGGL((dense_256_kernel<false, false, EPI>), grid, dim3(512), 0, s, job);
-    if constexpr (EPI != kGated) {
-      if (!rk && ck) hipLaunchKernelGGL((dense_256_kernel<false, true, EPI>), grid, dim3(512), 0, s, job);
-      if (rk && ck) hipLaunchKernelGGL((dense_256_kernel<true, true, EPI>), grid, dim3(512), 0, s, job);
-    }
-  } else if (tile == 128) {
-    if (!rk && !ck) hipLaunchKernelGGL((dense_128_kernel<128, false, false, EPI>), grid, dim3(256), 0, s, job);
-    if constexpr (EPI != kGated) {
-      if (!rk && ck) hipLaunchKernelGGL((dense_128_kernel<128, false, true, EPI>), grid, dim3(256), 0, s, job);
-      if (rk && ck) hipLaunchKernelGGL((dense_128_kernel<128, true, true, EPI>), grid, dim3(256), 0, s, job);
-    }
-  } else {
-    if (!ck) hipLaunchKernelGGL((dense_128_kernel<64, false, false, EPI>), grid, dim3(256), 0, s, job);
-    if constexpr (EPI != kGated) {
-      if (ck) hipLaunchKernelGGL((dense_128_kernel<64, false, true, EPI>), grid, dim3(256), 0, s, job);
+  if (tile == 256) hipLaunchKernelGGL((dense_256_kernel<false, false, EPI>), grid, dim3(512), 0, s, job);
+  else if (tile == 128) hipLaunchKernelGGL((dense_128_kernel<128, false, false, EPI>), grid, dim3(256), 0, s, job);
+  else hipLaunchKernelGGL((dense_128_kernel<64, false, false, EPI>), grid, dim3(256), 0, s, job);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------- plan of the gradients
+struct PairPlan {
+  int tiles;                     // index into kPairs
+  int splits[2], slices[2];      // dx, dw
+};
+constexpr int kPairs[][2] = {{0, 0}, {1, 1}, {2, 1}};   // kTiles of dx and of dw
+
+// dx [M0][N] over K0 and dw [M1][N] over K1; a product with no rows is left out.  Their tiles share
+// the CUs: the time is the work of all of them over 256 CUs, at least the longest tile's own,
+// and half a tile more for the uneven end.
+PairPlan plan_pair(const int64_t (&M)[2], int64_t N, const int64_t (&K)[2]) {
+  constexpr int kTry[] = {1, 2, 4, 8, 16};
+  PairPlan best{1, {1, 1}, {1, 1}};
+  double best_us = 1e30;
+  for (int t = 0; t < 3; ++t) {
+    for (int a : kTry) {
+      for (int b : kTry) {
+        PairPlan p{t, {a, b}, {1, 1}};
+        double work = 0, longest = 0, shortest = 1e30, joined = 0;
+        bool ok = true;
+        for (int j = 0; j < 2; ++j) {
+          const int want = j ? b : a;
+          if (M[j] == 0 || K[j] == 0) {
+            p.splits[j] = 1;
+            ok = ok && want == 1;
+            continue;
+          }
+          const TileCost& c = kTiles[kPairs[t][j]];
+          const int64_t KT = (K[j] + KS - 1) / KS;
+          const double whole = (double)((M[j] + c.rows - 1) / c.rows) * ((N + c.cols - 1) / c.cols);
+          if (want > 1 && (KT / want < 3 || whole >= 512)) {   // (too short, or no need)
+            ok = false;
+            break;
+          }
+          const int64_t per = (KT + want - 1) / want;
+          p.splits[j] = (int)((KT + per - 1) / per);
+          p.slices[j] = (int)per;
+          const double tiles = whole * p.splits[j];
+          work += tiles * (per * c.shared + c.fixed);
+          const double own = per * c.alone + c.fixed;
+          longest = fmax(longest, own);
+          shortest = fmin(shortest, own);
+          if (p.splits[j] > 1) joined += (double)M[j] * N * 4 * (p.splits[j] + 1);
+        }
+        if (!ok) continue;
+        double us = fmax(work / 256 + 0.5 * shortest, longest);
+        if (joined > 0) us += kJoinUs + joined / kJoinBytesPerUs;
+        if (us < best_us) best_us = us, best = p;
+      }
     }
   }
-  return hipGetLastError();
+  return best;
+}
+// bytes of the partial sums of product j
+size_t pair_part(const PairPlan& p, int j, int64_t M, int64_t N) {
+  return p.splits[j] > 1 ? ((size_t)p.splits[j] * M * N * 4 + 255) & ~size_t(255) : 0;
 }
 
 }  // namespace
 
-size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32, int vec) {
-  if (f32 || M == 0 || K == 0 || few_rows(M, K, r_kmajor, c_kmajor)) return 0;
-  const Plan p = plan(M, N, K, gated, r_kmajor);
+size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, bool f32, int vec) {
+  if (f32 || M == 0 || dense_rows_take(M, K)) return 0;
+  const Plan p = plan(M, N, K, gated);
   return p.splits > 1 || !vec ? (size_t)p.splits * M * part_pitch(N, gated) * 4 : 0;
 }
 
 hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s) {
   if (f32) return launch_dense_gemm_f32(g, s);
-  if (few_rows(g.M, g.K, g.r_kmajor, g.c_kmajor)) return launch_dense_rows(g, s);
-  const Plan p = plan(g.M, g.e.N, g.K, g.gated, g.r_kmajor);
+  if (dense_rows_take(g.M, g.K)) return launch_dense_rows(g, s);
+  const Plan p = plan(g.M, g.e.N, g.K, g.gated);
   Job job{};
   job.g = g;
   job.splits = p.splits;
@@ -596,6 +687,61 @@ hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t
   const dim3 grid((unsigned)((pieces + 255) / 256));
   if (g.gated) hipLaunchKernelGGL(dense_join_kernel<true>, grid, dim3(256), 0, s, job);
   else hipLaunchKernelGGL(dense_join_kernel<false>, grid, dim3(256), 0, s, job);
+  return hipGetLastError();
+}
+
+size_t dense_gradients_workspace(int64_t T, int64_t N, int64_t cols, bool f32) {
+  if (f32 || T == 0) return 0;
+  size_t most = 0;
+  for (int which = 1; which < 4; ++which) {        // dx, dw or both may be asked for
+    const int64_t M[2] = {which & 1 ? T : 0, which & 2 ? cols : 0}, K[2] = {cols, T};
+    const PairPlan p = plan_pair(M, N, K);
+    const size_t need = pair_part(p, 0, M[0], N) + pair_part(p, 1, M[1], N);
+    most = need > most ? need : most;
+  }
+  return most;
+}
+
+hipError_t launch_dense_gradients(const DenseGemm* dx, const DenseGemm* dw, void* ws, bool f32, hipStream_t s) {
+  if (f32) {
+    hipError_t err = dx ? launch_dense_gemm_f32(*dx, s) : hipSuccess;
+    return err == hipSuccess && dw ? launch_dense_gemm_f32(*dw, s) : err;
+  }
+  const DenseGemm* g[2] = {dx, dw};
+  const int64_t M[2] = {dx ? dx->M : 0, dw ? dw->M : 0}, K[2] = {dx ? dx->K : 0, dw ? dw->K : 0};
+  const int64_t N = dx ? dx->e.N : dw->e.N;
+  const PairPlan p = plan_pair(M, N, K);
+  Job job[2] = {};
+  int blocks[2] = {}, join_blocks[2] = {};
+  size_t at = 0;
+  for (int j = 0; j < 2; ++j) {
+    if (!g[j]) continue;
+    const TileCost& c = kTiles[kPairs[p.tiles][j]];
+    Job& q = job[j];
+    q.g = *g[j];
+    q.splits = p.splits[j];
+    q.slices = p.slices[j];
+    q.crows = (int)N;
+    q.mt = (int)((M[j] + c.rows - 1) / c.rows);
+    q.nt = (int)((N + c.cols - 1) / c.cols);
+    blocks[j] = (q.mt * q.nt + 7) / 8 * 8 * q.splits;
+    if (q.splits > 1) {
+      q.part = reinterpret_cast<float*>(static_cast<char*>(ws) + at);
+      q.ldpart = N;
+      at += pair_part(p, j, M[j], N);
+      join_blocks[j] = (int)((M[j] * (N / 8) + 255) / 256);
+    }
+  }
+  const int dw_first = !dx || (dw && p.slices[1] > p.slices[0]);
+  const dim3 grid((unsigned)(blocks[0] + blocks[1]));
+  const int n_first = blocks[dw_first];
+  if (p.tiles == 0) hipLaunchKernelGGL((dense_pair_kernel<256, 256>), grid, dim3(512), 0, s, job[0], job[1], n_first, dw_first);
+  else if (p.tiles == 1) hipLaunchKernelGGL((dense_pair_kernel<128, 128>), grid, dim3(256), 0, s, job[0], job[1], n_first, dw_first);
+  else hipLaunchKernelGGL((dense_pair_kernel<64, 128>), grid, dim3(256), 0, s, job[0], job[1], n_first, dw_first);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || !(join_blocks[0] + join_blocks[1])) return err;
+  hipLaunchKernelGGL(dense_join_pair_kernel, dim3((unsigned)(join_blocks[0] + join_blocks[1])), dim3(256), 0, s, job[0],
+                     job[1], join_blocks[0]);
   return hipGetLastError();
 }
 

@@ -70,10 +70,16 @@ struct DenseGemm {
   int gated;
   DenseEpi e;
 };
-// Bytes of scratch the product takes: the partial sums of a split contraction, and of an output
-// that cannot be stored in 16-byte pieces (vec == 0: a second kernel stores it by the element).
-size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, int r_kmajor, int c_kmajor, bool f32, int vec);
+// Forward products (both operands stored along k).  Bytes of scratch: the partial sums of a split
+// contraction, and of an output that cannot be stored in 16-byte pieces (vec == 0: a second
+// kernel stores it by the element).
+size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, bool f32, int vec);
 hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s);
+
+// The gradients dx [T][N] = dz w (c stored along its rows) and dw [cols][N] = dz^T x (both stored along
+// their rows), dz [T][cols]; either may be null.  Outputs in the operands' type, no epilogue.
+size_t dense_gradients_workspace(int64_t T, int64_t N, int64_t cols, bool f32);
+hipError_t launch_dense_gradients(const DenseGemm* dx, const DenseGemm* dw, void* ws, bool f32, hipStream_t s);
 
 // float32 products
 hipError_t launch_dense_gemm_f32(const DenseGemm& g, hipStream_t s);
