@@ -81,8 +81,11 @@ hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t
 size_t dense_gradients_workspace(int64_t T, int64_t N, int64_t cols, bool f32);
 hipError_t launch_dense_gradients(const DenseGemm* dx, const DenseGemm* dw, void* ws, bool f32, hipStream_t s);
 
-// float32 products
-hipError_t launch_dense_gemm_f32(const DenseGemm& g, hipStream_t s);
+// The same in float32 (dense_f32.hip)
+size_t dense_gemm_f32_workspace(int64_t M, int64_t N, int64_t K, int gated, int vec);
+hipError_t launch_dense_gemm_f32(const DenseGemm& g, void* ws, hipStream_t s);
+size_t dense_gradients_f32_workspace(int64_t rows, int64_t N, int64_t cols);
+hipError_t launch_dense_gradients_f32(const DenseGemm* dx, const DenseGemm* dw, void* ws, hipStream_t s);
 
 // bf16 products of few rows with both operands stored along k
 bool dense_rows_take(int64_t M, int64_t K);
