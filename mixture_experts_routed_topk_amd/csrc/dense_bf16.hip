@@ -213,14 +213,13 @@ void launch_tiles(const Job& job, int tile, hipStream_t s) {
 }  // namespace
 
 size_t dense_gemm_workspace(int64_t M, int64_t N, int64_t K, int gated, bool f32, int vec) {
-  if (M == 0) return 0;
-  if (f32) return dense_gemm_f32_workspace(M, N, K, gated, vec);
-  return dense_rows_take(M, K) ? 0 : forward_part(plan_bf16(M, N, K, gated), M, N, gated, vec);
+  if (M == 0 || dense_rows_take(M, K, f32)) return 0;
+  return f32 ? dense_gemm_f32_workspace(M, N, K, gated, vec) : forward_part(plan_bf16(M, N, K, gated), M, N, gated, vec);
 }
 
 hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t s) {
+  if (dense_rows_take(g.M, g.K, f32)) return launch_dense_rows(g, f32, s);
   if (f32) return launch_dense_gemm_f32(g, ws, s);
-  if (dense_rows_take(g.M, g.K)) return launch_dense_rows(g, s);
   const Plan p = plan_bf16(g.M, g.e.N, g.K, g.gated);
   return run_forward<uint16_t>(g, p, p.tile == 256 ? 256 : 128, ws, s, [&](const Job& job, int epi) {
     if (epi == kPartial) launch_tiles<kPartial>(job, p.tile, s);

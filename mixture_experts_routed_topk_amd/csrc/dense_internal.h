@@ -87,9 +87,9 @@ hipError_t launch_dense_gemm_f32(const DenseGemm& g, void* ws, hipStream_t s);
 size_t dense_gradients_f32_workspace(int64_t rows, int64_t N, int64_t cols);
 hipError_t launch_dense_gradients_f32(const DenseGemm* dx, const DenseGemm* dw, void* ws, hipStream_t s);
 
-// bf16 products of few rows with both operands stored along k
-bool dense_rows_take(int64_t M, int64_t K);
-hipError_t launch_dense_rows(const DenseGemm& g, hipStream_t s);
+// forward products of few rows
+bool dense_rows_take(int64_t M, int64_t K, bool f32);
+hipError_t launch_dense_rows(const DenseGemm& g, bool f32, hipStream_t s);
 
 // ---------------------------------------------------------------------------- backward
 // dz = dy * act'(pre) (gated: [da * up * act'(gate), da * act(gate)]) in the operands' type,
