@@ -343,7 +343,7 @@ moe_status moe_set_stage_events(void* const* events, int n);
  *
  * They keep the conventions above with one addition: activations have a row pitch.  A
  * pitch is in elements, 0 stands for packed rows, and otherwise it is at least the row's
- * length and at most 2^22.  Weights are packed.  No matrix has more than 2^40 elements.  Types are MOE_F32 or MOE_BF16; sums,
+ * length and at most 2^22.  Weights are packed.  No matrix has more than 2^34 elements.  Types are MOE_F32 or MOE_BF16; sums,
  * statistics and activations are computed in float32 and every output is rounded once to
  * its type (bf16: nearest even).  Results do not depend on timing: sums over workgroups
  * are added in a fixed order, without atomics.  Calls launch kernels only (no host wait, no
@@ -356,7 +356,7 @@ moe_status moe_set_stage_events(void* const* events, int n);
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 /* z * Phi(z) */, MOE_ACT_RELU = 3 } moe_act;
 
 typedef struct {
-  int64_t T;          /* rows, 0 .. 2^31 - 1                                               */
+  int64_t T;          /* rows, 0 .. 2^22 - 1                                               */
   int32_t H;          /* row length, a multiple of 8, 8 .. 65536                           */
   int32_t dtype;      /* moe_dtype of every tensor that is not float32 by its name         */
   float eps;          /* >= 0 and finite                                                   */
@@ -403,7 +403,7 @@ moe_status moe_rms_norm_backward(const moe_norm_problem* p, const void* dy, cons
                                  size_t workspace_bytes, void* stream);
 
 typedef struct {
-  int64_t T;          /* rows, 0 .. 2^31 - 1                                               */
+  int64_t T;          /* rows, 0 .. 2^22 - 1                                               */
   int32_t K;          /* inputs, a multiple of 8, 8 .. 65536                               */
   int32_t N;          /* outputs, 1 .. 2^20                                                */
   int32_t dtype;      /* moe_dtype of x, w, bias, pre, dx, dw and dbias                    */
@@ -444,7 +444,7 @@ moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, cons
                                size_t workspace_bytes, void* stream);
 
 typedef struct {
-  int64_t T;          /* rows, 0 .. 2^31 - 1                                               */
+  int64_t T;          /* rows, 0 .. 2^22 - 1                                               */
   int32_t H;          /* inputs, a multiple of 8, 8 .. 65536                               */
   int32_t I;          /* outputs, a multiple of 8, 8 .. 65536                              */
   int32_t dtype;      /* moe_dtype of every tensor                                         */

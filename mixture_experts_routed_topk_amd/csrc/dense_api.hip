@@ -9,11 +9,11 @@
 namespace moe {
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxRows = (int64_t(1) << 22) - 1;   // one workgroup of 1024 threads to a row stays below 2^32 threads
 constexpr int64_t kMaxPitch = int64_t(1) << 22;   // tile offsets fit in 32 bits
 constexpr int kMaxWidth = 65536;                  // H, I, K
 constexpr int kMaxOutputs = 1 << 20;              // N
-constexpr int64_t kMaxElements = int64_t(1) << 40;  // of any activation: tile counts fit in 31 bits
+constexpr int64_t kMaxElements = int64_t(1) << 34;  // of any matrix: a thread to eight of them stays below 2^32 threads
 
 bool aligned16(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) == 0; }
 bool aligned4(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) == 0; }
@@ -42,7 +42,7 @@ moe_status check(const moe_linear_problem* p) {
   if (!type_ok(p->dtype) || (p->out_dtype != p->dtype && p->out_dtype != MOE_F32)) return MOE_ERR_UNSUPPORTED;
   if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_RELU) return MOE_ERR_UNSUPPORTED;
   if (p->T < 0 || p->T > kMaxRows || !width_ok(p->K) || p->N < 1 || p->N > kMaxOutputs ||
-      p->T * p->N > kMaxElements || p->T * p->K > kMaxElements)
+      p->T * p->N > kMaxElements || p->T * p->K > kMaxElements || (int64_t)p->N * p->K > kMaxElements)
     return MOE_ERR_BAD_SHAPE;
   if (!pitch_ok(p->ldx, p->K, true) || !pitch_ok(p->lddx, p->K, true)) return MOE_ERR_BAD_SHAPE;
   for (int64_t ld : {p->ldy, p->ldr, p->ldp})

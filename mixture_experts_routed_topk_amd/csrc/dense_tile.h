@@ -302,6 +302,7 @@ __device__ __forceinline__ void tile_128(const Job& job, int block, int split, c
   constexpr int KS = ks<T>();
   constexpr int RBYTES = RR * 128, STAGE = RBYTES + REGION;
   constexpr int NR = RBYTES / 4096, NC = REGION / 4096;    // DMA instructions per wave and slice
+  static_assert(NC == 4, "a wave fills 32 rows of c's region");
   static_assert(RR == 128 || !RK, "rows stored along k come in regions of 128");
   int mt, nt;
   if (!tile_of(job, block, mt, nt)) return;
@@ -316,12 +317,15 @@ __device__ __forceinline__ void tile_128(const Job& job, int block, int split, c
   const int left = (int)min((int64_t)KS, g.K - k0 - (int64_t)(KT - 1) * KS);
   const char* rbase = origin<T, RK>(g.r, g.ldr, m0, k0);
   const char* cbase = origin<T, CK>(g.c, g.ldc, n0, k0);
+  // gated: rows 64 .. 127 of c's region, the second two waves' instructions, are the up projection's,
+  // N rows on (more than 32-bit offsets reach)
+  if constexpr (EPI == kGated) cbase += (int64_t)(wave >> 1) * g.e.N * g.ldc * (int64_t)sizeof(T);
   const int64_t rstep = slice_bytes<T, RK>(g.ldr), cstep = slice_bytes<T, CK>(g.ldc);
   Stream<T, RK, false, NR> sr;
   Stream<T, CK, true, NC> sc;
   sr.init(wave * NR, lane, g.ldr, [&](int row) -> int64_t { return min((int64_t)row, last_row<T, RK>(g.M - m0)); });
   sc.init(wave * NC, lane, g.ldc, [&](int row) -> int64_t {
-    if constexpr (EPI == kGated) return (int64_t)(row >> 6) * g.e.N + min(row & 63, g.e.N - 1 - n0);
+    if constexpr (EPI == kGated) return min(row & 63, g.e.N - 1 - n0);
     return min((int64_t)row, last_row<T, CK>(job.crows - n0));
   });
   const uint32_t lds0 = lds_addr(lds);

@@ -35,15 +35,16 @@ def size(fn, p, *args):
     return fn(ctypes.byref(p), *args, ctypes.byref(n)), n.value
 
 
-BAD_NORM = [(dict(T=-1), 2), (dict(T=2**31), 2), (dict(H=0), 2), (dict(H=4), 2), (dict(H=12), 2), (dict(H=65544), 2),
+BAD_NORM = [(dict(T=-1), 2), (dict(T=2**22), 2), (dict(H=0), 2), (dict(H=4), 2), (dict(H=12), 2), (dict(H=65544), 2),
             (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2), (dict(eps=float("inf")), 2), (dict(ldx=248), 2),
             (dict(ldx=260), 2), (dict(ldr=8), 2), (dict(ldh=2**22 + 8), 2), (dict(ldy=-8), 2),
             (dict(dtype=m.FP8_E4M3), 3), (dict(dtype=9), 3)]
-BAD_LINEAR = [(dict(T=-1), 2), (dict(T=2**31), 2), (dict(K=0), 2), (dict(K=60), 2), (dict(K=65544), 2), (dict(N=0), 2),
-              (dict(N=2**20 + 1), 2), (dict(T=2**21, N=2**20), 2), (dict(T=2**25, K=65536), 2), (dict(ldx=68), 2), (dict(ldx=56), 2), (dict(ldy=59), 2), (dict(ldr=2**22 + 1), 2),
+BAD_LINEAR = [(dict(T=-1), 2), (dict(T=2**22), 2), (dict(K=0), 2), (dict(K=60), 2), (dict(K=65544), 2), (dict(N=0), 2),
+              (dict(N=2**20 + 1), 2), (dict(T=2**15, N=2**20), 2), (dict(T=2**20, K=65536), 2),
+              (dict(K=65536, N=2**20), 2), (dict(ldx=68), 2), (dict(ldx=56), 2), (dict(ldy=59), 2), (dict(ldr=2**22 + 1), 2),
               (dict(ldp=-1), 2), (dict(lddx=60), 2), (dict(act=4), 3), (dict(act=-1), 3), (dict(dtype=m.FP4_E2M1), 3),
               (dict(dtype=m.F32), 3), (dict(out_dtype=m.FP8_E4M3), 3)]
-BAD_GATED = [(dict(T=-1), 2), (dict(H=60), 2), (dict(I=60), 2), (dict(I=0), 2), (dict(I=65544), 2), (dict(T=2**25, H=65536), 2), (dict(T=2**24, I=65536), 2), (dict(ldx=56), 2),
+BAD_GATED = [(dict(T=-1), 2), (dict(H=60), 2), (dict(I=60), 2), (dict(I=0), 2), (dict(I=65544), 2), (dict(T=2**20, H=65536), 2), (dict(T=2**18, I=65536), 2), (dict(ldx=56), 2),
              (dict(lda=60), 2), (dict(ldp=64), 2), (dict(ldp=132), 2), (dict(lddx=68), 2), (dict(act=0), 3),
              (dict(act=4), 3), (dict(dtype=m.FP8_E4M3), 3)]
 

@@ -299,6 +299,51 @@ def test_calls_on_several_streams_at_once():
                 assert ok
 
 
+# ----------------------------------------------------------------------------- far offsets
+
+@pytest.mark.parametrize("T", [3, 40, 700])
+def test_gated_weights_beyond_32_bit_offsets(T):
+    """The up projection's rows start more than 4 GiB behind the gate's; sampled columns against the
+    64-bit form."""
+    H, I = 65536, 32784
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.empty((2 * I, H), dtype=BF16, device="cuda").normal_(0, H ** -0.5, generator=g)
+    x = rnd("ox", (T, H), BF16)
+    a, pre = m.gated_linear(x, w, save_pre=True)
+    cols = torch.tensor([0, 1, 63, 64, 127, 128, 8191, 32768, I - 1], device="cuda")
+    ws = torch.cat([w[cols], w[I + cols]])
+    (ra, ba), (rz, bz) = ref.gated(x, ws, None, "silu", BF16)
+    ref.check(a[:, cols], ra, ba, "a")
+    ref.check(pre[:, torch.cat([cols, I + cols])], rz, bz, "pre")
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Activations of more than 4 GiB: the last rows of every output."""
+    T, H = 70000, 32768
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.empty((T, H), dtype=BF16, device="cuda").normal_(generator=g)
+    w, nw = rnd("ow", (24, H), BF16, H ** -0.5), rnd("onw", (H,), BF16, 0.2, 1.0)
+    y, _ = m.linear(x, w)
+    tail = x[-300:].clone()
+    (ry, by), _ = ref.linear(tail, w, None, None, "none", BF16, BF16)
+    ref.check(y[-300:], ry, by, "linear")
+    n, _, rstd = m.rms_norm(x, nw, EPS)
+    (rn, bn), _, (rr, br), _ = ref.norm(tail, nw, EPS, None, BF16)
+    ref.check(n[-300:], rn, bn, "norm")
+    ref.check(rstd[-300:], rr, br, "rstd")
+    dy = rnd("ody", (T, 24), BF16)
+    dx, dw, _ = m.linear_backward(dy, x, w)
+    grads = ref.backward(*ref.dz_linear(dy[-300:], None, "none"), tail, w, BF16)
+    ref.check(dx[-300:], *grads[0], "dx")
+    part = torch.zeros((24, 64), dtype=torch.float64, device="cuda")      # dw's last columns, in pieces of rows
+    mag = torch.zeros_like(part)
+    for i in range(0, T, 10000):
+        d, xs = dy[i:i + 10000].double(), x[i:i + 10000, -64:].double()
+        part += d.t() @ xs
+        mag += d.abs().t() @ xs.abs()
+    ref.check(dw[:, -64:], part, (T + 1) * ref.U32 * mag + 2.0 ** -8 * part.abs() * 1.01, "dw")
+
+
 # ----------------------------------------------------------------------------- refusals of the binding
 
 def test_binding_refuses():
