@@ -44,7 +44,7 @@ __device__ __forceinline__ void tile_256(const Job& job, int block, int split, c
   const char* cbase = origin<T, CK>(g.c, g.ldc, n0, k0);
   const int64_t rstep = slice_bytes<T, RK>(g.ldr), cstep = slice_bytes<T, CK>(g.ldc);
   // gated: the second column half is the up projection's rows, N rows on (more than 32-bit offsets reach)
-  const int64_t chalf = EPI == kGated ? (int64_t)g.e.N * g.ldc * (int64_t)sizeof(T) : 0;
+  const char* const chalf[2] = {cbase, cbase + (EPI == kGated ? (int64_t)g.e.N * g.ldc * (int64_t)sizeof(T) : 0)};
   Stream<T, RK, false, 2> sr[2];
   Stream<T, CK, true, 2> sc[2];
 #pragma unroll
@@ -67,7 +67,7 @@ __device__ __forceinline__ void tile_256(const Job& job, int block, int split, c
     }
   };
   auto issue_c = [&](int h, int kt) __attribute__((always_inline)) {
-    const char* base = cbase + h * chalf + kt * cstep;
+    const char* base = chalf[h] + kt * cstep;
     const uint32_t dst = lds0 + (uint32_t)(((kt & 1) * 4 + 2 + h) * REGION + wave * 2048);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
