@@ -363,22 +363,28 @@ __device__ __forceinline__ void tile_128(const Job& job, int block, int split, c
     if (kt + 1 < KT) issue(kt + 1);
     const char* R = lds + (kt & 1) * STAGE;
     const char* C = R + RBYTES;
+    // the whole slice's fragments before its products: both halves' LDS latency is paid once (4096 x 2048
+    // x 2048: 35.9 -> 34.2 us; the next slice's DMA behind the first products: 36.7)
+    Frag<T> r[2][FM], c[2][2][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      Frag<T> r[FM], c[2][2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) c[b][j] = fc.load(C, b * 64 + wn * 32, j, s);
+        for (int j = 0; j < 2; ++j) c[s][b][j] = fc.load(C, b * 64 + wn * 32, j, s);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) r[i] = fr.load(R, wm * (RR / 2) + i * 16, s);
+      for (int i = 0; i < FM; ++i) r[s][i] = fr.load(R, wm * (RR / 2) + i * 16, s);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[b][i][j] = multiply_add(c[b][j], r[i], acc[b][i][j]);
-    }
+          for (int j = 0; j < 2; ++j) acc[b][i][j] = multiply_add(c[s][b][j], r[s][i], acc[b][i][j]);
+    __builtin_amdgcn_sched_barrier(0);
   }
   const int col = n0 + wn * 32 + 8 * (lane >> 4);
   const int64_t m = m0 + wm * (RR / 2) + (lane & 15);
