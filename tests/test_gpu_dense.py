@@ -260,3 +260,34 @@ def test_gradients_match_differences(name):
     for k, g in enumerate(m.gated_linear_backward(da, x, w, pre, ACT[name], need_bias=True)):
         v = rnd(f"gv{k}", tuple(g.shape), F32).double()
         assert abs(directional(gat, args, k, v) - (g.double() * v).sum().item()) <= 1e-5 * (g.norm() * v.norm()).item()
+
+
+# ----------------------------------------------------------------------------- the largest tiles
+
+def test_large_linear():
+    T, K, N = 4000, 7176, 4096          # 256 tiles of 256 x 256, a contraction that ends 8 into a slice
+    x, w, b, r = linear_case(T, K, N, BF16, BF16, True, True, pad=1)
+    y, pre = m.linear(x, w, b, r, m.ACT_GELU, save_pre=True)
+    (ry, by), (rz, bz) = ref.linear(x, w, b, r, "gelu", BF16, BF16)
+    ref.check(y, ry, by, "y")
+    ref.check(pre, rz, bz, "pre")
+
+
+def test_large_gated():
+    T, H, I = 3999, 7176, 2040
+    x, w = rnd("bx", (T, H), BF16, pad=8), rnd("bw", (2 * I, H), BF16, H ** -0.5)
+    b = rnd("bb", (2 * I,), BF16, 0.5)
+    a, pre = m.gated_linear(x, w, b, save_pre=True)
+    (ra, ba), (rz, bz) = ref.gated(x, w, b, "silu", BF16)
+    ref.check(a, ra, ba, "a")
+    ref.check(pre, rz, bz, "pre")
+
+
+def test_large_gradients():
+    T, K, N = 8187, 7168, 4104          # both gradients in 256 x 256 tiles, both contractions ragged
+    x, w = rnd("lx", (T, K), BF16), rnd("lw", (N, K), BF16, K ** -0.5)
+    dy = rnd("ldy", (T, N), BF16)
+    dx, dw, db = m.linear_backward(dy, x, w, need_bias=True)
+    grads = ref.backward(*ref.dz_linear(dy, None, "none"), x, w, BF16)
+    for got, (r, b), what in zip((dx, dw, db), grads, ("dx", "dw", "db")):
+        ref.check(got, r, b, what)

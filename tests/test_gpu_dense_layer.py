@@ -299,6 +299,42 @@ def test_calls_on_several_streams_at_once():
                 assert ok
 
 
+def test_calls_from_several_host_threads():
+    import threading
+    sets = [calls(T, 256, 136, f"t{i}") for i, T in enumerate((2, 65, 300))]
+    want = [[[t.clone() for t in flat(f())] for f in fns] for fns in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                got = [flat(f()) for f in sets[i]]
+                torch.cuda.current_stream().synchronize()
+                if not all(same(t, r) for out, ref_out in zip(got, want[i]) for t, r in zip(out, ref_out)):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_results_do_not_depend_on_what_the_workspace_held():
+    """The caller's workspace may hold anything, NaN among it, and may be larger than needed."""
+    for T, K, N in ((20, 7168, 61), (200, 2048, 264), (8, 512, 512)):
+        x, w = rnd("wx", (T, K), BF16), rnd("ww", (N, K), BF16, K ** -0.5)
+        dy, z = rnd("wdy", (T, N), BF16), rnd("wz", (T, N), BF16)
+        ws = torch.full((1 << 27,), 0xFF, dtype=torch.uint8, device="cuda")
+        assert same(m.linear(x, w, workspace=ws)[0], m.linear(x, w)[0])
+        ws.fill_(0xFF)
+        got = m.linear_backward(dy, x, w, pre=z, act=m.ACT_SILU, need_bias=True, workspace=ws)
+        for a, b in zip(got, m.linear_backward(dy, x, w, pre=z, act=m.ACT_SILU, need_bias=True)):
+            assert same(a, b)
+
+
 # ----------------------------------------------------------------------------- far offsets
 
 @pytest.mark.parametrize("T", [3, 40, 700])
