@@ -554,7 +554,7 @@ def _rms_norm(x, weight, eps, residual, fp8, with_y):
     else:
         ldr = _rows("residual", residual, T, H, dtype, dev)
         h = torch.empty_like(x)
-    prob, _ = _problem(NormProblem, (T, H, dt, eps, _rows("x", x, T, H, dtype, dev), ldr, 0, 0))
+    prob, _ = _problem(NormProblem, (T, H, dt, float(eps), _rows("x", x, T, H, dtype, dev), ldr, 0, 0))
     y = torch.empty_like(x) if with_y else None
     rstd = x.new_empty(T, dtype=torch.float32)
     q = scale = None
@@ -620,7 +620,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     if bias is not None:
         _packed("bias", bias, (N,), dtype, dev)
     ldr = 0 if residual is None else _rows("residual", residual, T, N, odt, dev)
-    fields = (T, K, N, dt, _ACT[odt], act, _rows("x", x, T, K, dtype, dev), 0, ldr, 0, 0)
+    fields = (T, K, N, dt, _ACT[odt], int(act), _rows("x", x, T, K, dtype, dev), 0, ldr, 0, 0)
     prob, need = _problem(LinearProblem, fields, "moe_linear_workspace_size", 0)
     ws, n = _scratch(workspace, need, x, dev)
     y = x.new_empty((T, N), dtype=odt)
@@ -647,7 +647,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre: Opt
         raise ValueError("an activation's gradient needs pre")
     else:
         ldp = _rows("pre", pre, T, N, dtype, dev)
-    fields = (T, K, N, dt, ody, act, _rows("x", x, T, K, dtype, dev), _rows("dy", dy, T, N, dy.dtype, dev), 0, ldp, 0)
+    fields = (T, K, N, dt, ody, int(act), _rows("x", x, T, K, dtype, dev), _rows("dy", dy, T, N, dy.dtype, dev), 0, ldp, 0)
     return _backward("moe_linear_backward", LinearProblem, fields, dy, x, w, pre, N, need_bias, workspace, dev)
 
 
@@ -677,7 +677,7 @@ def gated_linear(x: torch.Tensor, w_gate_up: torch.Tensor, bias: Optional[torch.
     dt, dev, T, H, I = _gated_sizes(x, w_gate_up)
     if bias is not None:
         _packed("bias", bias, (2 * I,), x.dtype, dev)
-    fields = (T, H, I, dt, act, _rows("x", x, T, H, x.dtype, dev), 0, 0, 0)
+    fields = (T, H, I, dt, int(act), _rows("x", x, T, H, x.dtype, dev), 0, 0, 0)
     prob, need = _problem(GatedProblem, fields, "moe_gated_linear_workspace_size", 0)
     ws, n = _scratch(workspace, need, x, dev)
     a = x.new_empty((T, I))
@@ -692,7 +692,7 @@ def gated_linear_backward(da: torch.Tensor, x: torch.Tensor, w_gate_up: torch.Te
     """(dx, dw, dbias) of gated_linear from da and the pre it saved; dbias None without need_bias.
     See moe_gated_linear_backward."""
     dt, dev, T, H, I = _gated_sizes(x, w_gate_up)
-    fields = (T, H, I, dt, act, _rows("x", x, T, H, x.dtype, dev), _rows("da", da, T, I, x.dtype, dev),
+    fields = (T, H, I, dt, int(act), _rows("x", x, T, H, x.dtype, dev), _rows("da", da, T, I, x.dtype, dev),
               _rows("pre", pre, T, 2 * I, x.dtype, dev), 0)
     return _backward("moe_gated_linear_backward", GatedProblem, fields, da, x, w_gate_up, pre, 2 * I, need_bias,
                      workspace, dev)

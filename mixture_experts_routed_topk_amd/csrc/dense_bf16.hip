@@ -22,18 +22,16 @@ namespace {
 // 4096: 354 us; DMAs before the products 374, before the reads 378; reads spread between
 // the products 364-379).  With every tile reading the same, L2-resident operands the time is the same
 // within 2%: the loop is bound by what a CU does, not by its operand stream.
+// NH = 1 is half a tile, 128 rows from m0: R1, its reads and products and its DMAs are left out.
 constexpr int kLds256 = 2 * 4 * REGION;   // [slice parity][R0 R1 C0 C1]
-template <bool RK, bool CK, int EPI>
-__device__ __forceinline__ void tile_256(const Job& job, int block, int split, char* lds) {
+template <bool RK, bool CK, int EPI, int NH>
+__device__ __forceinline__ void tile_256(const Job& job, int64_t m0, int nt, int split, char* lds) {
   using T = uint16_t;
   constexpr int KS = ks<T>();
-  int mt, nt;
-  if (!tile_of(job, block, mt, nt)) return;
   const DenseGemm& g = job.g;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const int64_t m0 = (int64_t)mt * 256;
   const int n0 = nt * (EPI == kGated ? 128 : 256);
   const int64_t k0 = (int64_t)split * job.slices * KS;
   const int KT = (int)min((int64_t)job.slices, (g.K - k0 + KS - 1) / KS);
@@ -45,12 +43,13 @@ __device__ __forceinline__ void tile_256(const Job& job, int block, int split, c
   const int64_t rstep = slice_bytes<T, RK>(g.ldr), cstep = slice_bytes<T, CK>(g.ldc);
   // gated: the second column half is the up projection's rows, N rows on (more than 32-bit offsets reach)
   const char* const chalf[2] = {cbase, cbase + (EPI == kGated ? (int64_t)g.e.N * g.ldc * (int64_t)sizeof(T) : 0)};
-  Stream<T, RK, false, 2> sr[2];
+  Stream<T, RK, false, 2> sr[NH];
   Stream<T, CK, true, 2> sc[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    sr[h].init(wave * 2, lane, g.ldr,
-               [&](int row) -> int64_t { return min((int64_t)(h * 128 + row), last_row<T, RK>(g.M - m0)); });
+    if (h < NH)
+      sr[h].init(wave * 2, lane, g.ldr,
+                 [&](int row) -> int64_t { return min((int64_t)(h * 128 + row), last_row<T, RK>(g.M - m0)); });
     sc[h].init(wave * 2, lane, g.ldc, [&](int row) -> int64_t {
       if constexpr (EPI == kGated) return min(row, g.e.N - 1 - n0);
       return min((int64_t)(h * 128 + row), last_row<T, CK>(job.crows - n0));
@@ -78,9 +77,9 @@ __device__ __forceinline__ void tile_256(const Job& job, int block, int split, c
 
   const RowFrag<T, RK> fr(lane);
   const ColFrag<T, CK> fc(lane);
-  f32x4 acc[2][2][4][2];
+  f32x4 acc[NH][2][4][2];
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+  for (int a = 0; a < NH; ++a)
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -113,14 +112,18 @@ __device__ __forceinline__ void tile_256(const Job& job, int block, int split, c
   // this wave's reads are done and (but for the youngest `more` regions) its DMAs have landed; the
   // barrier makes both hold for the workgroup
   auto publish = [&](bool more) __attribute__((always_inline)) {
-    if (more) wait_vmcnt<8>();
+    if (more) wait_vmcnt<4 + 2 * NH>();
     else wait_vmcnt<0>();
     wait_lds();
     barrier();
   };
 
-  issue_r(0, 0), issue_c(0, 0), issue_c(1, 0), issue_r(1, 0);
-  if (KT > 1) issue_r(0, 1), issue_c(0, 1), issue_c(1, 1), issue_r(1, 1);
+  issue_r(0, 0), issue_c(0, 0), issue_c(1, 0);
+  if constexpr (NH == 2) issue_r(1, 0);
+  if (KT > 1) {
+    issue_r(0, 1), issue_c(0, 1), issue_c(1, 1);
+    if constexpr (NH == 2) issue_r(1, 1);
+  }
   publish(KT > 1);
   read_r(r0, 0, 0);
   read_c(c0, 0, 0);
@@ -132,24 +135,26 @@ __device__ __forceinline__ void tile_256(const Job& job, int block, int split, c
     multiply(acc[0][0], r0, c0);
     if (more) issue_r(0, kt + 2);
 
-    read_r(r1, 1, kt);
+    if constexpr (NH == 2) read_r(r1, 1, kt);
     multiply(acc[0][1], r0, c1);
     if (more) issue_c(0, kt + 2);
     publish(more);
 
     if (next) read_r(r0, 0, kt + 1);
-    multiply(acc[1][0], r1, c0);
+    if constexpr (NH == 2) multiply(acc[1][0], r1, c0);
     if (more) issue_c(1, kt + 2);
 
     if (next) read_c(c0, 0, kt + 1);
-    multiply(acc[1][1], r1, c1);
-    if (more) issue_r(1, kt + 2);
+    if constexpr (NH == 2) {
+      multiply(acc[1][1], r1, c1);
+      if (more) issue_r(1, kt + 2);
+    }
     publish(more);
   }
 
   const int row = lane & 15, col = 8 * (lane >> 4);
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
+  for (int a = 0; a < NH; ++a) {
     const int64_t m = m0 + a * 128 + wm * 64 + row;
     if constexpr (EPI == kGated) {
       store_rows<T, EPI>(job, split, m, n0 + wn * 32 + col, acc[a][0], acc[a][1]);
@@ -161,9 +166,35 @@ __device__ __forceinline__ void tile_256(const Job& job, int block, int split, c
 }
 
 template <bool RK, bool CK, int EPI>
+__device__ __forceinline__ void whole_256(const Job& job, int block, int split, char* lds) {
+  int mt, nt;
+  if (tile_of(job, block, mt, nt)) tile_256<RK, CK, EPI, 2>(job, (int64_t)mt * 256, nt, split, lds);
+}
+
+// Forward.  HALVES: the tiles from job.whole on are run as two workgroups of 128 rows each, on one XCD
+// one after the other (they share c's rows); a kernel of its own, since in the common one the extra
+// path costs 2% (6144 x 2048 x 7168: 160 against 168 us).
+template <int EPI, bool HALVES>
 __global__ __launch_bounds__(512, 1) void dense_256_kernel(Job job) {
   __shared__ __attribute__((aligned(1024))) char lds[kLds256];
-  tile_256<RK, CK, EPI>(job, blockIdx.x, blockIdx.y, lds);
+  if constexpr (!HALVES) {
+    whole_256<false, false, EPI>(job, blockIdx.x, blockIdx.y, lds);
+  } else {
+    const int total = job.mt * job.nt;
+    const int b = (int)blockIdx.x - job.whole;
+    int mt, nt;
+    if (b < 0) {
+      tile_at(job, (blockIdx.x & 7) * (job.whole >> 3) + (blockIdx.x >> 3), mt, nt);
+      tile_256<false, false, EPI, 2>(job, (int64_t)mt * 256, nt, 0, lds);
+    } else {
+      const int per = (total - job.whole + 7) >> 3;
+      const int t = job.whole + (b & 7) * per + (b >> 4);
+      if (t >= total) return;
+      tile_at(job, t, mt, nt);
+      const int64_t m0 = (int64_t)mt * 256 + ((b >> 3) & 1) * 128;
+      if (m0 < job.g.M) tile_256<false, false, EPI, 1>(job, m0, nt, 0, lds);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------- both gradients in one launch
@@ -181,11 +212,11 @@ __global__ __launch_bounds__(TA == 256 ? 512 : 256, TA == 256 ? 1 : 2) void dens
   const int b = first ? blockIdx.x : blockIdx.x - n_first;
   if (first == (dw_first != 0)) {
     const int n = (dw.mt * dw.nt + 7) / 8 * 8;
-    if constexpr (TB == 256) tile_256<true, true, kGrad>(dw, b % n, b / n, lds);
+    if constexpr (TB == 256) whole_256<true, true, kGrad>(dw, b % n, b / n, lds);
     else tile_128<uint16_t, TB, true, true, kGrad>(dw, b % n, b / n, lds);
   } else {
     const int n = (dx.mt * dx.nt + 7) / 8 * 8;
-    if constexpr (TA == 256) tile_256<false, true, kGrad>(dx, b % n, b / n, lds);
+    if constexpr (TA == 256) whole_256<false, true, kGrad>(dx, b % n, b / n, lds);
     else tile_128<uint16_t, TA, false, true, kGrad>(dx, b % n, b / n, lds);
   }
 }
@@ -210,7 +241,13 @@ Plan plan_bf16(int64_t M, int64_t N, int64_t K, int gated) { return plan_forward
 template <int EPI>
 void launch_tiles(const Job& job, int tile, hipStream_t s) {
   const dim3 grid = tile_grid(job);
-  if (tile == 256) hipLaunchKernelGGL((dense_256_kernel<false, false, EPI>), grid, dim3(512), 0, s, job);
+  if (tile == 256) {
+    if (EPI != kPartial && job.whole < job.mt * job.nt) {
+      hipLaunchKernelGGL((dense_256_kernel<EPI, EPI != kPartial>), grid, dim3(512), 0, s, job);
+    } else {
+      hipLaunchKernelGGL((dense_256_kernel<EPI, false>), grid, dim3(512), 0, s, job);
+    }
+  }
   else if (tile == 128) hipLaunchKernelGGL((dense_128_kernel<uint16_t, 128, false, false, EPI>), grid, dim3(256), 0, s, job);
   else hipLaunchKernelGGL((dense_128_kernel<uint16_t, 64, false, false, EPI>), grid, dim3(256), 0, s, job);
 }

@@ -13,11 +13,11 @@ struct NormArgs {
   int64_t T;
   int H;
   float eps;
-  int64_t ldx, ldr, ldh, ldy;   // row pitches in elements
-  const void* x;                // backward: dx is written through xo
+  int64_t ldx, ldr, ldh, ldy;   // row pitches in elements (backward: of dx, dh, h, dy)
+  const void* x;
   const void* res;              // residual (backward: dh), may be null
   const void* weight;
-  void* y;                      // may be null (backward: dy is read through dy)
+  void* y;                      // may be null
   void* h;                      // x + residual (forward, when there is a residual)
   float* rstd;
   uint8_t* q;                   // e4m3 codes [T][H], may be null

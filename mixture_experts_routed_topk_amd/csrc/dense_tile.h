@@ -187,7 +187,8 @@ struct ColFrag {
 struct Job {
   DenseGemm g;
   int mt, nt;          // tiles
-  int splits;          // contraction split over blockIdx.y
+  int whole;           // 256 x 256 tiles, forward: tiles from this one on (a multiple of 256) are run as halves
+  int splits;          // parts of the contraction
   int slices;          // slices of one split
   int crows;           // rows of c (gated: 2 I)
   float* part;         // [splits][M][ldpart] partial sums (splits > 1)
@@ -219,19 +220,23 @@ struct Stream {
   }
 };
 
-// Tile (mt, nt) of workgroup b.  Consecutive workgroups go to the eight XCDs in turn; each XCD
-// takes a contiguous run of tiles, ordered in groups of 8 tile rows with the row fastest, so
-// the 32 tiles that run together on an XCD are 8 x 4 and share their operands in its L2.
-__device__ __forceinline__ bool tile_of(const Job& job, int b, int& mt, int& nt) {
-  const int total = job.mt * job.nt;
-  const int per = (total + 7) >> 3;
-  const int t = (b & 7) * per + (b >> 3);
-  if ((b >> 3) >= per || t >= total) return false;
+// Tile t of a product: groups of 8 tile rows, the row fastest
+__device__ __forceinline__ void tile_at(const Job& job, int t, int& mt, int& nt) {
   const int grp = t / (8 * job.nt);
   const int rows = min(8, job.mt - grp * 8);
   const int l = t - grp * 8 * job.nt;
   mt = grp * 8 + l % rows;
   nt = l / rows;
+}
+// Tile (mt, nt) of workgroup b.  Consecutive workgroups go to the eight XCDs in turn; each XCD
+// takes a contiguous run of tiles, so the 32 tiles that run together on an XCD are 8 x 4 and
+// share their operands in its L2.
+__device__ __forceinline__ bool tile_of(const Job& job, int b, int& mt, int& nt) {
+  const int total = job.mt * job.nt;
+  const int per = (total + 7) >> 3;
+  const int t = (b & 7) * per + (b >> 3);
+  if ((b >> 3) >= per || t >= total) return false;
+  tile_at(job, t, mt, nt);
   return true;
 }
 
@@ -453,6 +458,11 @@ struct JoinCost {
 };
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 
+// The last round of 256-row tiles runs as halves when those find a CU each (8192 x 2048 x 7168, 3.5 rounds:
+// 247 -> 235 us; 0.7 to 0.8 of a whole tile's time).  The plan does not count on it: in 16 of 16 products where
+// that would have moved the choice from 128-row tiles these stayed faster, by 1 to 14%.
+inline int64_t whole_tiles(int rows, int64_t tiles) { return rows == 256 && tiles % 256 <= 128 ? tiles / 256 * 256 : tiles; }
+
 // The tile and split of a forward product with the least estimated time.  Tiles go over the 256 CUs in
 // rounds of the workgroups that a CU holds; a slice takes a workgroup at least `alone` us, and `shared`
 // us of its CU; `fixed` us go to a tile's first DMA and epilogue, and a split adds a second launch
@@ -500,6 +510,8 @@ hipError_t run_forward(const DenseGemm& g, const Plan& p, int tile_cols, void* w
   const bool fused_gate = g.gated && !parts;
   const int tn = tile_cols / (fused_gate ? 2 : 1);
   job.nt = ((fused_gate ? g.e.N : job.crows) + tn - 1) / tn;
+  const int64_t all = (int64_t)job.mt * job.nt;
+  job.whole = (int)(parts ? all : whole_tiles(p.tile, all));
   if (parts) {
     job.part = static_cast<float*>(ws);
     job.ldpart = part_pitch(g.e.N, g.gated);
@@ -512,7 +524,10 @@ hipError_t run_forward(const DenseGemm& g, const Plan& p, int tile_cols, void* w
   else hipLaunchKernelGGL((dense_join_kernel<T, false>), grid, dim3(256), 0, s, job);
   return hipGetLastError();
 }
-inline dim3 tile_grid(const Job& job) { return dim3((unsigned)((job.mt * job.nt + 7) / 8 * 8), (unsigned)job.splits); }
+inline dim3 tile_grid(const Job& job) {
+  const int halved = job.mt * job.nt - job.whole;
+  return dim3((unsigned)((job.whole + 7) / 8 * 8 + (halved + 7) / 8 * 16), (unsigned)job.splits);
+}
 
 // ---------------------------------------------------------------------------- plan of the gradients
 struct PairPlan {

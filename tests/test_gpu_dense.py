@@ -291,3 +291,25 @@ def test_large_gradients():
     grads = ref.backward(*ref.dz_linear(dy, None, "none"), x, w, BF16)
     for got, (r, b), what in zip((dx, dw, db), grads, ("dx", "dw", "db")):
         ref.check(got, r, b, what)
+
+
+# Three whole rounds of 256 x 256 tiles and less than half a round, which runs as halves; the last tile row's
+# lower halves have no rows, and the contraction ends 8 into a slice.
+
+def test_half_tiles_linear():
+    T, K, N = 7700, 2056, 7168
+    x, w, b, r = linear_case(T, K, N, BF16, BF16, True, True, pad=1)
+    y, pre = m.linear(x, w, b, r, m.ACT_RELU, save_pre=True)
+    (ry, by), (rz, bz) = ref.linear(x, w, b, r, "relu", BF16, BF16)
+    ref.check(y, ry, by, "y")
+    ref.check(pre, rz, bz, "pre")
+
+
+def test_half_tiles_gated():
+    T, H, I = 3900, 2056, 7168
+    x, w = rnd("hx", (T, H), BF16, pad=8), rnd("hw", (2 * I, H), BF16, H ** -0.5)
+    b = rnd("hb", (2 * I,), BF16, 0.5)
+    a, pre = m.gated_linear(x, w, b, save_pre=True)
+    (ra, ba), (rz, bz) = ref.gated(x, w, b, "silu", BF16)
+    ref.check(a, ra, ba, "a")
+    ref.check(pre, rz, bz, "pre")
