@@ -2,7 +2,7 @@
 //
 // linear: dz = dy act'(pre).  gated: dz = [da up act'(gate), da act(gate)], pre = [gate, up].
 // dz goes to scratch in the operands' type (the type the MFMA products take; each dz is
-// rounded once, as the saved pre-activations were), with zeros in the columns between the
+// rounded once, as the saved pre-activations were; TWO: what that takes is kept as a second part), with zeros in the columns between the
 // last one and its pitch so that rows can be read in whole 16-byte pieces.  The bias gradient sums the
 // float32 dz before that rounding: a workgroup sums its rows' columns in registers, and the
 // workgroups' partial rows are added in a fixed order by column_sum_kernel.
@@ -27,15 +27,37 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int n, int N, b
   }
 }
 
+// What rounding to T takes from v; nothing where that is infinite
+template <typename T>
+__device__ __forceinline__ float rest(float v) {
+  const float r = Piece<T>::round(v);
+  return fabsf(r) < INFINITY ? v - r : 0.f;
+}
+
 // Workgroup (x, y): columns 512 y .. 512 y + 511 (eight a lane) of rows 8 x .. 8 x + 7; wave w takes rows
 // w and w + 4.  The four waves' column sums meet in LDS.
-template <typename T, typename D, bool GATED>
+template <typename T, typename D, bool GATED, bool TWO>
 __global__ __launch_bounds__(kThreads) void dz_kernel(DzArgs a, int vec) {
   constexpr bool FAST = sizeof(T) == 2;
   constexpr int ROWS = kDzRows / 4;
   __shared__ float red[GATED ? 2 : 1][4][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = blockIdx.y * 512 + lane * 8;
+  if constexpr (TWO) {                               // workgroups behind dz's: x's rows, twice
+    const int dz_groups = ((GATED ? a.N : (int)a.ldz) + 511) / 512;
+    if ((int)blockIdx.y >= dz_groups) {
+      const int k = n - dz_groups * 512;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        const int64_t t = (int64_t)blockIdx.x * kDzRows + wave + 4 * r;
+        if (t >= a.T || k >= a.K) continue;
+        const i32x4 v = Piece<uint16_t>::raw(a.x, t * a.ldx + k);
+        *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(a.x2) + t * a.K + k) = v;
+        *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(a.x2) + (t + a.T) * a.K + k) = v;
+      }
+      return;
+    }
+  }
   const int width = GATED ? a.N : (int)a.ldz;        // columns written (with the pitch's zeros)
   float s0[8] = {}, s1[8] = {};
   if (n < width) {
@@ -70,6 +92,15 @@ __global__ __launch_bounds__(kThreads) void dz_kernel(DzArgs a, int vec) {
       if (a.dz) {
         Piece<T>::store(a.dz, t * a.ldz + n, d[r]);
         if constexpr (GATED) Piece<T>::store(a.dz, t * a.ldz + a.N + n, u[r]);
+        if constexpr (TWO) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            d[r][i] = rest<T>(d[r][i]);
+            if (GATED) u[r][i] = rest<T>(u[r][i]);
+          }
+          Piece<T>::store(a.dz, (t + a.T) * a.ldz + n, d[r]);
+          if constexpr (GATED) Piece<T>::store(a.dz, (t + a.T) * a.ldz + a.N + n, u[r]);
+        }
       }
     }
   }
@@ -121,12 +152,12 @@ __global__ __launch_bounds__(kThreads) void zero_bytes_kernel(uint8_t* p, int64_
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) p[i] = 0;
 }
 
-template <typename T, typename D>
+template <typename T, typename D, bool TWO>
 hipError_t launch(const DzArgs& a, int vec, hipStream_t s) {
   const int64_t width = a.gated ? a.N : a.ldz;
-  const dim3 grid((unsigned)dz_parts(a.T), (unsigned)((width + 511) / 512));
-  if (a.gated) hipLaunchKernelGGL((dz_kernel<T, T, true>), grid, dim3(kThreads), 0, s, a, vec);
-  else hipLaunchKernelGGL((dz_kernel<T, D, false>), grid, dim3(kThreads), 0, s, a, vec);
+  const dim3 grid((unsigned)dz_parts(a.T), (unsigned)((width + 511) / 512 + (TWO ? (a.K + 511) / 512 : 0)));
+  if (a.gated) hipLaunchKernelGGL((dz_kernel<T, T, true, TWO>), grid, dim3(kThreads), 0, s, a, vec);
+  else hipLaunchKernelGGL((dz_kernel<T, D, false, TWO>), grid, dim3(kThreads), 0, s, a, vec);
   return hipGetLastError();
 }
 
@@ -140,9 +171,10 @@ hipError_t launch_dz(const DzArgs& a, bool f32, hipStream_t s) {
   };
   const int esz = f32 ? 4 : 2;
   const int vec = ok(a.dy, a.ldy, a.dy_f32 ? 4 : esz) && (!a.pre || ok(a.pre, a.ldp, esz));
-  hipError_t err = f32         ? launch<float, float>(a, vec, s)
-                   : a.dy_f32 ? launch<uint16_t, float>(a, vec, s)
-                              : launch<uint16_t, uint16_t>(a, vec, s);
+  hipError_t err;
+  if (f32) err = launch<float, float, false>(a, vec, s);
+  else if (a.x2) err = a.dy_f32 ? launch<uint16_t, float, true>(a, vec, s) : launch<uint16_t, uint16_t, true>(a, vec, s);
+  else err = a.dy_f32 ? launch<uint16_t, float, false>(a, vec, s) : launch<uint16_t, uint16_t, false>(a, vec, s);
   if (err != hipSuccess || !a.dbias) return err;
   return launch_column_sum(a.part, dz_parts(a.T), a.gated ? 2 * (int64_t)a.N : a.N, a.dbias, f32, s);
 }

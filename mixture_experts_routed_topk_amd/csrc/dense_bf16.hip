@@ -271,14 +271,16 @@ hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t
   });
 }
 
-size_t dense_gradients_workspace(int64_t rows, int64_t N, int64_t cols, bool f32) {
+size_t dense_gradients_workspace(int64_t rows, int64_t N, int64_t cols, bool f32, bool two_parts) {
   if (rows == 0) return 0;
-  return f32 ? dense_gradients_f32_workspace(rows, N, cols) : gradients_part<uint16_t>(kPairs, kPairTiles, kPairJoin, rows, N, cols);
+  return f32 ? dense_gradients_f32_workspace(rows, N, cols)
+             : gradients_part<uint16_t>(kPairs, kPairTiles, kPairJoin, rows, N, cols, two_parts);
 }
 
-hipError_t launch_dense_gradients(const DenseGemm* dx, const DenseGemm* dw, void* ws, bool f32, hipStream_t s) {
+hipError_t launch_dense_gradients(const DenseGemm* dx, const DenseGemm* dw, void* ws, bool f32, bool two_parts,
+                                  hipStream_t s) {
   if (f32) return launch_dense_gradients_f32(dx, dw, ws, s);
-  return run_gradients<uint16_t>(kPairs, kPairTiles, kPairJoin, dx, dw, ws, s,
+  return run_gradients<uint16_t>(kPairs, kPairTiles, kPairJoin, dx, dw, two_parts, ws, s,
                                  [&](int pair, dim3 grid, const Job& x, const Job& w, int n_first, int dw_first) {
     if (pair == 0) hipLaunchKernelGGL((dense_pair_kernel<256, 256>), grid, dim3(512), 0, s, x, w, n_first, dw_first);
     else if (pair == 1) hipLaunchKernelGGL((dense_pair_kernel<128, 128>), grid, dim3(256), 0, s, x, w, n_first, dw_first);

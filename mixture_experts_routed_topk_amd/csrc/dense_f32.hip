@@ -56,11 +56,11 @@ hipError_t launch_dense_gemm_f32(const DenseGemm& g, void* ws, hipStream_t s) {
 }
 
 size_t dense_gradients_f32_workspace(int64_t rows, int64_t N, int64_t cols) {
-  return gradients_part<float>(kPairs, kPairTiles, kJoin, rows, N, cols);
+  return gradients_part<float>(kPairs, kPairTiles, kJoin, rows, N, cols, false);
 }
 
 hipError_t launch_dense_gradients_f32(const DenseGemm* dx, const DenseGemm* dw, void* ws, hipStream_t s) {
-  return run_gradients<float>(kPairs, kPairTiles, kJoin, dx, dw, ws, s,
+  return run_gradients<float>(kPairs, kPairTiles, kJoin, dx, dw, false, ws, s,
                               [&](int pair, dim3 grid, const Job& x, const Job& w, int n_first, int dw_first) {
     if (pair == 0) hipLaunchKernelGGL(dense_pair_f32_kernel<128>, grid, dim3(256), 0, s, x, w, n_first, dw_first);
     else if (pair == 1) hipLaunchKernelGGL(dense_pair_f32_kernel<64>, grid, dim3(256), 0, s, x, w, n_first, dw_first);

@@ -581,19 +581,19 @@ PairPlan plan_pair(const int (&pairs)[NP][2], const TileCost (&costs)[NT], JoinC
   }
   return best;
 }
-// bytes of the partial sums of product j
-inline size_t pair_part(const PairPlan& p, int j, int64_t M, int64_t N) {
-  return p.splits[j] > 1 ? ((size_t)p.splits[j] * M * N * 4 + 255) & ~size_t(255) : 0;
+// bytes of the partial sums of product j; two_parts: two rows of dx's product add up to one
+inline size_t pair_part(const PairPlan& p, int j, int64_t M, int64_t N, bool two_parts) {
+  return p.splits[j] > 1 || (two_parts && j == 0) ? ((size_t)p.splits[j] * M * N * 4 + 255) & ~size_t(255) : 0;
 }
 
 template <typename T, int NP, int NT>
 size_t gradients_part(const int (&pairs)[NP][2], const TileCost (&costs)[NT], JoinCost joint, int64_t rows, int64_t N,
-                      int64_t cols) {
+                      int64_t cols, bool two_parts) {
   size_t most = 0;
   for (int which = 1; which < 4; ++which) {        // dx, dw or both may be asked for
     const int64_t M[2] = {which & 1 ? rows : 0, which & 2 ? cols : 0}, K[2] = {cols, rows};
     const PairPlan p = plan_pair<T>(pairs, costs, joint, M, N, K);
-    const size_t need = pair_part(p, 0, M[0], N) + pair_part(p, 1, M[1], N);
+    const size_t need = pair_part(p, 0, M[0], N, two_parts) + pair_part(p, 1, M[1], N, two_parts);
     most = need > most ? need : most;
   }
   return most;
@@ -602,12 +602,12 @@ size_t gradients_part(const int (&pairs)[NP][2], const TileCost (&costs)[NT], Jo
 // Launches the gradients: tiles(pair, grid, dx, dw, n_first, dw_first) launches the pair kernel
 template <typename T, int NP, int NT, typename F>
 hipError_t run_gradients(const int (&pairs)[NP][2], const TileCost (&costs)[NT], JoinCost joint, const DenseGemm* dx,
-                         const DenseGemm* dw, void* ws, hipStream_t s, F&& tiles) {
+                         const DenseGemm* dw, bool two_parts, void* ws, hipStream_t s, F&& tiles) {
   const DenseGemm* g[2] = {dx, dw};
   const int64_t M[2] = {dx ? dx->M : 0, dw ? dw->M : 0}, K[2] = {dx ? dx->K : 0, dw ? dw->K : 0};
   const int64_t N = dx ? dx->e.N : dw->e.N;
   const PairPlan p = plan_pair<T>(pairs, costs, joint, M, N, K);
-  Job job[2] = {};
+  Job job[2] = {}, sum[2] = {};
   int blocks[2] = {}, join_blocks[2] = {};
   size_t at = 0;
   for (int j = 0; j < 2; ++j) {
@@ -621,18 +621,21 @@ hipError_t run_gradients(const int (&pairs)[NP][2], const TileCost (&costs)[NT],
     q.mt = (int)((M[j] + c.rows - 1) / c.rows);
     q.nt = (int)((N + c.cols - 1) / c.cols);
     blocks[j] = (q.mt * q.nt + 7) / 8 * 8 * q.splits;
-    if (q.splits > 1) {
+    const bool halve = two_parts && j == 0;
+    if (q.splits > 1 || halve) {
       q.part = reinterpret_cast<float*>(static_cast<char*>(ws) + at);
       q.ldpart = N;
-      at += pair_part(p, j, M[j], N);
-      join_blocks[j] = (int)((M[j] * (N / 8) + 255) / 256);
+      at += pair_part(p, j, M[j], N, two_parts);
+      sum[j] = q;
+      if (halve) sum[j].g.M /= 2, sum[j].splits *= 2;      // (a split's second T rows follow its first)
+      join_blocks[j] = (int)((sum[j].g.M * (N / 8) + 255) / 256);
     }
   }
   const int dw_first = !dx || (dw && p.slices[1] > p.slices[0]);
   hipError_t err = tiles(p.tiles, dim3((unsigned)(blocks[0] + blocks[1])), job[0], job[1], blocks[dw_first], dw_first);
   if (err != hipSuccess || !(join_blocks[0] + join_blocks[1])) return err;
-  hipLaunchKernelGGL(dense_join_pair_kernel<T>, dim3((unsigned)(join_blocks[0] + join_blocks[1])), dim3(256), 0, s, job[0],
-                     job[1], join_blocks[0]);
+  hipLaunchKernelGGL(dense_join_pair_kernel<T>, dim3((unsigned)(join_blocks[0] + join_blocks[1])), dim3(256), 0, s, sum[0],
+                     sum[1], join_blocks[0]);
   return hipGetLastError();
 }
 

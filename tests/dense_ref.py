@@ -90,14 +90,15 @@ def dz_gated(da, pre, name):
             torch.cat([(da * u).abs() * e + 4 * U32 * dg.abs(), da.abs() * e + 4 * U32 * du.abs()], 1))
 
 
-def backward(dz, edz, x, w, dtype):
-    """((dx, bound), (dw, bound), (db, bound)): the products take dz rounded to dtype."""
+def backward(dz, edz, x, w, dtype, two_parts=False):
+    """((dx, bound), (dw, bound), (db, bound)): the products take dz rounded to dtype, or in two_parts, the second
+    being what that rounding took, rounded in its turn."""
     x, w = x.double(), w.double()
-    er = edz + HALF[dtype] * (dz.abs() + edz)          # the rounded dz's error
+    er = edz + HALF[dtype] ** (2 if two_parts else 1) * (dz.abs() + edz)          # the rounded dz's error
     out = []
     for r, e, c in ((dz, er, w.t()), (dz.t(), er.t(), x.t())):
         p, ep = product(r, c)
-        ep = ep * (1 + HALF[dtype]) + e @ c.abs().t()
+        ep = ep * (1 + HALF[dtype]) * (2 if two_parts else 1) + e @ c.abs().t()      # (two parts: twice the terms)
         out.append((p, ep + HALF[dtype] * (p.abs() + ep)))
     db = dz.sum(0)
     eb = edz.sum(0) + (dz.shape[0] + 1) * U32 * dz.abs().sum(0)

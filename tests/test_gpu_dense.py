@@ -1,6 +1,7 @@
 """The dense operators around the routed experts (RMS norm, linear, gated projection) against
 their 64-bit plain forms (dense_ref.py, whose bounds are derived there), forward and backward."""
 
+import ctypes
 import zlib
 
 import pytest
@@ -313,3 +314,49 @@ def test_half_tiles_gated():
     (ra, ba), (rz, bz) = ref.gated(x, w, b, "silu", BF16)
     ref.check(a, ra, ba, "a")
     ref.check(pre, rz, bz, "pre")
+
+
+# ----------------------------------------------------------------------------- few rows: dz in two bf16 parts
+
+@pytest.mark.parametrize("need", ["dx", "dw", "both"])
+@pytest.mark.parametrize("T,K,N", [(1, 8, 1), (2, 2048, 104), (3, 520, 257), (7, 1032, 2056), (8, 4104, 40), (16, 1408, 2048),
+                                   (32, 2048, 520)])
+def test_few_rows_gradients_keep_dz(T, K, N, need):
+    x, w = rnd("fx", (T, K), BF16, pad=8 * (T % 2)), rnd("fw", (N, K), BF16, K ** -0.5)
+    for name, odt in (("silu", BF16), ("gelu", F32), ("none", F32)):
+        dy, pre = rnd("fdy", (T, N), odt), rnd("fz", (T, N), BF16, 1.5) if name != "none" else None
+        grads = ref.backward(*ref.dz_linear(dy, pre, name), x, w, BF16, two_parts=True)
+        prob = m.LinearProblem(T, K, N, m.BF16, m.F32 if odt is F32 else m.BF16, ACT[name], x.stride(0), 0, 0, 0, 0)
+        n = ctypes.c_size_t(0)
+        assert m.lib().moe_linear_workspace_size(ctypes.byref(prob), 1, ctypes.byref(n)) == 0
+        ws = torch.full((n.value,), 255, dtype=torch.uint8, device="cuda")      # NaN in every type
+        dx = torch.empty((T, K), dtype=BF16, device="cuda") if need != "dw" else None
+        dw = torch.empty((N, K), dtype=BF16, device="cuda") if need != "dx" else None
+        at = lambda t: None if t is None else t.data_ptr()          # noqa: E731
+        assert m.lib().moe_linear_backward(
+            ctypes.byref(prob), dy.data_ptr(), x.data_ptr(), w.data_ptr(), at(pre), at(dx), at(dw), None, ws.data_ptr(),
+            n.value, torch.cuda.current_stream().cuda_stream) == 0
+        for got, (r, b), what in zip((dx, dw), grads, ("dx", "dw")):
+            if got is not None:
+                ref.check(got, r, b, f"{what} {name}")
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 64, 8), (2, 4760, 104), (9, 136, 1408), (32, 2048, 360)])
+def test_few_rows_gated_gradients_keep_dz(T, H, I):
+    x, w = rnd("gx", (T, H), BF16), rnd("gw", (2 * I, H), BF16, H ** -0.5)
+    da, pre = rnd("gda", (T, I), BF16), rnd("gz", (T, 2 * I), BF16, 1.5)
+    dx, dw, db = m.gated_linear_backward(da, x, w, pre, need_bias=True)
+    grads = ref.backward(*ref.dz_gated(da, pre, "silu"), x, w, BF16, two_parts=True)
+    for got, (r, b), what in zip((dx, dw, db), grads, ("dx", "dw", "db")):
+        ref.check(got, r, b, what)
+
+
+def test_few_rows_infinite_dz():
+    """A dz that bf16 cannot hold is infinite, as with many rows, and no NaN comes of its second part."""
+    T, K, N = 3, 64, 40
+    x, w = torch.ones((T, K), dtype=BF16, device="cuda"), torch.ones((N, K), dtype=BF16, device="cuda")
+    dy = torch.ones((T, N), dtype=F32, device="cuda")
+    dy[1, 2] = 3.4e38          # finite in float32, past bf16's largest value
+    dx, dw, _ = m.linear_backward(dy, x, w)
+    assert torch.isposinf(dx[1]).all() and torch.isposinf(dw[2]).all()
+    assert (dx[[0, 2]] == N).all() and (dw[[0, 1, 3, 39]] == T).all()
