@@ -27,6 +27,13 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, int n, int N, b
   }
 }
 
+// Two bf16 values with those that are not finite replaced by zero
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+  if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+  if ((v & 0x7f800000u) == 0x7f800000u) v &= 0xffffu;
+  return v;
+}
+
 // What rounding to T takes from v; nothing where that is infinite
 template <typename T>
 __device__ __forceinline__ float rest(float v) {
@@ -43,7 +50,7 @@ __global__ __launch_bounds__(kThreads) void dz_kernel(DzArgs a, int vec) {
   __shared__ float red[GATED ? 2 : 1][4][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = blockIdx.y * 512 + lane * 8;
-  if constexpr (TWO) {                               // workgroups behind dz's: x's rows, twice
+  if constexpr (TWO) {                               // workgroups behind dz's: x's rows, then their finite values
     const int dz_groups = ((GATED ? a.N : (int)a.ldz) + 511) / 512;
     if ((int)blockIdx.y >= dz_groups) {
       const int k = n - dz_groups * 512;
@@ -51,8 +58,11 @@ __global__ __launch_bounds__(kThreads) void dz_kernel(DzArgs a, int vec) {
       for (int r = 0; r < ROWS; ++r) {
         const int64_t t = (int64_t)blockIdx.x * kDzRows + wave + 4 * r;
         if (t >= a.T || k >= a.K) continue;
-        const i32x4 v = Piece<uint16_t>::raw(a.x, t * a.ldx + k);
+        i32x4 v = Piece<uint16_t>::raw(a.x, t * a.ldx + k);
         *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(a.x2) + t * a.K + k) = v;
+        // (an infinity times dz's first part is the result; times the second it could make that NaN)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (int)finite_bf16x2((uint32_t)v[i]);
         *reinterpret_cast<i32x4*>(static_cast<uint16_t*>(a.x2) + (t + a.T) * a.K + k) = v;
       }
       return;

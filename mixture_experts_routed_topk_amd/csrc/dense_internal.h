@@ -79,7 +79,8 @@ hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t
 // The gradients dx [T][N] = dz w (c stored along its rows) and dw [cols][N] = dz^T x (both stored along
 // their rows), dz [T][cols]; either may be null.  Outputs in the operands' type, no epilogue.
 // two_parts (bf16): dz and x are 2 T rows, dz's second T what rounding took from its first and x's the
-// first again; so dw is over all of dz as it is, and a row of dx is the sum of two of dx's 2 T.
+// first again with zeros for what is not finite; so dw is over all of dz as it is, and a row of dx is the sum of two of
+// dx's 2 T, or the first of them where that is not finite.
 size_t dense_gradients_workspace(int64_t rows, int64_t N, int64_t cols, bool f32, bool two_parts);
 hipError_t launch_dense_gradients(const DenseGemm* dx, const DenseGemm* dw, void* ws, bool f32, bool two_parts, hipStream_t s);
 
@@ -109,7 +110,7 @@ struct DzArgs {
   void* dz;                     // may be null: column sums only
   int64_t ldz;
   const void* x;                // with x2: dz is written in two parts (row t and row T + t), and x
-  int64_t ldx;                  // [T][K] to both halves of x2 [2T][K]
+  int64_t ldx;                  // [T][K] to both halves of x2 [2T][K], in the second with zeros for infinities and NaN
   void* x2;
   int K;
   float* part;                  // [dz_parts(T)][cols], null without dbias

@@ -193,6 +193,7 @@ struct Job {
   int crows;           // rows of c (gated: 2 I)
   float* part;         // [splits][M][ldpart] partial sums (splits > 1)
   int64_t ldpart;
+  int second_parts;    // the join: odd partial sums come from dz's second part
 };
 
 // This lane's DMA sources for NI instructions (first, first + 1, ...) of one region whose
@@ -422,6 +423,10 @@ __device__ __forceinline__ void join(const Job& job, int64_t i) {
     float v[8];
     const int64_t at = ((int64_t)s * job.g.M + m) * job.ldpart + n;
     Piece<float>::load(job.part, at, v);
+    if (!GATED && job.second_parts && (s & 1)) {   // (where the first part gave no finite sum, that is the result)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = fabsf(z[j]) < INFINITY ? v[j] : 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] += v[j];
     if constexpr (GATED) {
@@ -627,7 +632,7 @@ hipError_t run_gradients(const int (&pairs)[NP][2], const TileCost (&costs)[NT],
       q.ldpart = N;
       at += pair_part(p, j, M[j], N, two_parts);
       sum[j] = q;
-      if (halve) sum[j].g.M /= 2, sum[j].splits *= 2;      // (a split's second T rows follow its first)
+      if (halve) sum[j].g.M /= 2, sum[j].splits *= 2, sum[j].second_parts = 1;      // (a split's second T rows follow its first)
       join_blocks[j] = (int)((sum[j].g.M * (N / 8) + 255) / 256);
     }
   }
