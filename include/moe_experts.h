@@ -433,9 +433,9 @@ moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w,
 /*
  * Gradients of moe_linear:  dz = dy * act'(pre);  dx = dz w;  dw = dz^T x;  dbias = sum_t dz.
  * (The gradient of the residual is dy itself.)  relu'(0) = 0.  The two products take dz
- * rounded to dtype, with at most 32 rows in two such parts (16 bits of it; where the first part's sum is not
- * finite it is the result, so infinities and NaN come out as with more rows); dbias sums it in float32 before
- * that rounding.
+ * rounded to dtype; with at most 32 rows, and unless it is a bf16 value already, in two such parts (16
+ * bits of it; where the first part's sum is not finite it is the result, so infinities and NaN come out as with
+ * more rows).  dbias sums it in float32 before that rounding.
  *
  *   dy [T, N], x [T, K], w [N, K]; pre [T, N] (not read, may be NULL, with MOE_ACT_NONE)
  *   dx [T, K], dw [N, K], dbias [N] out; each may be NULL, and then is not computed, and

@@ -94,7 +94,9 @@ bool dz_is_dy(const Backward& b) {
 // 2048 x 1408: 19.6 against 15.9 us, 7168 x 2048: 37.6 against 34.6).
 constexpr int64_t kTwoPartRows = 32;
 bool dz_in_two_parts(const Backward& b) {
-  return b.dtype == MOE_BF16 && b.T <= kTwoPartRows && (b.act != MOE_ACT_NONE || b.dy_dtype == MOE_F32);
+  // (a bf16 dy that relu's slope only keeps or drops is a bf16 dz already)
+  const bool exact = b.dy_dtype == MOE_BF16 && !b.gated && (b.act == MOE_ACT_NONE || b.act == MOE_ACT_RELU);
+  return b.dtype == MOE_BF16 && b.T <= kTwoPartRows && !exact;
 }
 int64_t dz_pitch(const Backward& b) { return (b.cols + 7) / 8 * 8; }
 

@@ -1,0 +1,22 @@
+"""Host-side behaviour of the dense operators: workspaces, plans and the binding's conversions (no HIP call is reached)."""
+
+import pytest
+
+import mixture_experts_routed_topk_amd as m
+from test_dense_abi_cpu import L, gated, linear, size
+
+
+@pytest.mark.parametrize("T", [1, 16, 32])
+def test_few_rows_take_a_second_part_only_where_dz_has_one(T):
+    """At most 32 bf16 rows take dz in two parts, and x twice, unless dz is a bf16 value exactly: dy itself,
+    or what relu keeps of a bf16 dy."""
+    K, N = 2048, 64
+
+    def need(**kw):
+        return size(L.moe_linear_workspace_size, linear(T=T, K=K, N=N, **kw), 1)[1]
+
+    x2 = 2 * T * K * 2                                     # x's copies
+    two = need(act=m.ACT_SILU)
+    assert need(act=m.ACT_RELU) + x2 <= two and need(act=m.ACT_NONE) + x2 <= two
+    assert need(act=m.ACT_RELU, out_dtype=m.F32) == need(act=m.ACT_NONE, out_dtype=m.F32) == two
+    assert size(L.moe_gated_linear_workspace_size, gated(T=T, H=K, I=N, act=m.ACT_RELU), 1)[1] > x2
