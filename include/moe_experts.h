@@ -371,8 +371,8 @@ typedef struct {
  *   h = x + residual, rounded to dtype (h = x without a residual);
  *   rstd = 1 / sqrt(mean_j h_j^2 + eps);   y_j = h_j * rstd * weight_j.
  * The 8-bit output takes the same y in float32, before any rounding, by the rule of
- * moe_quantize_rows_fp8 (scale amax / 448 per 128 columns, 1 for an all-zero group): the rows
- * moe_experts_forward_quantized takes.
+ * moe_quantize_rows_fp8 (scale amax / 448 per 128 columns, 1 for a group where that is zero; codes
+ * saturate at 448): the rows moe_experts_forward_quantized takes.
  *
  *   x [T, H], residual [T, H] or NULL, weight [H]
  *   y [T, H] out, or NULL when q is wanted alone;  rstd [T] float32 out

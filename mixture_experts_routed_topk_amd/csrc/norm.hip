@@ -98,27 +98,32 @@ __global__ __launch_bounds__(block_threads<WPR>()) void rms_norm_kernel(NormArgs
         for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 16));
-        const float s = amax > 0.f ? amax / 448.0f : 1.0f;
+        const float s0 = amax / 448.0f, s = s0 > 0.f ? s0 : 1.0f;
+        uint32_t lo = 0, hi = 0;
         // v / s from one reciprocal: the quotient's error is taken back once, which rounds as the
         // division does (eight IEEE divisions and the e4m3 rounding in integer steps take as long as
         // the row's memory traffic)
-        float d[8];
-        if (s > 0x1p-96f && s < 0x1p96f) {
+        if (s0 > 0x1p-96f && s0 < 0x1p96f) {   // (a NaN keeps its sign in its code)
           const float inv = 1.0f / s;
+          float d[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float quo = v[i][j] * inv;
             d[j] = fmaf(fmaf(-quo, s, v[i][j]), inv, quo);
           }
-        } else {   // (1 / s or the correction may leave float32's range)
+          lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], lo, false);
+          lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], lo, true);
+          hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[4], d[5], hi, false);
+          hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[6], d[7], hi, true);
+        } else {
+          // 1 / s or the correction may leave float32's range; and a scale of few bits may lie so far below
+          // amax / 448 that a value passes 464 times it, where the conversion gives NaN and the rule saturates
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = v[i][j] / s;
+          for (int j = 0; j < 4; ++j) {
+            lo |= f32_to_e4m3(v[i][j] / s) << (8 * j);
+            hi |= f32_to_e4m3(v[i][4 + j] / s) << (8 * j);
+          }
         }
-        uint32_t lo = 0, hi = 0;
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], lo, false);
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], lo, true);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[4], d[5], hi, false);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[6], d[7], hi, true);
         *reinterpret_cast<uint2*>(a.q + row * a.H + p * 8) = make_uint2(lo, hi);
         if ((lane & 15) == 0) a.q_scale[row * (a.H / 128) + p / 16] = s;
       }

@@ -13,6 +13,11 @@ pytestmark = pytest.mark.gpu
 INF, NAN = float("inf"), float("nan")
 
 
+def same(a, b):
+    """torch.equal as a plain bool (a failure then prints no tensors)"""
+    return bool(torch.equal(a, b))
+
+
 def check_special(got, want, bound, what):
     """Infinities (by sign) and NaN in the same places as in `want`, the rest within `bound`."""
     got = got.double()
@@ -60,3 +65,56 @@ def test_gradients_with_infinite_operands(T, K, N, kind, name, odt):
     if name != "relu":     # (the case is what it says: one infinity in a column's sums leaves no NaN; relu's zeros do)
         assert not torch.isnan(want[0][0][:, 3]).any() and torch.isinf(want[0][0][:, 3]).all()
         assert not torch.isnan(want[1][0][:, 5]).any() and torch.isinf(want[1][0][:, 5]).all()
+
+
+# ----------------------------------------------------------------------------- the norm's e4m3 codes
+
+def rule(y):
+    """moe_quantize_rows_fp8's rule on float32 values [T, H], evaluated on the host: (codes, scales)."""
+    g = y.float().cpu().view(y.shape[0], -1, 128)
+    amax = torch.where(torch.isnan(g), torch.zeros_like(g), g.abs()).amax(2, keepdim=True)
+    s = amax / torch.tensor(448.0)
+    s = torch.where(s > 0, s, torch.ones_like(s))
+    v = g / s
+    code = v.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    code = torch.where(torch.isnan(v), torch.full_like(code, 0x7F), code)
+    return code.view(y.shape).cuda(), s[:, :, 0].cuda()
+
+
+@pytest.mark.parametrize("H", [256, 2176])
+def test_norm_codes_of_groups_whose_scale_has_few_bits(H):
+    """Channels so small beside their row's norm that amax / 448 keeps few of float32's bits, one bit or none: rounding
+    the scale can put a value past 448 times it, which saturates, and a group whose scale would be zero has scale 1."""
+    T = 150
+    x, w = rnd("qx", (T, H), BF16, 2.0), torch.ones(H, dtype=BF16, device="cuda")
+    x[:, :128] = rnd("qsmall", (T, 128), BF16) * 2.0 ** -4
+    x[:, :128] *= (2.0 ** -(torch.arange(T, device="cuda") % 15)).to(BF16)[:, None]
+    w[:128] = 2.0 ** -133                                 # bf16's smallest value
+    x[7, :128], x[8, 3] = 0, 0
+    q, s, _, h, rstd = m.rms_norm_fp8(x, w, 1e-6)
+    y = (x.float().cpu() * rstd.cpu()[:, None]) * w.float().cpu()
+    rq, rs = rule(y)
+    few = (rs[:, 0] < 16 * 2.0 ** -149).sum().item()      # (the case is what it says)
+    assert few > T // 4 and (rs[:, 0] == 1).sum().item() > T // 8
+    assert same(s, rs) and same(q, rq)
+    assert torch.isfinite(q.view(torch.float8_e4m3fn).float()).all()
+
+
+def test_norm_codes_of_infinities_and_nan():
+    """Rows of +-1 leave the weight itself as the norm's result: its codes are those of moe_quantize_rows_fp8, with
+    infinities and NaN of either sign among them and in rows whose norm is not finite (a NaN's code is 0x7f or 0xff)."""
+    def codes(q):
+        return torch.where(q == 0xFF, 0x7F, q)
+    T, H = 40, 512
+    x = torch.where(rnd("ix", (T, H), F32) > 0, 1.0, -1.0).to(BF16)
+    w = rnd("iw", (H,), BF16)
+    w[5], w[130], w[131], w[300], w[301] = NAN, INF, 2.0, -NAN, -INF
+    w[384:] = NAN
+    q, s, y, *_ = m.rms_norm_fp8(x, w, 0.0, with_y=True)
+    want, ws = m.quantize_rows_fp8((x * w).contiguous())
+    assert same(s, ws) and same(codes(q), want)
+    x[3, 9], x[4, 200], x[5, 500] = NAN, INF, -INF
+    q, s, y, h, rstd = m.rms_norm_fp8(x, rnd("iw", (H,), BF16), 0.0, with_y=True)
+    rq, rs = rule((x.float() * rstd[:, None]) * rnd("iw", (H,), BF16).float())
+    assert same(s, rs) and same(codes(q), rq)
+    assert not torch.isfinite(q[3].view(torch.float8_e4m3fn).float()).any()
