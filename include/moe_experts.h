@@ -432,7 +432,8 @@ moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w,
 
 /*
  * Gradients of moe_linear:  dz = dy * act'(pre);  dx = dz w;  dw = dz^T x;  dbias = sum_t dz.
- * (The gradient of the residual is dy itself.)  relu'(0) = 0.  The two products take dz
+ * (The gradient of the residual is dy itself.)  relu'(0) = 0, and where pre <= 0 relu's dz is 0 whatever dy is;
+ * relu of NaN is NaN, and so is its slope.  The two products take dz
  * rounded to dtype; with at most 32 rows, and unless it is a bf16 value already, in two such parts (16
  * bits of it; where the first part's sum is not finite it is the result, so infinities and NaN come out as with
  * more rows).  dbias sums it in float32 before that rounding.

@@ -89,13 +89,14 @@ __global__ __launch_bounds__(kThreads) void dz_kernel(DzArgs a, int vec) {
         for (int i = 0; i < 8; ++i) {
           const ActPair p = act_pair<FAST>(a.act, z[r][i]);
           const float da = d[r][i];
-          d[r][i] = da * u[r][i] * p.slope;
+          d[r][i] = times_slope(a.act, da * u[r][i], p.slope);
           u[r][i] = da * p.value;
           s1[i] += u[r][i];
         }
       } else if (a.pre) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[r][i] = n + i < a.N ? d[r][i] * act_pair<FAST>(a.act, z[r][i]).slope : 0.f;
+        for (int i = 0; i < 8; ++i)
+          d[r][i] = n + i < a.N ? times_slope(a.act, d[r][i], act_pair<FAST>(a.act, z[r][i]).slope) : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) s0[i] += d[r][i];

@@ -93,6 +93,7 @@ template <bool FAST>
 __device__ __forceinline__ float act_fn(int act, float z) {
   if (act == kActNone) return z;
   if (FAST && act == kActGelu) return z * gauss_fast(z).cdf;
+  if (act == kActRelu) return z <= 0.0f ? 0.0f : z;   // (NaN stays NaN, as in the other activations)
   return gate_fn<FAST>(act - kActSilu + kGateSilu, z);
 }
 static_assert(kActGelu - kActSilu + kGateSilu == kGateGelu && kActRelu - kActSilu + kGateSilu == kGateRelu,
@@ -130,8 +131,12 @@ __device__ __forceinline__ ActPair act_pair(int act, float z) {
     const float cdf = 0.5f * erfcf(-0.70710678118654752f * z);
     return {z * cdf, cdf + z * (0.39894228040143268f * expf(-0.5f * z * z))};
   }
-  if (act == kActRelu) return {z > 0.0f ? z : 0.0f, z > 0.0f ? 1.0f : 0.0f};
+  if (act == kActRelu) return {z <= 0.0f ? 0.0f : z, z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z)};
   return {z, 1.0f};
+}
+// d act'(z): where relu is closed nothing, whatever d holds
+__device__ __forceinline__ float times_slope(int act, float d, float slope) {
+  return act == kActRelu && slope == 0.0f ? 0.0f : d * slope;
 }
 
 // ---------------------------------------------------------------------------- element store

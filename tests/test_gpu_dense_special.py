@@ -118,3 +118,61 @@ def test_norm_codes_of_infinities_and_nan():
     rq, rs = rule((x.float() * rstd[:, None]) * rnd("iw", (H,), BF16).float())
     assert same(s, rs) and same(codes(q), rq)
     assert not torch.isfinite(q[3].view(torch.float8_e4m3fn).float()).any()
+
+
+# ----------------------------------------------------------------------------- activations
+
+def relu(z):
+    return torch.where(z <= 0, 0.0, z)
+
+
+@pytest.mark.parametrize("T,K,N", [(3, 72, 41), (20, 2048, 264), (70, 200, 264), (300, 136, 521), (2100, 328, 1032)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name", ref.ACTS)
+def test_nan_rows_stay_nan(T, K, N, dtype, name):
+    """A NaN in a row of x is in every output of that row, whatever the activation, and in no other row."""
+    x, w, b = rnd("nx", (T, K), dtype), rnd("nw", (N, K), dtype, K ** -0.5), rnd("nb", (N,), dtype)
+    clean = m.linear(x, w, b, act=ACT[name])[0]
+    x[T // 2, K - 1] = NAN
+    y, pre = m.linear(x, w, b, act=ACT[name], save_pre=True)
+    rows = torch.arange(T, device="cuda") != T // 2
+    assert torch.isnan(y[T // 2]).all() and torch.isnan(pre[T // 2]).all()
+    assert torch.equal(y[rows], clean[rows])
+    if name != "none" and N % 16 == 8:
+        g = torch.cat([w, w])
+        a, _ = m.gated_linear(x, g, act=ACT[name])
+        assert torch.isnan(a[T // 2]).all() and torch.isfinite(a[rows]).all()
+
+
+@pytest.mark.parametrize("dtype,odt", [(BF16, BF16), (BF16, F32), (F32, F32)], ids=["bf16", "bf16_f32", "f32"])
+@pytest.mark.parametrize("T,K,N", [(3, 72, 41), (40, 136, 264)])
+def test_relu_gradient_of_special_values(T, K, N, dtype, odt):
+    """dz is dy where pre > 0, 0 where pre <= 0 whatever dy is, and NaN where pre is NaN."""
+    x, w = rnd("rx", (T, K), dtype), rnd("rw", (N, K), dtype, K ** -0.5)
+    dy, pre = rnd("rdy", (T, N), odt), rnd("rz", (T, N), dtype)
+    pre[0, 0], pre[0, 1], pre[0, 2], pre[1, 3], pre[1, 4] = -1.0, 0.0, -INF, 1.0, INF
+    dy[0, 0], dy[0, 1], dy[0, 2], dy[1, 3] = INF, NAN, -INF, -INF
+    dx, dw, db = m.linear_backward(dy, x, w, pre=pre, act=m.ACT_RELU, need_bias=True)
+    dz = torch.where(pre.double() > 0, dy.double(), 0.0)
+    for got, (r, b), what in zip((dx, dw, db), ref.backward(dz, torch.zeros_like(dz), x, w, dtype), ("dx", "dw", "db")):
+        check_special(got, r, b, what)
+    assert torch.isfinite(dx[0]).all() and torch.isfinite(dw[:3]).all() and not torch.isfinite(dx[1]).any()
+    pre[2, 5] = NAN
+    dx, dw, db = m.linear_backward(dy, x, w, pre=pre, act=m.ACT_RELU, need_bias=True)
+    assert torch.isnan(dx[2]).all() and torch.isnan(dw[5]).all() and torch.isnan(db[5])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H,I", [(3, 72, 40), (40, 136, 264)])
+def test_gated_relu_gradient_of_special_values(T, H, I, dtype):
+    x, w = rnd("gx", (T, H), dtype), rnd("gw", (2 * I, H), dtype, H ** -0.5)
+    da, pre = rnd("gda", (T, I), dtype), rnd("gz", (T, 2 * I), dtype)
+    pre[0, 0], pre[0, I] = -1.0, INF                 # up infinite behind a closed gate: no gradient for the gate
+    pre[1, 1], pre[1, I + 1] = 2.0, -INF             # behind an open one an infinite one
+    dx, dw, db = m.gated_linear_backward(da, x, w, pre, m.ACT_RELU, need_bias=True)
+    g, u = pre.double().chunk(2, 1)
+    dz = torch.cat([torch.where(g > 0, da.double() * u, 0.0), da.double() * relu(g)], 1)
+    grads = ref.backward(dz, 4 * ref.U32 * dz.abs(), x, w, dtype, two_parts=T <= 32 and dtype is BF16)
+    for got, (r, b), what in zip((dx, dw, db), grads, ("dx", "dw", "db")):
+        check_special(got, r, b, what)
+    assert torch.isfinite(dx[0]).all() and not torch.isfinite(dx[1]).any()
