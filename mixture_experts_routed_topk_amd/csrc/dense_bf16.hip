@@ -266,6 +266,7 @@ hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t
   return run_forward<uint16_t>(g, p, p.tile == 256 ? 256 : 128, ws, s, [&](const Job& job, int epi) {
     if (epi == kPartial) launch_tiles<kPartial>(job, p.tile, s);
     else if (epi == kGated) launch_tiles<kGated>(job, p.tile, s);
+    else if (epi == kLinearWide) launch_tiles<kLinearWide>(job, p.tile, s);
     else launch_tiles<kLinear>(job, p.tile, s);
     return hipGetLastError();
   });

@@ -62,54 +62,58 @@ struct Piece<uint16_t> {   // bf16 bits
 };
 
 // ---------------------------------------------------------------------------- activations
-// Gauss tail of the normal distribution and its density for results that are rounded to bf16:
-// for |z| with x = |z| / sqrt 2, erfc(x) = e^(-x^2) erfcx(x) and erfcx(x) = t p(t), t = 1 / (1 +
-// 0.455 x), p a polynomial of degree 7 fitted here in the minimax sense to the relative error
-// (5.1e-7 for x >= 0; in float32 Phi is off by 4.0e-7, and by 4.4e-6 of itself at z = -12).  One
-// exponential serves Phi and the density.  (erfcf and expf: 45 us of vector work in the
-// backward pass of 2731 x 5632 elements.)
+// Gauss tail of the normal distribution and its density: for |z| with x = |z| / sqrt 2, erfc(x) =
+// e^(-x^2) erfcx(x) and erfcx(x) = t p(t), t = 1 / (1 + c x), p a polynomial fitted here in the minimax
+// sense to the relative error.  For results rounded to bf16, degree 7 with c = 0.455 (5.1e-7 for x >= 0; in float32
+// Phi is off by 4.0e-7, and by 4.4e-6 of itself at z = -12); for float32 results (WIDE), degree 9 with
+// c = 0.44 (2.6e-8; in float32 Phi is off by at most 7e-7 + 1.2e-7 z^2 of itself).  One exponential serves Phi and the
+// density.  (erfcf and expf: 45 us of vector work in the backward pass of 2731 x 5632 elements.)
 struct Gauss {
   float cdf;       // Phi(z)
   float density;   // phi(z)
 };
-__device__ __forceinline__ Gauss gauss_fast(float z) {
+template <bool WIDE>
+__device__ __forceinline__ Gauss gauss(float z) {
+  constexpr float wide[10] = {-0.039485052f, 0.19474044f,  -0.33856088f, 0.20246184f, -0.047061890f,
+                              0.13442233f,   0.17246558f, 0.22454564f,  0.24822831f, 0.24824367f};
+  constexpr float narrow[8] = {0.068594001f, -0.23870015f, 0.19744349f, 0.038967494f,
+                               0.19179685f,  0.22839320f,  0.25680113f, 0.25670451f};
+  constexpr int n = WIDE ? 10 : 8;
   const float e = __expf(-0.5f * z * z);
-  const float t = __builtin_amdgcn_rcpf(1.0f + (0.455f * 0.70710678118654752f) * fabsf(z));
-  float p = 0.068594001f;
-  p = p * t - 0.23870015f;
-  p = p * t + 0.19744349f;
-  p = p * t + 0.038967494f;
-  p = p * t + 0.19179685f;
-  p = p * t + 0.22839320f;
-  p = p * t + 0.25680113f;
-  p = p * t + 0.25670451f;
+  const float t = __builtin_amdgcn_rcpf(1.0f + ((WIDE ? 0.44f : 0.455f) * 0.70710678118654752f) * fabsf(z));
+  float p = WIDE ? wide[0] : narrow[0];
+#pragma unroll
+  for (int i = 1; i < n; ++i) p = p * t + (WIDE ? wide[i] : narrow[i % 8]);
   const float tail = 0.5f * p * t * e;
   return {z < 0.f ? tail : 1.0f - tail, 0.39894228040143268f * e};
 }
 
-// act(z) and its slope.  FAST, for results rounded to bf16: silu on the hardware exp and
-// reciprocal (as in gate_fn), gelu by gauss_fast.
-template <bool FAST>
+// How an activation is computed.  kActBf16, for results rounded to bf16 (dz among them; dbias is rounded to bf16 after
+// its sum): silu on the hardware exp and reciprocal (as in gate_fn), gelu by gauss.  kActWide, for float32
+// results of bf16 operands: silu by exp and a division, gelu by the longer gauss.  kActF32: float32 operands.
+enum ActKind { kActBf16, kActWide, kActF32 };
+template <ActKind KIND>
 __device__ __forceinline__ float act_fn(int act, float z) {
+  constexpr bool FAST = KIND == kActBf16;
   if (act == kActNone) return z;
-  if (FAST && act == kActGelu) return z * gauss_fast(z).cdf;
+  if (KIND != kActF32 && act == kActGelu) return z * gauss<KIND == kActWide>(z).cdf;
   if (act == kActRelu) return z <= 0.0f ? 0.0f : z;   // (NaN stays NaN, as in the other activations)
   return gate_fn<FAST>(act - kActSilu + kGateSilu, z);
 }
 static_assert(kActGelu - kActSilu + kGateSilu == kGateGelu && kActRelu - kActSilu + kGateSilu == kGateRelu,
               "activations keep the gates' order");
 
-template <bool FAST>
+template <ActKind KIND>
 __device__ __forceinline__ void act8(int act, float z[8]) {
   if (act == kActSilu) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_fn<FAST>(kActSilu, z[i]);
+    for (int i = 0; i < 8; ++i) z[i] = act_fn<KIND>(kActSilu, z[i]);
   } else if (act == kActGelu) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_fn<FAST>(kActGelu, z[i]);
+    for (int i = 0; i < 8; ++i) z[i] = act_fn<KIND>(kActGelu, z[i]);
   } else if (act == kActRelu) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = act_fn<FAST>(kActRelu, z[i]);
+    for (int i = 0; i < 8; ++i) z[i] = act_fn<KIND>(kActRelu, z[i]);
   }
 }
 
@@ -125,7 +129,7 @@ __device__ __forceinline__ ActPair act_pair(int act, float z) {
   }
   if (act == kActGelu) {   // z Phi(z) and Phi(z) + z phi(z)
     if (FAST) {
-      const Gauss g = gauss_fast(z);
+      const Gauss g = gauss<false>(z);
       return {z * g.cdf, g.cdf + z * g.density};
     }
     const float cdf = 0.5f * erfcf(-0.70710678118654752f * z);
@@ -166,8 +170,8 @@ __device__ __forceinline__ EpiRes epi_res(const DenseEpi& e, int64_t m, int64_t 
 }
 
 // Stores eight columns of output row m; z (and, gated, u) are the float32 sums.  T is the
-// operands' type.  e.vec and n < e.N.
-template <typename T, bool GATED>
+// operands' type, WIDE whether float32 results of bf16 operands have an activation (wide_act).  e.vec and n < e.N.
+template <typename T, bool GATED, bool WIDE>
 __device__ __forceinline__ void epi_store_vec(const DenseEpi& e, int64_t m, int n, float z[8], float u[8],
                                               const EpiBias<T, GATED>& bias, const EpiRes& res) {
   if (e.bias) {
@@ -185,7 +189,7 @@ __device__ __forceinline__ void epi_store_vec(const DenseEpi& e, int64_t m, int 
     Piece<T>::store(e.pre, m * e.ldp + n, z);
     if (GATED) Piece<T>::store(e.pre, m * e.ldp + e.N + n, u);
   }
-  act8<sizeof(T) == 2>(e.act, z);
+  act8<sizeof(T) == 4 ? kActF32 : (WIDE ? kActWide : kActBf16)>(e.act, z);
   if (GATED) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= u[i];
@@ -212,7 +216,8 @@ __device__ __forceinline__ void epi_store1(const DenseEpi& e, int64_t m, int n, 
     Piece<T>::put(e.pre, m * e.ldp + n, z);
     if (GATED) Piece<T>::put(e.pre, m * e.ldp + e.N + n, u);
   }
-  z = act_fn<sizeof(T) == 2>(e.act, z);
+  if constexpr (sizeof(T) == 4) z = act_fn<kActF32>(e.act, z);
+  else z = !GATED && e.out_f32 ? act_fn<kActWide>(e.act, z) : act_fn<kActBf16>(e.act, z);
   if (GATED) z *= u;
   if (e.res) z += e.out_f32 ? Piece<float>::get(e.res, m * e.ldr + n) : Piece<T>::get(e.res, m * e.ldr + n);
   if (e.out_f32) Piece<float>::put(e.out, m * e.ldo + n, z);
@@ -225,7 +230,8 @@ __device__ __forceinline__ void epi_store(const DenseEpi& e, int64_t m, int n, f
                                           const EpiBias<T, GATED>& bias, const EpiRes& res) {
   if (n >= e.N) return;
   if (e.vec) {
-    epi_store_vec<T, GATED>(e, m, n, z, u, bias, res);
+    if (sizeof(T) == 2 && !GATED && wide_act(e)) epi_store_vec<T, GATED, sizeof(T) == 2 && !GATED>(e, m, n, z, u, bias, res);
+    else epi_store_vec<T, GATED, false>(e, m, n, z, u, bias, res);
     return;
   }
 #pragma unroll

@@ -55,6 +55,9 @@ struct DenseEpi {
   int vec;                      // rows of out, res and pre may be accessed in 16-byte pieces
 };
 
+// Whether bf16 operands' results are activations kept in float32
+__host__ __device__ inline bool wide_act(const DenseEpi& e) { return e.out_f32 && (e.act == kActSilu || e.act == kActGelu); }
+
 // out[M][N] from r (M rows) and c (N rows, gated 2N): element (m, k) of r is r[m * ldr + k],
 // or r[k * ldr + m] with r_kmajor; c likewise.  Rows start on 16 bytes, and their last 16-byte
 // piece may be read whole: past K it holds zeros, past the rows of a k-major operand anything.

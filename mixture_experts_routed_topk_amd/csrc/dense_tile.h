@@ -51,8 +51,10 @@ __device__ __forceinline__ void barrier() {
   fence();
 }
 
-// kPartial: float32 sums to job.part; kGrad: those, or with one split the plain result in the operands' type
-enum { kLinear = 0, kGated = 1, kPartial = 2, kGrad = 3 };
+// kPartial: float32 sums to job.part; kGrad: those, or with one split the plain result in the operands' type;
+// kLinearWide: kLinear with wide_act (kernels of their own: as a branch in kLinear's, the longer code of both took 3% of
+// 8192 x 2048 x 7168 without an activation)
+enum { kLinear = 0, kGated = 1, kPartial = 2, kGrad = 3, kLinearWide = 4 };
 
 // ---------------------------------------------------------------------------- DMA
 // float32 stored along its rows: the XOR of a k row's 16-byte chunks, by g = (k / 4) % 4.  A fragment
@@ -277,7 +279,7 @@ __device__ __forceinline__ void store_rows(const Job& job, int split, int64_t m,
       float z[8], u[8];
 #pragma unroll
       for (int v = 0; v < 8; ++v) z[v] = acc[i][v >> 2][v & 3], u[v] = up[i][v >> 2][v & 3];
-      epi_store_vec<T, EPI == kGated>(e, m + 16 * i, n, z, u, bias, res[i]);
+      epi_store_vec<T, EPI == kGated, EPI == kLinearWide>(e, m + 16 * i, n, z, u, bias, res[i]);
     }
   }
 }
@@ -521,7 +523,8 @@ hipError_t run_forward(const DenseGemm& g, const Plan& p, int tile_cols, void* w
     job.part = static_cast<float*>(ws);
     job.ldpart = part_pitch(g.e.N, g.gated);
   }
-  hipError_t err = tiles(job, parts ? kPartial : (g.gated ? kGated : kLinear));
+  const bool wide = sizeof(T) == 2 && wide_act(g.e);
+  hipError_t err = tiles(job, parts ? kPartial : (g.gated ? kGated : (wide ? kLinearWide : kLinear)));
   if (err != hipSuccess || !parts) return err;
   const int64_t pieces = g.M * ((g.e.N + 7) / 8);
   const dim3 grid((unsigned)((pieces + 255) / 256));

@@ -176,3 +176,21 @@ def test_gated_relu_gradient_of_special_values(T, H, I, dtype):
     for got, (r, b), what in zip((dx, dw, db), grads, ("dx", "dw", "db")):
         check_special(got, r, b, what)
     assert torch.isfinite(dx[0]).all() and not torch.isfinite(dx[1]).any()
+
+
+@pytest.mark.parametrize("T,N", [(3, 24), (20, 61), (200, 64), (333, 60), (2500, 1032)])
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_float32_outputs_have_float32_activations(name, T, N):
+    """bf16 operands with a float32 output: each z is one bf16 value exactly, so the output's error is the
+    activation's.  silu = z / (1 + exp(-z)): exp off by 2 u32 of itself, sum and quotient by one each: 4 u32.  gelu = z / 2
+    erfc(-z / sqrt 2): an argument off by 2 u32 moves erfc by at most (z^2 + 1) times that, erfc is off by 8 u32 (4 units in the
+    last place) and the products by 2."""
+    z = torch.linspace(-24, 24, T * 8).view(8, T).t().contiguous() if T > 3 else torch.linspace(-9, 9, 24).view(3, 8)
+    x = z.to(BF16).cuda()
+    w = torch.zeros((N, 8), dtype=BF16, device="cuda")
+    w[torch.arange(N), torch.arange(N) % 8] = 1
+    y, _ = m.linear(x, w, act=ACT[name], out_dtype=F32)
+    zd = x.double()[:, torch.arange(N) % 8]
+    want = ref.act(name, zd) if name == "silu" else 0.5 * zd * torch.erfc(-zd * 0.5 ** 0.5)   # (erfc keeps the far tail)
+    tol = 4.0 if name == "silu" else 12 + 2 * zd * zd
+    ref.check(y, want, tol * ref.U32 * want.abs() + 2.0 ** -149, f"{name} of float32 outputs")
