@@ -451,9 +451,6 @@ def check_mfma_blocks(a: torch.Tensor, b: torch.Tensor, b_scale: Optional[torch.
 # (Decode steps make these calls by the thousand, each a few microseconds of GPU time: the checks
 # below take the common case in one comparison and say what is wrong only after it fails.)
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-
 
 def _rows(name: str, t: torch.Tensor, T: int, cols: int, dtype: torch.dtype, dev: int) -> int:
     """Checks a [T, cols] activation matrix on GPU `dev`; returns its row pitch in elements."""
@@ -511,11 +508,12 @@ def _addr(t: Optional[torch.Tensor]):
 
 def _run(fn, dev: int, *args) -> None:
     """Calls fn(*args, current stream of GPU `dev`) with that GPU current."""
-    if _current_device() == dev:
-        status = fn(*args, _raw_stream(dev))
+    C = torch._C             # (looked up here: a torch without GPU support has neither name, and imports the package)
+    if C._cuda_getDevice() == dev:
+        status = fn(*args, C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev))
+            status = fn(*args, C._cuda_getCurrentRawStream(dev))
     if status:
         _check(status)
 

@@ -1,9 +1,15 @@
 """Host-side behaviour of the dense operators: workspaces, plans and the binding's conversions (no HIP call is reached)."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 
 import mixture_experts_routed_topk_amd as m
 from test_dense_abi_cpu import L, gated, linear, size
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("T", [1, 16, 32])
@@ -20,3 +26,16 @@ def test_few_rows_take_a_second_part_only_where_dz_has_one(T):
     assert need(act=m.ACT_RELU) + x2 <= two and need(act=m.ACT_NONE) + x2 <= two
     assert need(act=m.ACT_RELU, out_dtype=m.F32) == need(act=m.ACT_NONE, out_dtype=m.F32) == two
     assert size(L.moe_gated_linear_workspace_size, gated(T=T, H=K, I=N, act=m.ACT_RELU), 1)[1] > x2
+
+
+def test_package_imports_on_a_torch_without_gpu_support():
+    """Host-only calls (workspace sizes, plans) need no GPU entry points of torch."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, n)\n"
+            "import mixture_experts_routed_topk_amd as m\n"
+            "p = m.make_problem(4, 128, 128, 4, 2, m.BF16, m.BF16)\n"
+            "assert m.workspace_size(p) > 0 and m.plan_describe(p)\n"
+            "try: m.linear(torch.zeros(1, 8, dtype=torch.bfloat16), torch.zeros(8, 8, dtype=torch.bfloat16))\n"
+            "except ValueError: print('refused')\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr[-2000:]
