@@ -534,7 +534,11 @@ def _scratch(workspace: Optional[torch.Tensor], need: int, x: torch.Tensor, dev:
 def _problem(kind, fields: tuple, size_fn: Optional[str] = None, *args):
     """(reference to the C problem, its workspace bytes): both follow from the fields alone, so
     they are made once per problem.  The library only reads the struct."""
-    ref = ctypes.byref(kind(*fields))
+    prob = kind(*fields)
+    for (name, _), given in zip(kind._fields_, fields):      # (ctypes keeps an integer's low bits without a word)
+        if isinstance(given, int) and getattr(prob, name) != given:
+            raise ValueError(f"{name} = {given} is out of range")
+    ref = ctypes.byref(prob)
     n = ctypes.c_size_t(0)
     if size_fn is not None:
         _check(getattr(lib(), size_fn)(ref, *args, ctypes.byref(n)))

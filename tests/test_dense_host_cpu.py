@@ -39,3 +39,16 @@ def test_package_imports_on_a_torch_without_gpu_support():
             "except ValueError: print('refused')\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("kind,fields", [
+    (m.NormProblem, (1, 2 ** 32 + 128, m.BF16, 1e-6, 0, 0, 0, 0)),
+    (m.LinearProblem, (1, 64, 2 ** 32 + 8, m.BF16, m.BF16, 0, 0, 0, 0, 0, 0)),
+    (m.LinearProblem, (1, 2 ** 32 + 64, 8, m.BF16, m.BF16, 0, 0, 0, 0, 0, 0)),
+    (m.LinearProblem, (1, 64, 8, m.BF16, m.BF16, 2 ** 32, 0, 0, 0, 0, 0)),
+    (m.GatedProblem, (1, 64, 2 ** 32 + 8, m.BF16, m.ACT_SILU, 0, 0, 0, 0)),
+    (m.NormProblem, (2 ** 64 + 4, 128, m.BF16, 1e-6, 0, 0, 0, 0))])
+def test_sizes_that_wrap_are_refused(kind, fields):
+    """A C struct's fields keep the low bits of what is put in: a row of 2^32 + 128 elements is not one of 128."""
+    with pytest.raises(ValueError):
+        m._problem(kind, fields)
