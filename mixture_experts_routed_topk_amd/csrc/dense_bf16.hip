@@ -221,23 +221,7 @@ __global__ __launch_bounds__(TA == 256 ? 512 : 256, TA == 256 ? 1 : 2) void dens
   }
 }
 
-// ---------------------------------------------------------------------------- costs
-// Fitted to 43 products of 60 to 8192 rows, each measured with every tile and split (rms error of the
-// estimate 13%; the choices take 1.6% longer than the best ones).  `shared` of the 128-row tiles is
-// 8% above its fit: they draw twice the operands of the 256-row ones, which shows when operands
-// come from HBM (8192 x 2048 x 7168, fresh inputs each call: 273 against 241 us).
-constexpr TileCost kTiles[] = {{256, 256, 1, 1.115, 1.115, 7.0}, {128, 128, 2, 0.549, 0.38, 0.57}, {64, 128, 3, 0.328, 0.251, 0.02}};
-constexpr JoinCost kJoin = {2.8, 3.36e6};
-
-// The gradients' tiles: pairs for dx and dw.  Fitted to 23 backward passes with every pair of tiles
-// and splits (rms error 12%, choices 1% longer than the best; here the 64-row tiles
-// have the LDS of the 128-row ones, two to a CU).
-constexpr TileCost kPairTiles[] = {{256, 256, 1, 1.31, 1.21, 4.8}, {128, 128, 2, 0.638, 0.343, 0.82}, {64, 128, 2, 0.512, 0.405, 0.04}};
-constexpr int kPairs[][2] = {{0, 0}, {1, 1}, {2, 1}};
-constexpr JoinCost kPairJoin = {3.7, 3.3e6};
-
-Plan plan_bf16(int64_t M, int64_t N, int64_t K, int gated) { return plan_forward<uint16_t>(kTiles, kJoin, M, N, K, gated); }
-
+// ---------------------------------------------------------------------------- launches
 template <int EPI>
 void launch_tiles(const Job& job, int tile, hipStream_t s) {
   const dim3 grid = tile_grid(job);
@@ -275,13 +259,13 @@ hipError_t launch_dense_gemm(const DenseGemm& g, void* ws, bool f32, hipStream_t
 size_t dense_gradients_workspace(int64_t rows, int64_t N, int64_t cols, bool f32, bool two_parts) {
   if (rows == 0) return 0;
   return f32 ? dense_gradients_f32_workspace(rows, N, cols)
-             : gradients_part<uint16_t>(kPairs, kPairTiles, kPairJoin, rows, N, cols, two_parts);
+             : gradients_part<uint16_t>(kPairsBf16, kPairTilesBf16, kPairJoinBf16, rows, N, cols, two_parts);
 }
 
 hipError_t launch_dense_gradients(const DenseGemm* dx, const DenseGemm* dw, void* ws, bool f32, bool two_parts,
                                   hipStream_t s) {
   if (f32) return launch_dense_gradients_f32(dx, dw, ws, s);
-  return run_gradients<uint16_t>(kPairs, kPairTiles, kPairJoin, dx, dw, two_parts, ws, s,
+  return run_gradients<uint16_t>(kPairsBf16, kPairTilesBf16, kPairJoinBf16, dx, dw, two_parts, ws, s,
                                  [&](int pair, dim3 grid, const Job& x, const Job& w, int n_first, int dw_first) {
     if (pair == 0) hipLaunchKernelGGL((dense_pair_kernel<256, 256>), grid, dim3(512), 0, s, x, w, n_first, dw_first);
     else if (pair == 1) hipLaunchKernelGGL((dense_pair_kernel<128, 128>), grid, dim3(256), 0, s, x, w, n_first, dw_first);

@@ -8,14 +8,6 @@
 namespace moe {
 namespace {
 
-// (a slice's MFMAs alone: 32 x RR x 128 products at 256 flops a cycle, 1.7 us of 128 rows at 2.4 GHz)
-constexpr TileCost kTiles[] = {{128, 128, 2, 1.9, 1.9, 3.0}, {64, 128, 3, 1.0, 1.0, 2.0}, {32, 128, 3, 0.6, 0.55, 2.0}};
-constexpr JoinCost kJoin = {3.5, 3.3e6};
-constexpr TileCost kPairTiles[] = {{128, 128, 2, 1.9, 1.9, 3.0}, {64, 128, 2, 1.0, 1.0, 2.0}, {32, 128, 2, 0.6, 0.55, 2.0}};
-constexpr int kPairs[][2] = {{0, 0}, {1, 0}, {2, 0}};
-
-Plan plan_f32(int64_t M, int64_t N, int64_t K, int gated) { return plan_forward<float>(kTiles, kJoin, M, N, K, gated); }
-
 template <int EPI>
 void launch_tiles(const Job& job, int tile, hipStream_t s) {
   const dim3 grid = tile_grid(job);
@@ -56,11 +48,11 @@ hipError_t launch_dense_gemm_f32(const DenseGemm& g, void* ws, hipStream_t s) {
 }
 
 size_t dense_gradients_f32_workspace(int64_t rows, int64_t N, int64_t cols) {
-  return gradients_part<float>(kPairs, kPairTiles, kJoin, rows, N, cols, false);
+  return gradients_part<float>(kPairsF32, kPairTilesF32, kJoinF32, rows, N, cols, false);
 }
 
 hipError_t launch_dense_gradients_f32(const DenseGemm* dx, const DenseGemm* dw, void* ws, hipStream_t s) {
-  return run_gradients<float>(kPairs, kPairTiles, kJoin, dx, dw, false, ws, s,
+  return run_gradients<float>(kPairsF32, kPairTilesF32, kJoinF32, dx, dw, false, ws, s,
                               [&](int pair, dim3 grid, const Job& x, const Job& w, int n_first, int dw_first) {
     if (pair == 0) hipLaunchKernelGGL(dense_pair_f32_kernel<128>, grid, dim3(256), 0, s, x, w, n_first, dw_first);
     else if (pair == 1) hipLaunchKernelGGL(dense_pair_f32_kernel<64>, grid, dim3(256), 0, s, x, w, n_first, dw_first);

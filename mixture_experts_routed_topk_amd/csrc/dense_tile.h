@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include "dense_device.h"
+#include "dense_plan.h"
 
 namespace moe {
 namespace {
@@ -34,8 +35,6 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-template <typename T>
-constexpr int ks() { return 128 / (int)sizeof(T); }   // k per slice
 constexpr int REGION = 128 * 128;                     // bytes of 128 operand rows in a slice (16 KB)
 
 __device__ const i32x4 zero_chunk[1] = {{0, 0, 0, 0}};
@@ -450,60 +449,7 @@ __global__ __launch_bounds__(256) void dense_join_pair_kernel(Job a, Job b, int 
   else join<T, false>(b, (int64_t)(blockIdx.x - n_first) * 256 + threadIdx.x);
 }
 
-// ---------------------------------------------------------------------------- plans
-struct Plan {
-  int tile;      // rows of a tile
-  int splits;
-  int slices;    // per split
-};
-struct TileCost {
-  int rows, cols, per_cu;
-  double alone, shared, fixed;
-};
-struct JoinCost {
-  double us, bytes_per_us;
-};
-constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
-
-// The last round of 256-row tiles runs as halves when those find a CU each (8192 x 2048 x 7168, 3.5 rounds:
-// 247 -> 235 us; 0.7 to 0.8 of a whole tile's time).  The plan does not count on it: in 16 of 16 products where
-// that would have moved the choice from 128-row tiles these stayed faster, by 1 to 14%.
-inline int64_t whole_tiles(int rows, int64_t tiles) { return rows == 256 && tiles % 256 <= 128 ? tiles / 256 * 256 : tiles; }
-
-// The tile and split of a forward product with the least estimated time.  Tiles go over the 256 CUs in
-// rounds of the workgroups that a CU holds; a slice takes a workgroup at least `alone` us, and `shared`
-// us of its CU; `fixed` us go to a tile's first DMA and epilogue, and a split adds a second launch
-// and a pass over its partial sums.
-template <typename T, int NT>
-Plan plan_forward(const TileCost (&costs)[NT], JoinCost joined, int64_t M, int64_t N, int64_t K, int gated) {
-  const int64_t cols = gated ? 2 * N : N;
-  const int64_t KT = (K + ks<T>() - 1) / ks<T>();
-  Plan best{128, 1, (int)KT};
-  double best_us = 1e30;
-  for (const TileCost& t : costs) {
-    const int64_t tiles = ((M + t.rows - 1) / t.rows) * ((cols + t.cols - 1) / t.cols);
-    for (int want : kSplits) {
-      if (want > 1 && KT / want < 3) break;
-      const int64_t per = (KT + want - 1) / want;
-      const int s = (int)((KT + per - 1) / per);      // (every split has slices)
-      const int64_t queue = (tiles * s + 255) / 256;  // workgroups of one CU
-      const int64_t rest = queue % t.per_cu;
-      double us = (queue / t.per_cu) * (per * fmax(t.alone, t.per_cu * t.shared) + t.fixed);
-      if (rest) us += per * fmax(t.alone, rest * t.shared) + t.fixed;
-      if (s > 1) us += joined.us + (double)M * cols * 4 * (s + 1) / joined.bytes_per_us;
-      if (us < best_us) best_us = us, best = Plan{t.rows, s, (int)per};
-    }
-  }
-  return best;
-}
-inline int64_t part_pitch(int64_t N, int gated) { return ((gated ? 2 * N : N) + 7) / 8 * 8; }
-
-// Bytes of partial sums of a forward product: of a split contraction, and of an output whose rows
-// cannot be stored in pieces
-inline size_t forward_part(const Plan& p, int64_t M, int64_t N, int gated, int vec) {
-  return p.splits > 1 || !vec ? (size_t)p.splits * M * part_pitch(N, gated) * 4 : 0;
-}
-
+// ---------------------------------------------------------------------------- launches
 // Launches a forward product: tiles(job, epilogue) launches the tile kernel
 template <typename T, typename F>
 hipError_t run_forward(const DenseGemm& g, const Plan& p, int tile_cols, void* ws, hipStream_t s, F&& tiles) {
@@ -535,76 +481,6 @@ hipError_t run_forward(const DenseGemm& g, const Plan& p, int tile_cols, void* w
 inline dim3 tile_grid(const Job& job) {
   const int halved = job.mt * job.nt - job.whole;
   return dim3((unsigned)((job.whole + 7) / 8 * 8 + (halved + 7) / 8 * 16), (unsigned)job.splits);
-}
-
-// ---------------------------------------------------------------------------- plan of the gradients
-struct PairPlan {
-  int tiles;                     // index into the pairs of tiles
-  int splits[2], slices[2];      // dx, dw
-};
-// dx [M0][N] over K0 and dw [M1][N] over K1; a product with no rows is left out.  Their tiles share
-// the CUs: the time is the work of all of them over 256 CUs, at least the longest tile's own,
-// and half a tile more for the uneven end.
-template <typename T, int NP, int NT>
-PairPlan plan_pair(const int (&pairs)[NP][2], const TileCost (&costs)[NT], JoinCost joint, const int64_t (&M)[2], int64_t N, const int64_t (&K)[2]) {
-  constexpr int kTry[] = {1, 2, 4, 8, 16};
-  PairPlan best{0, {1, 1}, {1, 1}};
-  double best_us = 1e30;
-  for (int t = 0; t < NP; ++t) {
-    for (int a : kTry) {
-      for (int b : kTry) {
-        PairPlan p{t, {a, b}, {1, 1}};
-        double work = 0, longest = 0, shortest = 1e30, joined = 0;
-        bool ok = true;
-        for (int j = 0; j < 2; ++j) {
-          const int want = j ? b : a;
-          if (M[j] == 0 || K[j] == 0) {
-            p.splits[j] = 1;
-            ok = ok && want == 1;
-            continue;
-          }
-          const TileCost& c = costs[pairs[t][j]];
-          const int64_t KT = (K[j] + ks<T>() - 1) / ks<T>();
-          const double whole = (double)((M[j] + c.rows - 1) / c.rows) * ((N + c.cols - 1) / c.cols);
-          if (want > 1 && (KT / want < 3 || whole >= 512)) {   // (too short, or no need)
-            ok = false;
-            break;
-          }
-          const int64_t per = (KT + want - 1) / want;
-          p.splits[j] = (int)((KT + per - 1) / per);
-          p.slices[j] = (int)per;
-          const double tiles = whole * p.splits[j];
-          work += tiles * (per * c.shared + c.fixed);
-          const double own = per * c.alone + c.fixed;
-          longest = fmax(longest, own);
-          shortest = fmin(shortest, own);
-          if (p.splits[j] > 1) joined += (double)M[j] * N * 4 * (p.splits[j] + 1);
-        }
-        if (!ok) continue;
-        double us = fmax(work / 256 + 0.47 * shortest, longest);
-        if (joined > 0) us += joint.us + joined / joint.bytes_per_us;
-        if (us < best_us) best_us = us, best = p;
-      }
-    }
-  }
-  return best;
-}
-// bytes of the partial sums of product j; two_parts: two rows of dx's product add up to one
-inline size_t pair_part(const PairPlan& p, int j, int64_t M, int64_t N, bool two_parts) {
-  return p.splits[j] > 1 || (two_parts && j == 0) ? ((size_t)p.splits[j] * M * N * 4 + 255) & ~size_t(255) : 0;
-}
-
-template <typename T, int NP, int NT>
-size_t gradients_part(const int (&pairs)[NP][2], const TileCost (&costs)[NT], JoinCost joint, int64_t rows, int64_t N,
-                      int64_t cols, bool two_parts) {
-  size_t most = 0;
-  for (int which = 1; which < 4; ++which) {        // dx, dw or both may be asked for
-    const int64_t M[2] = {which & 1 ? rows : 0, which & 2 ? cols : 0}, K[2] = {cols, rows};
-    const PairPlan p = plan_pair<T>(pairs, costs, joint, M, N, K);
-    const size_t need = pair_part(p, 0, M[0], N, two_parts) + pair_part(p, 1, M[1], N, two_parts);
-    most = need > most ? need : most;
-  }
-  return most;
 }
 
 // Launches the gradients: tiles(pair, grid, dx, dw, n_first, dw_first) launches the pair kernel
