@@ -136,10 +136,12 @@ size_t gradients_part(const int (&pairs)[NP][2], const TileCost (&costs)[NT], Jo
 }
 
 // ---------------------------------------------------------------------------- costs, bf16
-// Fitted to 43 products of 60 to 8192 rows, each measured with every tile and split (rms error of the
-// estimate 13%; the choices take 1.6% longer than the best ones).  `shared` of the 128-row tiles is
-// 8% above its fit: they draw twice the operands of the 256-row ones, which shows when operands
-// come from HBM (8192 x 2048 x 7168, fresh inputs each call: 273 against 241 us).
+// Fitted to 43 products of 60 to 8192 rows on operands that stay in the caches, each measured with every tile and
+// split (rms error of the estimate 13%; the choices take 1.6% longer than the best ones).  `shared` of the 128-row tiles
+// is 8% above its fit: they draw twice the operands of the 256-row ones, which shows when operands come from HBM.
+// Over 152 products of 137 to 8192 rows with other operands at every call, half of them drawn where the choice hangs on
+// this figure, the tiles chosen take 5.3% longer than the best measured with 0.38, and 5.6% with the fit's 0.352, 5.6% with
+// 0.39, 6.6% with 0.40 and 7.2% with 0.41 (there 128-row tiles give way to 64-row ones that are slower by 15%).
 constexpr TileCost kTilesBf16[] = {{256, 256, 1, 1.115, 1.115, 7.0}, {128, 128, 2, 0.549, 0.38, 0.57}, {64, 128, 3, 0.328, 0.251, 0.02}};
 constexpr JoinCost kJoinBf16 = {2.8, 3.36e6};
 
