@@ -416,7 +416,10 @@ typedef struct {
   int64_t lddx;       /* pitch of dx                            a multiple of 8, or 0      */
 } moe_linear_problem;
 
-/* Bytes of workspace of moe_linear (backward == 0) or moe_linear_backward. */
+/* Which call a workspace is for: the forward, the backward call, or that without dbias (any other value: MOE_BACKWARD). */
+enum { MOE_FORWARD = 0, MOE_BACKWARD = 1, MOE_BACKWARD_NO_BIAS = 2 };
+
+/* Bytes of workspace of moe_linear (backward == MOE_FORWARD) or moe_linear_backward. */
 moe_status moe_linear_workspace_size(const moe_linear_problem* p, int backward, size_t* bytes);
 
 /*
@@ -458,7 +461,7 @@ typedef struct {
   int64_t lddx;       /* pitch of dx                            a multiple of 8, or 0      */
 } moe_gated_problem;
 
-/* Bytes of workspace of moe_gated_linear (backward == 0) or moe_gated_linear_backward. */
+/* Bytes of workspace of moe_gated_linear (backward == MOE_FORWARD) or moe_gated_linear_backward. */
 moe_status moe_gated_linear_workspace_size(const moe_gated_problem* p, int backward, size_t* bytes);
 
 /*

@@ -654,7 +654,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre: Opt
 
 
 def _backward(fn_name, kind, fields, dy, x, w, pre, cols, need_bias, workspace, dev):
-    prob, need = _problem(kind, fields, fn_name.replace("_backward", "_workspace_size"), 1)
+    prob, need = _problem(kind, fields, fn_name.replace("_backward", "_workspace_size"), 1 if need_bias else 2)
     ws, n = _scratch(workspace, need, x, dev)
     dx = torch.empty_like(x)
     dw = torch.empty_like(w)

@@ -103,7 +103,7 @@ int64_t dz_pitch(const Backward& b) { return (b.cols + 7) / 8 * 8; }
 struct BackwardLayout {
   size_t dz, x2, part, gemm, total;
 };
-BackwardLayout layout(const Backward& b) {
+BackwardLayout layout(const Backward& b, bool bias) {
   BackwardLayout L;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -116,7 +116,7 @@ BackwardLayout layout(const Backward& b) {
   const int64_t rows = two ? 2 * b.T : b.T;        // of the products' dz and x
   L.dz = take(dz_is_dy(b) ? 0 : (size_t)rows * dz_pitch(b) * esize(b.dtype));
   L.x2 = take(two ? (size_t)rows * b.K * esize(b.dtype) : 0);
-  L.part = take((size_t)dz_parts(b.T) * b.cols * 4);
+  L.part = take(bias ? (size_t)dz_parts(b.T) * b.cols * 4 : 0);
   L.gemm = take(dense_gradients_workspace(rows, b.K, b.cols, f32, two));
   L.total = o;
   return L;
@@ -141,7 +141,7 @@ moe_status run_backward(const Backward& b, const void* dy, const void* x, const 
   const bool need_pre = b.act != MOE_ACT_NONE;
   if (b.T > 0 && (!dy || (need_pre && !pre) || (dx && !w) || (dw && !x))) return MOE_ERR_NULL_ARG;
   if (!all_aligned16(dy, x, w, pre, dx, dw, dbias, workspace)) return MOE_ERR_BAD_SHAPE;
-  const BackwardLayout L = layout(b);
+  const BackwardLayout L = layout(b, dbias != nullptr);
   if (b.T > 0 && L.total > 0 && !workspace) return MOE_ERR_NULL_ARG;
   if (b.T > 0 && workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   (void)hipGetLastError();   // an error left by an earlier, unrelated HIP call is not ours
@@ -289,7 +289,7 @@ moe_status moe_linear_workspace_size(const moe_linear_problem* p, int backward, 
   const moe_status st = check(p);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_NULL_ARG;
-  *bytes = backward ? layout(backward_of(*p)).total : forward_bytes(*p);
+  *bytes = backward ? layout(backward_of(*p), backward != MOE_BACKWARD_NO_BIAS).total : forward_bytes(*p);
   return MOE_OK;
 }
 
@@ -339,7 +339,8 @@ moe_status moe_gated_linear_workspace_size(const moe_gated_problem* p, int backw
   const moe_status st = check(p);
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_NULL_ARG;
-  *bytes = backward ? layout(backward_of(*p)).total : dense_gemm_workspace(p->T, p->I, p->H, 1, p->dtype == MOE_F32, 1);
+  *bytes = backward ? layout(backward_of(*p), backward != MOE_BACKWARD_NO_BIAS).total
+                    : dense_gemm_workspace(p->T, p->I, p->H, 1, p->dtype == MOE_F32, 1);
   return MOE_OK;
 }
 

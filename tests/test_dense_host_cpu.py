@@ -1,5 +1,6 @@
 """Host-side behaviour of the dense operators: workspaces, plans and the binding's conversions (no HIP call is reached)."""
 
+import ctypes
 import os
 import subprocess
 import sys
@@ -7,7 +8,7 @@ import sys
 import pytest
 
 import mixture_experts_routed_topk_amd as m
-from test_dense_abi_cpu import L, gated, linear, size
+from test_dense_abi_cpu import A, L, gated, linear, size
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -52,3 +53,16 @@ def test_sizes_that_wrap_are_refused(kind, fields):
     """A C struct's fields keep the low bits of what is put in: a row of 2^32 + 128 elements is not one of 128."""
     with pytest.raises(ValueError):
         m._problem(kind, fields)
+
+
+@pytest.mark.parametrize("T", [3, 700, 100_000])
+def test_workspace_without_a_bias_gradient(T):
+    """The partial sums of dbias, eight rows each, are taken only where dbias is asked for."""
+    for fn, call, p, cols in ((L.moe_linear_workspace_size, L.moe_linear_backward, linear(T=T, N=64, act=m.ACT_SILU), 64),
+                              (L.moe_gated_linear_workspace_size, L.moe_gated_linear_backward, gated(T=T), 128)):
+        full, less = size(fn, p, 1)[1], size(fn, p, 2)[1]
+        assert 0 < less <= full - (T + 7) // 8 * cols * 4
+        args = [A] * 6 + [None, A]                                   # dy, x, w, pre, dx, dw, dbias, workspace
+        assert call(ctypes.byref(p), *args, less - 1, None) == 4
+        args[6] = A
+        assert call(ctypes.byref(p), *args, less, None) == 4

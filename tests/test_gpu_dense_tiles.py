@@ -1,6 +1,8 @@
 """Every tile kernel of the dense operators (dense_tiles.py) against the 64-bit plain forms: with bias, activation,
 residual and saved projections, on rows inside wider buffers; and every tensor of calls made on several streams at once."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -89,3 +91,22 @@ def test_every_tensor_of_calls_on_several_streams():
         bad = [(i, k, j) for i, (g, wnt) in enumerate(zip(got, want)) for k, (out, ref_out) in enumerate(zip(g, wnt))
                for j, (t, r) in enumerate(zip(out, ref_out)) if not same(t, r)]
         assert not bad, f"(set, call, tensor) {bad}"
+
+
+@pytest.mark.parametrize("T,K,N", [(5, 72, 40), (33, 200, 264), (1030, 264, 520)])
+def test_gradients_without_bias_in_their_own_workspace(T, K, N):
+    """The workspace of a call without dbias is what it says: the call stays inside, and gives the same gradients."""
+    x, w = rnd("x", (T, K), BF16), rnd("w", (N, K), BF16, K ** -0.5)
+    dy, pre = rnd("dy", (T, N), BF16), rnd("z", (T, N), BF16)
+    p = m.LinearProblem(T, K, N, m.BF16, m.BF16, m.ACT_SILU, 0, 0, 0, 0, 0)
+    n = ctypes.c_size_t(0)
+    assert m.lib().moe_linear_workspace_size(ctypes.byref(p), 2, ctypes.byref(n)) == 0
+    ws = torch.full((n.value + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    assert m.lib().moe_linear_backward(ctypes.byref(p), dy.data_ptr(), x.data_ptr(), w.data_ptr(), pre.data_ptr(), dx.data_ptr(),
+                                       dw.data_ptr(), None, ws.data_ptr(), n.value,
+                                       torch.cuda.current_stream().cuda_stream) == 0
+    full = m.linear_backward(dy, x, w, pre=pre, act=m.ACT_SILU, need_bias=True)
+    assert same(dx, full[0]) and same(dw, full[1]) and bool((ws[n.value:] == 0xA5).all())
+    for a, b in zip(m.linear_backward(dy, x, w, pre=pre, act=m.ACT_SILU)[:2], full):
+        assert same(a, b)
