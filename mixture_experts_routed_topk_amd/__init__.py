@@ -297,10 +297,16 @@ def experts_forward_quantized(hidden_q: torch.Tensor, hidden_scale: torch.Tensor
     (moe_experts_forward_quantized): hidden_q [T,H] e4m3 codes (uint8 or float8_e4m3fn) and
     hidden_scale [T,H/128] float32, as rms_norm_fp8 and quantize_rows_fp8 return them.  The
     output is bf16."""
-    for name, t in (("hidden_q", hidden_q), ("hidden_scale", hidden_scale), ("topk_idx", topk_idx),
-                    ("topk_w", topk_w), ("w_gate_up", w_gate_up), ("w_down", w_down),
-                    ("w_gate_up_scale", w_gate_up_scale), ("w_down_scale", w_down_scale)):
+    given = [("hidden_q", hidden_q), ("hidden_scale", hidden_scale), ("topk_idx", topk_idx), ("topk_w", topk_w),
+             ("w_gate_up", w_gate_up), ("w_down", w_down), ("w_gate_up_scale", w_gate_up_scale),
+             ("w_down_scale", w_down_scale)]
+    given += [(name, t) for name, t in (("out", out), ("workspace", workspace)) if t is not None]
+    for name, t in given:
         _need_gpu(name, t)
+    dev = hidden_q.get_device()
+    for name, t in given:
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, hidden_q on cuda:{dev}")
     if hidden_q.dtype not in (torch.uint8, torch.float8_e4m3fn) or hidden_q.dim() != 2:
         raise ValueError("hidden_q must be a 2-D tensor of e4m3 codes (uint8 or float8_e4m3fn)")
     T, H = hidden_q.shape
@@ -312,20 +318,15 @@ def experts_forward_quantized(hidden_q: torch.Tensor, hidden_scale: torch.Tensor
         raise ValueError("topk_w and topk_idx shapes differ")
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=hidden_q.device)
-    else:
-        _need_gpu("out", out)
-        if tuple(out.shape) != (T, H) or out.dtype != torch.bfloat16:
-            raise ValueError("out must be bf16 [T, H]")
+    elif tuple(out.shape) != (T, H) or out.dtype != torch.bfloat16:
+        raise ValueError("out must be bf16 [T, H]")
     prob = problem_for(out, topk_idx, w_gate_up, w_down, w_gate_up_scale, flags)
     check_scales(prob, w_gate_up_scale, w_down_scale)
     if workspace is None:
         workspace = torch.empty(max(workspace_size(prob), 1), dtype=torch.uint8, device=hidden_q.device)
-    else:
-        _need_gpu("workspace", workspace)
-    _check(lib().moe_experts_forward_quantized(
-        ctypes.byref(prob), _ptr(hidden_q), _ptr(hidden_scale), _ptr(topk_idx), _ptr(topk_w), _ptr(w_gate_up),
-        _ptr(w_down), _ptr(w_gate_up_scale), _ptr(w_down_scale), _ptr(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(hidden_q.device)))
+    _run(lib().moe_experts_forward_quantized, dev, ctypes.byref(prob), _ptr(hidden_q), _ptr(hidden_scale), _ptr(topk_idx),
+         _ptr(topk_w), _ptr(w_gate_up), _ptr(w_down), _ptr(w_gate_up_scale), _ptr(w_down_scale), _ptr(out), _ptr(workspace),
+         workspace.numel() * workspace.element_size())
     return out
 
 

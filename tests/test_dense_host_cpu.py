@@ -6,6 +6,7 @@ import subprocess
 import sys
 
 import pytest
+import torch
 
 import mixture_experts_routed_topk_amd as m
 from test_dense_abi_cpu import A, L, gated, linear, size
@@ -66,3 +67,33 @@ def test_workspace_without_a_bias_gradient(T):
         assert call(ctypes.byref(p), *args, less - 1, None) == 4
         args[6] = A
         assert call(ctypes.byref(p), *args, less, None) == 4
+
+
+class Elsewhere(torch.Tensor):
+    """A host tensor that says it is on a GPU: enough for the checks that come before any GPU call."""
+    gpu = 0
+    device = property(lambda self: torch.device("cuda", self.gpu))
+
+    def get_device(self):
+        return self.gpu
+
+
+def on(gpu, *shape, dtype=torch.uint8):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(Elsewhere)
+    t.gpu = gpu
+    return t
+
+
+@pytest.mark.parametrize("which", range(10))
+def test_quantized_forward_refuses_tensors_of_several_gpus(which):
+    """Every tensor of a call on one GPU (that of hidden_q), the caller's out and workspace among them."""
+    T, H, I, E, k = 4, 128, 128, 2, 2
+    f32, i32 = torch.float32, torch.int32
+    spec = [((T, H), torch.uint8), ((T, 1), f32), ((T, k), i32), ((T, k), f32), ((E, 2 * I, H), torch.uint8),
+            ((E, H, I), torch.uint8), ((E, 2, 1), f32), ((E, 1, 1), f32), ((T, H), torch.bfloat16), ((1 << 20,), torch.uint8)]
+    if which == 0:                                            # all but hidden_q
+        args = [on(int(i > 0), *s, dtype=d) for i, (s, d) in enumerate(spec)]
+    else:
+        args = [on(int(i == which), *s, dtype=d) for i, (s, d) in enumerate(spec)]
+    with pytest.raises(ValueError, match="cuda:"):
+        m.experts_forward_quantized(*args[:8], out=args[8], workspace=args[9])
