@@ -157,7 +157,10 @@ __global__ __launch_bounds__(block_threads<WPR>()) void rms_norm_backward_kernel
       if (a.res) next.dh[i] = Piece<T>::raw(a.res, row * a.ldr + p * 8);
     }
   };
-  // sixteen waves leave a lane 128 registers: no room for a second row, nor for g and n beside dy and h
+  // sixteen waves leave a lane 128 registers: no room for a second row, nor for g and n beside dy and h.  Even so
+  // those instances spill (43 and 83 registers of bf16 and float32 rows up to 32768, 323 and 424 beyond), which
+  // costs them half their rate and more: 2048 x 16384 with dh 125 us in bf16 (2.15 TB/s) and 219 in float32, 512 x
+  // 65536 255 and 365 us, against 4.1 to 4.8 TB/s up to 8192
   constexpr bool kAhead = WPR < 16;
   int slot = 0;
   const int64_t step = (int64_t)gridDim.x * RPB;
@@ -222,7 +225,9 @@ __global__ __launch_bounds__(block_threads<WPR>()) void rms_norm_backward_kernel
 }
 
 // Lanes of a row hold at most 4 pieces (2048 columns a wave) while a row fits four waves, so
-// a row's registers stay few enough for several blocks per CU; longer rows take 16 waves.
+// a row's registers stay few enough for several blocks per CU (backward in float32 with 4 pieces: one); longer
+// rows take 16 waves, and past 32768 columns 8 pieces, where the float32 forward spills too (104 registers; 512 x
+// 65536 185 us, 2.9 TB/s).
 template <typename F>
 hipError_t by_width(int H, F&& f) {
   const int np = H / 8;
@@ -239,7 +244,8 @@ int rows_of_block(int H) { return H / 8 <= 256 ? rows_per_block<1>() : 1; }
 
 int64_t backward_blocks(int64_t T, int H) {
   const int64_t need = (T + rows_of_block(H) - 1) / rows_of_block(H);
-  const int64_t most = H / 8 <= 1024 ? 512 : 256;   // two blocks of four waves, or one of sixteen, per CU
+  // two blocks of four waves, or one of sixteen, per CU (float32 with 4 pieces a lane: one after the other)
+  const int64_t most = H / 8 <= 1024 ? 512 : 256;
   return need < most ? need : most;
 }
 
