@@ -317,7 +317,7 @@ moe_status moe_check_mfma_blocks(int fmt, const uint8_t* a, const uint8_t* b, co
 enum {
   MOE_STAGE_ZERO = 0,      /* clear the float32 accumulator                      */
   MOE_STAGE_ROUTE = 1,     /* routing bookkeeping                                */
-  MOE_STAGE_QUANT_X = 2,   /* fp8 only: quantise the hidden states               */
+  MOE_STAGE_QUANT_X = 2,   /* fp8 and fp4: quantise the hidden states             */
   MOE_STAGE_GATE_UP = 3,   /* gate/up projection + SwiGLU                        */
   MOE_STAGE_QUANT_ACT = 4, /* not launched: fp8 / fp4 gate_up kernels quantise the
                               SwiGLU output in their epilogue                    */
@@ -329,8 +329,10 @@ enum {
 /*
  * Per-stage timing hook for profilers and benchmarks.  `events` points to
  * 2 * MOE_STAGE_COUNT hipEvent_t handles (entries may be NULL); while set, each
- * later moe_experts_forward on the calling host thread records events[2*s] on its
- * stream just before stage s and events[2*s+1] just after it.  The handles are
+ * later moe_experts_forward (or _noalloc, _quantized) on the calling host thread
+ * records events[2*s] on its stream just before stage s and events[2*s+1] just after
+ * it.  The events of a stage that the call's path skips are not recorded:
+ * moe_experts_forward_quantized skips MOE_STAGE_QUANT_X.  The handles are
  * copied; the caller keeps ownership of the events.  events == NULL (or n == 0)
  * clears the hook.  n must be 0 or 2 * MOE_STAGE_COUNT (else MOE_ERR_BAD_SHAPE).
  */

@@ -4,7 +4,8 @@ A thin ctypes layer over libmoe_experts.so (declared in include/moe_experts.h).
 It only marshals arguments: torch tensors provide device pointers, the current
 HIP stream and workspace memory; every step of the forward runs in the library's
 HIP kernels.  There is no fallback: if the library is not built, or a tensor is
-not on the GPU, the call raises.
+not on the GPU, the call raises.  Results carry no autograd history, also of tensors
+that require gradients: a training loop calls the *_backward functions itself.
 """
 
 from __future__ import annotations
@@ -20,7 +21,7 @@ __all__ = [
     "experts_forward", "experts_forward_noalloc", "check_scales", "check_mfma_blocks", "route", "route_logits", "quantize_rows_fp8", "workspace_size", "plan_describe",
     "experts_forward_quantized", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "linear", "linear_backward",
     "gated_linear", "gated_linear_backward", "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_RELU",
-    "Problem", "MoeError", "lib", "FLAG_CHECK_INDICES", "FLAG_DETERMINISTIC", "FLAG_ATOMIC_COMBINE", "FLAG_ACT_GELU", "FLAG_ACT_RELU",
+    "Problem", "NormProblem", "LinearProblem", "GatedProblem", "MoeError", "lib", "FLAG_CHECK_INDICES", "FLAG_DETERMINISTIC", "FLAG_ATOMIC_COMBINE", "FLAG_ACT_GELU", "FLAG_ACT_RELU",
     "FLAG_FORCE_GROUPED", "FLAG_FORCE_DECODE", "LIB_PATH",
 ]
 
@@ -451,6 +452,9 @@ def check_mfma_blocks(a: torch.Tensor, b: torch.Tensor, b_scale: Optional[torch.
 # ----------------------------------------------------------------------------- dense operators
 # (Decode steps make these calls by the thousand, each a few microseconds of GPU time: the checks
 # below take the common case in one comparison and say what is wrong only after it fails.)
+# `workspace`, where a call takes one, is any contiguous tensor of at least the bytes that lib()'s moe_*_workspace_size
+# gives for the NormProblem, LinearProblem or GatedProblem; calls that may overlap take different ones.  Without
+# it each call takes its own from torch's allocator.
 
 
 def _rows(name: str, t: torch.Tensor, T: int, cols: int, dtype: torch.dtype, dev: int) -> int:

@@ -8,7 +8,9 @@ import torch
 
 import dense_ref as ref
 import mixture_experts_routed_topk_amd as m
+import synth
 from dense_tiles import GATED, GRADIENTS, LINEAR
+from synth.device import device_layer
 from test_gpu_dense import ACT, BF16, F32, linear_case, rnd
 from test_gpu_dense_layer import calls, flat, same
 
@@ -110,3 +112,31 @@ def test_gradients_without_bias_in_their_own_workspace(T, K, N):
     assert same(dx, full[0]) and same(dw, full[1]) and bool((ws[n.value:] == 0xA5).all())
     for a, b in zip(m.linear_backward(dy, x, w, pre=pre, act=m.ACT_SILU)[:2], full):
         assert same(a, b)
+
+
+@pytest.mark.parametrize("T", [1, 200])
+def test_stage_events_of_the_quantised_forward(T):
+    """moe_experts_forward_quantized records the events of the stages it runs, and leaves the row quantisation's as they were."""
+    D = device_layer(synth.Spec("stages", T=T, H=384, I=256, E=8, k=2, act="bf16", weight="fp8", scale="f32", seed=9))
+    args = (D["idx"], D["w"], D["w_gate_up"], D["w_down"], D["w_gate_up_scale"], D["w_down_scale"])
+    q, s = m.quantize_rows_fp8(D["x"])
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(2 * len(m.STAGES))]
+    recorded = {}
+    for name, call in (("forward", lambda: m.experts_forward(D["x"], *args)),
+                       ("quantized", lambda: m.experts_forward_quantized(q, s, *args))):
+        for e in events:
+            e.record()
+        torch.cuda.synchronize()
+        mid = torch.cuda.Event(enable_timing=True)
+        mid.record()
+        m.set_stage_events([e.cuda_event for e in events])
+        try:
+            call()
+        finally:
+            m.set_stage_events(None)
+        torch.cuda.synchronize()
+        again = [mid.elapsed_time(e) > 0 for e in events]
+        assert again[::2] == again[1::2]
+        recorded[name] = {stage for stage, a in zip(m.STAGES, again[::2]) if a}
+    assert {"gate_up", "down", "finalize"} < recorded["forward"]
+    assert recorded["forward"] - recorded["quantized"] == {"quant_x"} and recorded["quantized"] < recorded["forward"]
