@@ -87,7 +87,8 @@ def test_widest_pitch():
                     m.linear_backward(c[1], c[0], w, pre=c[2], act=m.ACT_SILU, need_bias=True)):
         assert same(a, b)
     half = dy[:, :N // 2]
-    for a, b in zip(m.gated_linear_backward(half, x, w, pre), m.gated_linear_backward(half.contiguous(), c[0], w, c[2])):
+    for a, b in zip(m.gated_linear_backward(half, x, w, pre, need_bias=True),
+                    m.gated_linear_backward(half.contiguous(), c[0], w, c[2], need_bias=True)):
         assert same(a, b)
     for a, b in zip(m.rms_norm(x, nw, residual=dy[:, :K]), m.rms_norm(c[0], nw, residual=c[1][:, :K].contiguous())):
         assert same(a, b)
