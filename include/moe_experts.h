@@ -372,6 +372,7 @@ typedef struct {
  * Root-mean-square norm with the residual's addition.  Per row:
  *   h = x + residual, rounded to dtype (h = x without a residual);
  *   rstd = 1 / sqrt(mean_j h_j^2 + eps);   y_j = h_j * rstd * weight_j.
+ * (The sum of squares is float32: where it passes 3.4e38 rstd is 0.)
  * The 8-bit output takes the same y in float32, before any rounding, by the rule of
  * moe_quantize_rows_fp8 (scale amax / 448 per 128 columns, 1 for a group where that is zero; codes
  * saturate at 448): the rows moe_experts_forward_quantized takes.

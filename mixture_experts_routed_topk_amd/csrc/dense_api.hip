@@ -87,10 +87,11 @@ Backward backward_of(const moe_gated_problem& p) {
 bool dz_is_dy(const Backward& b) {
   return !b.gated && b.act == MOE_ACT_NONE && b.dy_dtype == b.dtype && b.N % 8 == 0 && b.ldy % 8 == 0;
 }
-// With few rows the products take dz in two bf16 parts, its rounding and what that took: the
-// rounding's error does not average out over so few rows (T = 2, 104 gated columns: dw off by
-// 2.6e-3 of its norm, 1.7e-3 of it from its own rounding; from some 20 rows on 2.3 to 2.4e-3).  Up to 32 rows one
-// 64-row tile holds both parts, so the weights are read once; the sum of the parts costs 2 to 5 us (16 rows, gated
+// With few rows the products take dz in two bf16 parts, its rounding and what that took.  One part puts dw off by 2.3 to
+// 2.6e-3 of its norm at any number of rows, 1.7e-3 of it from its own rounding; two leave the 1.7e-3.  Many rows do without:
+// the products are bound by the MFMA and would take twice as long.  Few rows are bound by the weights, and up to 32
+// one 64-row tile holds both parts, so the weights are read once: the limit is where that ends, and with 33 rows the
+// gradients have the precision of many.  The sum of the parts costs 2 to 5 us (16 rows, gated
 // 2048 x 1408: 19.6 against 15.9 us, 7168 x 2048: 37.6 against 34.6).
 constexpr int64_t kTwoPartRows = 32;
 bool dz_in_two_parts(const Backward& b) {

@@ -27,7 +27,7 @@ struct JoinCost {
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 
 // The last round of 256-row tiles runs as halves when those find a CU each (8192 x 2048 x 7168, 3.5 rounds:
-// 247 -> 235 us; 0.7 to 0.8 of a whole tile's time).  The plan does not count on it: in 16 of 16 products where
+// 247 -> 235 us a call, 277 -> 267 in calls back to back; 0.7 to 0.8 of a whole tile's time).  The plan does not count on it: in 16 of 16 products where
 // that would have moved the choice from 128-row tiles these stayed faster, by 1 to 14%.
 inline int64_t whole_tiles(int rows, int64_t tiles) { return rows == 256 && tiles % 256 <= 128 ? tiles / 256 * 256 : tiles; }
 
