@@ -420,14 +420,22 @@ __device__ __forceinline__ void join(const Job& job, int64_t i) {
   const EpiBias<T, GATED> bias(job.g.e, n);
   const EpiRes res = epi_res<T>(job.g.e, m, job.g.M, n);
   float z[8] = {}, u[8] = {};
-  for (int s = 0; s < job.splits; ++s) {
+  const bool pairs = !GATED && job.second_parts;
+  for (int s = 0; pairs && s < job.splits; s += 2) {   // (where the first part gave no finite sum, that is the result)
+    float v[8], rest[8];
+    const int64_t at = ((int64_t)s * job.g.M + m) * job.ldpart + n;
+    Piece<float>::load(job.part, at, v);
+    Piece<float>::load(job.part, at + job.g.M * job.ldpart, rest);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      z[j] += v[j];
+      z[j] += fabsf(z[j]) < INFINITY ? rest[j] : 0.f;
+    }
+  }
+  for (int s = 0; !pairs && s < job.splits; ++s) {
     float v[8];
     const int64_t at = ((int64_t)s * job.g.M + m) * job.ldpart + n;
     Piece<float>::load(job.part, at, v);
-    if (!GATED && job.second_parts && (s & 1)) {   // (where the first part gave no finite sum, that is the result)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fabsf(z[j]) < INFINITY ? v[j] : 0.f;
-    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] += v[j];
     if constexpr (GATED) {
