@@ -491,6 +491,143 @@ moe_status moe_gated_linear_backward(const moe_gated_problem* p, const void* da,
                                      const void* pre, void* dx, void* dw, void* dbias, void* workspace,
                                      size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Rows in expert order and back.  For layers whose experts run on sorted rows as calls of their
+ * own (training, e4m3 experts one product at a time): moe_route's or moe_route_logits' inv gives
+ * every slot's sorted position.  The conventions are those of the dense operators above.
+ * ------------------------------------------------------------------------------------- */
+
+typedef struct {
+  int64_t T;          /* tokens, 0 .. 2^22 - 1                                             */
+  int64_t rows;       /* rows of the sorted matrix, 0 .. 2^31 - 1                          */
+  int32_t H;          /* row length, a multiple of 8 (e4m3: of 128), .. 65536              */
+  int32_t k;          /* slots of a token, 1 .. 1024                                       */
+  int32_t dtype;      /* moe_dtype of the rows: MOE_F32, MOE_BF16; moe_permute alone also MOE_FP8_E4M3 */
+  int64_t ldt;        /* pitch of the tokens' rows (x, out, dout)  a multiple of 8 (e4m3: 16), or 0 */
+  int64_t ldy;        /* pitch of the sorted rows (y, dy)          a multiple of 8 (e4m3: 16), or 0 */
+} moe_permute_problem;
+
+/*
+ * y[inv[t*k + j]] = x[t] for every slot (t, j) with a position: 0 <= inv < rows (others, -1 among them, are left out).
+ * Rows of y that no slot names are left as they were.  Positions are distinct, as moe_route leaves them.
+ *
+ *   x [T, H], inv [T*k] int32, y [rows, H] out
+ *   x_scale [T, H/128] and y_scale [rows, H/128] float32, packed: the scales of e4m3 rows, moved along; both or neither
+ * The gradient of x is moe_unpermute of y's gradient without weights.
+ */
+moe_status moe_permute(const moe_permute_problem* p, const void* x, const float* x_scale, const int32_t* inv, void* y,
+                       float* y_scale, void* stream);
+
+/*
+ * out[t] = sum_j topk_w[t, j] y[inv[t*k + j]] over the slots with a position, in slot order, float32 sums rounded once; a
+ * token without any gets zeros.
+ *
+ *   y [rows, H], inv [T*k] int32, topk_w [T, k] float32 or NULL (weights of 1), out [T, H]
+ */
+moe_status moe_unpermute(const moe_permute_problem* p, const void* y, const int32_t* inv, const float* topk_w, void* out,
+                         void* stream);
+
+/*
+ * Gradients of moe_unpermute:  dy[inv[t*k + j]] = topk_w[t, j] dout[t];  dtopk_w[t, j] = <dout[t], y[inv[t*k + j]]>, 0 for a
+ * slot without a position.  Rows of dy that no slot names are left as they were.
+ *
+ *   dout [T, H]; y [rows, H] (needed for dtopk_w alone); topk_w [T, k] or NULL
+ *   dy [rows, H] out or NULL; may be y itself, which it then replaces;  dtopk_w [T, k] float32 out or NULL
+ */
+moe_status moe_unpermute_backward(const moe_permute_problem* p, const void* dout, const void* y, const int32_t* inv,
+                                  const float* topk_w, void* dy, float* dtopk_w, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * e4m3 matrix products with a scale for each block of 128: the dense operators on the weights of fp8
+ * experts, for one matrix (a shared expert) or for all experts on sorted rows, with gradients.
+ * The conventions are those of the dense operators above.
+ *
+ * x arrives as moe_rms_norm's 8-bit output, moe_quantize_rows_fp8 or moe_permute leave it: codes and one float32
+ * scale per row and 128 columns.  Weights are codes with one scale per 128 x 128 block.  A slice
+ * of 128 products is summed by the block-scaled MFMA, to within 2^-10 of its largest product; slices are added in
+ * float32.  Results are rounded once to bf16.
+ *
+ * With E != 0 expert e multiplies rows offsets[e] .. offsets[e+1] - 1 of x by its own matrix: the offsets of
+ * moe_route, int32, non-decreasing, at most T.  (Others are taken into [0, T] and made non-decreasing.)  Rows of y, a, pre
+ * and dx that belong to no expert are left as they were.
+ * ------------------------------------------------------------------------------------- */
+
+typedef struct {
+  int64_t T;          /* rows, 0 .. 2^22 - 1                                               */
+  int32_t K;          /* inputs, a multiple of 128, 128 .. 65536                           */
+  int32_t N;          /* outputs (gated: I), a multiple of 128, 128 .. 65536               */
+  int32_t E;          /* experts, 1 .. 1024, or 0: one matrix for all rows                 */
+  int32_t scale_fmt;  /* moe_scale_fmt of the weights: MOE_SCALE_F32 or MOE_SCALE_UE8M0    */
+  int32_t act;        /* moe_act; linear with E != 0: MOE_ACT_NONE; gated: SILU, GELU or RELU */
+  int64_t ldx;        /* pitch of x (codes, or bf16 in a backward call)  a multiple of 16, or 0 */
+  int64_t ldy;        /* pitch of y or a (backward: of dy or da)  a multiple of 8, or 0    */
+  int64_t ldr;        /* pitch of residual                        a multiple of 8, or 0    */
+  int64_t ldp;        /* pitch of pre (gated: rows of 2N)         a multiple of 8, or 0    */
+  int64_t lddx;       /* pitch of dx                              a multiple of 8, or 0    */
+} moe_fp8_problem;
+
+/*
+ * Weights to e4m3 with one scale per 128 x 128 block, for `count` matrices [N, K] (N, K multiples of 128) one after the other.
+ * The block's scale is amax / 448: float32, correctly rounded (MOE_SCALE_F32), or the smallest power of two that is not
+ * below it, at least 2^-126 (MOE_SCALE_UE8M0); 1 for a block of zeros.  Codes as in moe_quantize_rows_fp8.
+ *
+ *   w [count, N, K] in dtype (MOE_F32 or MOE_BF16); q [count, N, K] uint8 out
+ *   scales [count, N/128, K/128] float32, or uint8 exponents, out
+ */
+moe_status moe_quantize_blocks_fp8(const void* w, int32_t dtype, int32_t count, int32_t N, int32_t K, int32_t scale_fmt,
+                                   uint8_t* q, void* scales, void* stream);
+
+/* Bytes of workspace of moe_linear_fp8 (backward == MOE_FORWARD) or moe_linear_fp8_backward. */
+moe_status moe_linear_fp8_workspace_size(const moe_fp8_problem* p, int backward, size_t* bytes);
+
+/*
+ * z = x w^T + bias;  y = act(z) + residual.
+ *
+ *   x_q [T, K] codes, x_scale [T, K/128] float32; w_q [N, K] codes, w_scale [N/128, K/128] (each with E first when E != 0)
+ *   offsets [E+1] int32, or NULL with E == 0
+ *   bias [N], residual [T, N], pre [T, N] out (z in bf16): each may be NULL, and is with E != 0 (MOE_ERR_UNSUPPORTED)
+ *   y [T, N] bf16 out; may be residual itself (same pitch), which it then replaces
+ */
+moe_status moe_linear_fp8(const moe_fp8_problem* p, const uint8_t* x_q, const float* x_scale, const uint8_t* w_q,
+                          const void* w_scale, const int32_t* offsets, const void* bias, const void* residual, void* y,
+                          void* pre, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of moe_linear_fp8:  dz = dy * act'(pre);  dx = dz w;  dw = dz^T x;  dbias = sum_t dz.
+ * w is the codes times their scales, x the bf16 rows that were quantised for the forward.  The products take e4m3: dz in
+ * groups of 128 of its columns for dx; dz and x in groups of 128 of their rows (counted from the expert's
+ * first) for dw.  These groups' scales are the smallest powers of two that are not below amax / 448, at least 2^-126 (1 for a
+ * group of zeros); a value that is not finite has the NaN code.  dbias sums the float32 dz.
+ *
+ *   dy [T, N], x [T, K], pre [T, N] bf16 (pre is not read with MOE_ACT_NONE)
+ *   dx [T, K], dw [E, N, K], dbias [N] bf16 out; each may be NULL, and then is not computed; w_q, w_scale
+ *   (without dx) and x (without dw) may be NULL too; dbias is NULL with E != 0 (MOE_ERR_UNSUPPORTED)
+ * An expert without rows gets zeros in dw.
+ */
+moe_status moe_linear_fp8_backward(const moe_fp8_problem* p, const void* dy, const void* x, const uint8_t* w_q,
+                                   const void* w_scale, const int32_t* offsets, const void* pre, void* dx, void* dw,
+                                   void* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of moe_gated_linear_fp8 (backward == MOE_FORWARD) or moe_gated_linear_fp8_backward. */
+moe_status moe_gated_linear_fp8_workspace_size(const moe_fp8_problem* p, int backward, size_t* bytes);
+
+/*
+ * [gate | up] = x w_gate_up^T;  a = act(gate) * up.  w_gate_up_q [2N, K], rows [0, N) gate, as one routed expert's weights.
+ *
+ *   a [T, N] bf16 out;  pre [T, 2N] bf16 out or NULL: [gate | up], what the backward pass reads
+ */
+moe_status moe_gated_linear_fp8(const moe_fp8_problem* p, const uint8_t* x_q, const float* x_scale, const uint8_t* w_gate_up_q,
+                                const void* w_scale, const int32_t* offsets, void* a, void* pre, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of moe_gated_linear_fp8:  dz = [da * up * act'(gate) | da * act(gate)];  dx = dz w_gate_up;  dw = dz^T x, in e4m3 as
+ * in moe_linear_fp8_backward.   da [T, N], x [T, K], pre [T, 2N];  dx [T, K], dw [E, 2N, K] out or NULL
+ */
+moe_status moe_gated_linear_fp8_backward(const moe_fp8_problem* p, const void* da, const void* x, const uint8_t* w_gate_up_q,
+                                         const void* w_scale, const int32_t* offsets, const void* pre, void* dx, void* dw,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,8 +20,9 @@ import torch
 __all__ = [
     "experts_forward", "experts_forward_noalloc", "check_scales", "check_mfma_blocks", "route", "route_logits", "quantize_rows_fp8", "workspace_size", "plan_describe",
     "experts_forward_quantized", "rms_norm", "rms_norm_fp8", "rms_norm_backward", "linear", "linear_backward",
-    "gated_linear", "gated_linear_backward", "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_RELU",
-    "Problem", "NormProblem", "LinearProblem", "GatedProblem", "MoeError", "lib", "FLAG_CHECK_INDICES", "FLAG_DETERMINISTIC", "FLAG_ATOMIC_COMBINE", "FLAG_ACT_GELU", "FLAG_ACT_RELU",
+    "gated_linear", "gated_linear_backward", "permute", "permute_backward", "unpermute", "unpermute_backward",
+    "quantize_blocks_fp8", "linear_fp8", "linear_fp8_backward", "gated_linear_fp8", "gated_linear_fp8_backward", "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_RELU",
+    "Problem", "NormProblem", "LinearProblem", "GatedProblem", "PermuteProblem", "Fp8Problem", "MoeError", "lib", "FLAG_CHECK_INDICES", "FLAG_DETERMINISTIC", "FLAG_ATOMIC_COMBINE", "FLAG_ACT_GELU", "FLAG_ACT_RELU",
     "FLAG_FORCE_GROUPED", "FLAG_FORCE_DECODE", "LIB_PATH",
 ]
 
@@ -50,7 +51,10 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_workspace_size", "moe_exper
            "moe_noalloc_scratch_bytes", "moe_experts_forward_quantized",
            "moe_rms_norm", "moe_rms_norm_workspace_size", "moe_rms_norm_backward",
            "moe_linear", "moe_linear_workspace_size", "moe_linear_backward",
-           "moe_gated_linear", "moe_gated_linear_workspace_size", "moe_gated_linear_backward"]
+           "moe_gated_linear", "moe_gated_linear_workspace_size", "moe_gated_linear_backward",
+           "moe_permute", "moe_unpermute", "moe_unpermute_backward", "moe_quantize_blocks_fp8",
+           "moe_linear_fp8", "moe_linear_fp8_workspace_size", "moe_linear_fp8_backward",
+           "moe_gated_linear_fp8", "moe_gated_linear_fp8_workspace_size", "moe_gated_linear_fp8_backward"]
 
 # stage ids (moe_set_stage_events)
 STAGES = ["zero", "route", "quant_x", "gate_up", "quant_act", "down", "finalize"]
@@ -78,6 +82,17 @@ class GatedProblem(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("act", ctypes.c_int32), ("ldx", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldp", ctypes.c_int64),
                 ("lddx", ctypes.c_int64)]
+
+
+class PermuteProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("rows", ctypes.c_int64), ("H", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("ldt", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class Fp8Problem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("scale_fmt", ctypes.c_int32), ("act", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("ldr", ctypes.c_int64), ("ldp", ctypes.c_int64), ("lddx", ctypes.c_int64)]
 
 
 class MoeError(RuntimeError):
@@ -125,7 +140,9 @@ def lib():
     L.moe_experts_forward_quantized.restype = ctypes.c_int
     L.moe_experts_forward_quantized.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     PN, PL, PG = (ctypes.POINTER(c) for c in (NormProblem, LinearProblem, GatedProblem))
+    PP, P8 = ctypes.POINTER(PermuteProblem), ctypes.POINTER(Fp8Problem)
     pz = ctypes.POINTER(sz)
+    i32 = ctypes.c_int32
     for fn, args in ((L.moe_rms_norm, [PN] + [vp] * 9), (L.moe_rms_norm_workspace_size, [PN, pz]),
                      (L.moe_rms_norm_backward, [PN] + [vp] * 8 + [sz, vp]),
                      (L.moe_linear, [PL] + [vp] * 7 + [sz, vp]),
@@ -133,7 +150,16 @@ def lib():
                      (L.moe_linear_backward, [PL] + [vp] * 8 + [sz, vp]),
                      (L.moe_gated_linear, [PG] + [vp] * 6 + [sz, vp]),
                      (L.moe_gated_linear_workspace_size, [PG, ctypes.c_int, pz]),
-                     (L.moe_gated_linear_backward, [PG] + [vp] * 8 + [sz, vp])):
+                     (L.moe_gated_linear_backward, [PG] + [vp] * 8 + [sz, vp]),
+                     (L.moe_permute, [PP] + [vp] * 6), (L.moe_unpermute, [PP] + [vp] * 5),
+                     (L.moe_unpermute_backward, [PP] + [vp] * 7),
+                     (L.moe_quantize_blocks_fp8, [vp] + [i32] * 5 + [vp] * 3),
+                     (L.moe_linear_fp8, [P8] + [vp] * 10 + [sz, vp]),
+                     (L.moe_linear_fp8_workspace_size, [P8, ctypes.c_int, pz]),
+                     (L.moe_linear_fp8_backward, [P8] + [vp] * 10 + [sz, vp]),
+                     (L.moe_gated_linear_fp8, [P8] + [vp] * 8 + [sz, vp]),
+                     (L.moe_gated_linear_fp8_workspace_size, [P8, ctypes.c_int, pz]),
+                     (L.moe_gated_linear_fp8_backward, [P8] + [vp] * 9 + [sz, vp])):
         fn.restype = ctypes.c_int
         fn.argtypes = args
     L.moe_set_stage_events.restype = ctypes.c_int
@@ -453,7 +479,7 @@ def check_mfma_blocks(a: torch.Tensor, b: torch.Tensor, b_scale: Optional[torch.
 # (Decode steps make these calls by the thousand, each a few microseconds of GPU time: the checks
 # below take the common case in one comparison and say what is wrong only after it fails.)
 # `workspace`, where a call takes one, is any contiguous tensor of at least the bytes that lib()'s moe_*_workspace_size
-# gives for the NormProblem, LinearProblem or GatedProblem; calls that may overlap take different ones.  Without
+# gives for the NormProblem, LinearProblem, GatedProblem or Fp8Problem; calls that may overlap take different ones.  Without
 # it each call takes its own from torch's allocator.
 
 
@@ -703,3 +729,256 @@ def gated_linear_backward(da: torch.Tensor, x: torch.Tensor, w_gate_up: torch.Te
               _rows("pre", pre, T, 2 * I, x.dtype, dev), 0)
     return _backward("moe_gated_linear_backward", GatedProblem, fields, da, x, w_gate_up, pre, 2 * I, need_bias,
                      workspace, dev)
+
+
+# ----------------------------------------------------------------------------- rows in expert order
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _positions(inv: torch.Tensor, T: int, dev: int) -> int:
+    """Checks the sorted positions of T tokens' slots; returns the slots of a token."""
+    if not isinstance(inv, torch.Tensor) or inv.dtype is not torch.int32:
+        raise ValueError("inv must be an int32 tensor")
+    if inv.get_device() != dev or inv.device.type != "cuda":
+        raise ValueError(f"inv is on {inv.device}, the call's other tensors on cuda:{dev}")
+    if not inv.is_contiguous():
+        raise ValueError("inv must be contiguous")
+    n = inv.numel()
+    if T == 0 or n == 0 or n % T:
+        if T == 0 and n == 0:
+            return 1
+        raise ValueError(f"inv must have k entries for each of {T} tokens, got {n}")
+    return n // T
+
+
+def _into(name: str, out: Optional[torch.Tensor], like: torch.Tensor, rows: int, cols: int, dev: int):
+    """(tensor, pitch): the caller's output rows, or new ones."""
+    if out is None:
+        return like.new_empty((rows, cols)), 0
+    return out, _rows(name, out, rows, cols, like.dtype, dev)
+
+
+def permute(x: torch.Tensor, inv: torch.Tensor, rows: Optional[int] = None, scale: Optional[torch.Tensor] = None,
+            out: Optional[torch.Tensor] = None):
+    """(y, y_scale): y[inv[t*k + j]] = x[t], the tokens' rows in expert order, for inv [T*k] int32 as route and
+    route_logits return it (-1: no row).  x [T,H] bf16 or float32, or e4m3 codes (uint8 or float8_e4m3fn) with scale
+    [T,H/128] float32, which is moved along (y_scale; None otherwise).  y has `rows` rows (default T*k, or out's); those that no
+    slot names are left as they were in `out`, and unset without it.  See moe_permute."""
+    if isinstance(x, torch.Tensor) and x.dtype in _CODES:
+        if x.device.type != "cuda" or x.dim() != 2:
+            raise ValueError("x must be a GPU tensor of two dimensions")
+        dt, dev = FP8_E4M3, x.get_device()
+    else:
+        dt, dev = _matrix("x", x)
+    T, H = x.shape
+    k = _positions(inv, T, dev)
+    ldt = _rows("x", x, T, H, x.dtype, dev)
+    if rows is None:
+        rows = inv.numel() if out is None else out.shape[0]
+    y, ldy = _into("out", out, x, rows, H, dev)
+    y_scale = None
+    if scale is not None:
+        if dt != FP8_E4M3 or H % 128:
+            raise ValueError("scales come with e4m3 codes of H a multiple of 128")
+        _packed("scale", scale, (T, H // 128), torch.float32, dev)
+        y_scale = scale.new_empty((rows, H // 128))
+    prob, _ = _problem(PermuteProblem, (T, rows, H, k, dt, ldt, ldy))
+    _run(lib().moe_permute, dev, prob, x.data_ptr(), _addr(scale), inv.data_ptr(), y.data_ptr(), _addr(y_scale))
+    return y, y_scale
+
+
+def permute_backward(dy: torch.Tensor, inv: torch.Tensor, T: int) -> torch.Tensor:
+    """dx [T,H] of permute from dy [rows,H]: dx[t] = sum_j dy[inv[t*k + j]]."""
+    return _unpermute("dy", dy, inv, None, T)
+
+
+def unpermute(y: torch.Tensor, inv: torch.Tensor, topk_w: torch.Tensor) -> torch.Tensor:
+    """out[t] = sum_j topk_w[t,j] y[inv[t*k + j]] [T,H]: rows in expert order back to their tokens, weighted.  y [rows,H]
+    bf16 or float32, inv [T*k] int32, topk_w [T,k] float32; see moe_unpermute."""
+    if not isinstance(topk_w, torch.Tensor) or topk_w.dim() != 2:
+        raise ValueError("topk_w must be a tensor of two dimensions")
+    return _unpermute("y", y, inv, topk_w, topk_w.shape[0])
+
+
+def _unpermute(name, y, inv, topk_w, T):
+    dt, dev = _matrix(name, y)
+    rows, H = y.shape
+    k = _positions(inv, T, dev)
+    if topk_w is not None:
+        _packed("topk_w", topk_w, (T, topk_w.shape[1] if T == 0 else k), torch.float32, dev)
+    prob, _ = _problem(PermuteProblem, (T, rows, H, k, dt, 0, _rows(name, y, rows, H, y.dtype, dev)))
+    out = y.new_empty((T, H))
+    _run(lib().moe_unpermute, dev, prob, y.data_ptr(), inv.data_ptr(), _addr(topk_w), out.data_ptr())
+    return out
+
+
+def unpermute_backward(dout: torch.Tensor, y: torch.Tensor, inv: torch.Tensor, topk_w: torch.Tensor,
+                       out: Optional[torch.Tensor] = None):
+    """(dy, dtopk_w) of unpermute: dy[inv[t*k + j]] = topk_w[t,j] dout[t] in `out` (y itself allowed) or a new tensor,
+    whose other rows are left as they were or unset; dtopk_w[t,j] = <dout[t], y[inv[t*k + j]]> float32.  See
+    moe_unpermute_backward."""
+    dt, dev = _matrix("dout", dout)
+    T, H = dout.shape
+    if not isinstance(y, torch.Tensor) or y.dim() != 2:
+        raise ValueError("y must be a tensor of two dimensions")
+    rows = y.shape[0]
+    k = _positions(inv, T, dev)
+    ldy = _rows("y", y, rows, H, dout.dtype, dev)
+    if not isinstance(topk_w, torch.Tensor) or topk_w.dim() != 2:
+        raise ValueError("topk_w must be a tensor of two dimensions")
+    _packed("topk_w", topk_w, (T, topk_w.shape[1] if T == 0 else k), torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(y)
+        if out.stride() != y.stride():
+            out = torch.empty_strided(y.shape, y.stride(), dtype=y.dtype, device=y.device)
+    elif _rows("out", out, rows, H, dout.dtype, dev) != ldy:
+        raise ValueError("out must have y's row pitch")
+    dw = torch.empty_like(topk_w)
+    prob, _ = _problem(PermuteProblem, (T, rows, H, k, dt, _rows("dout", dout, T, H, dout.dtype, dev), ldy))
+    _run(lib().moe_unpermute_backward, dev, prob, dout.data_ptr(), y.data_ptr(), inv.data_ptr(), topk_w.data_ptr(),
+         out.data_ptr(), dw.data_ptr())
+    return out, dw
+
+
+# ----------------------------------------------------------------------------- e4m3 products
+
+def quantize_blocks_fp8(w: torch.Tensor, ue8m0: bool = False):
+    """(codes, scales) of weights [N,K] or [E,N,K] (bf16 or float32, N and K multiples of 128): e4m3 codes (uint8) with one
+    scale per 128 x 128 block, float32 or, with ue8m0, uint8 exponents of powers of two; see moe_quantize_blocks_fp8."""
+    if not isinstance(w, torch.Tensor) or w.dtype not in _ACT or w.dim() not in (2, 3):
+        raise ValueError("w must be a bf16 or float32 tensor of two or three dimensions")
+    _need_gpu("w", w)
+    N, K = w.shape[-2:]
+    if N % 128 or K % 128:
+        raise ValueError("both sides of a weight matrix must be multiples of 128")
+    count = w.shape[0] if w.dim() == 3 else 1
+    q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(w.shape[:-2] + (N // 128, K // 128), dtype=torch.uint8 if ue8m0 else torch.float32, device=w.device)
+    _run(lib().moe_quantize_blocks_fp8, w.get_device(), w.data_ptr(), _ACT[w.dtype], count, N, K,
+         SCALE_UE8M0 if ue8m0 else SCALE_F32, q.data_ptr(), scales.data_ptr())
+    return q, scales
+
+
+def _fp8_weights(w_q, w_scale, offsets, gated: bool, dev: int):
+    """(K, N, E, scale_fmt) of e4m3 weights [cols,K], or [E,cols,K] with offsets."""
+    if not isinstance(w_q, torch.Tensor) or w_q.dtype not in _CODES:
+        raise ValueError("w_q must be a tensor of e4m3 codes (uint8 or float8_e4m3fn)")
+    if w_q.dim() != (2 if offsets is None else 3):
+        raise ValueError("w_q must be [N,K], or [E,N,K] with offsets")
+    _packed("w_q", w_q, tuple(w_q.shape), w_q.dtype, dev)
+    E = 0 if offsets is None else w_q.shape[0]
+    cols, K = w_q.shape[-2:]
+    if K % 128 or cols % (256 if gated else 128):
+        raise ValueError("both sides of a weight matrix must be multiples of 128")
+    if not isinstance(w_scale, torch.Tensor) or w_scale.dtype not in (torch.float32, torch.uint8):
+        raise ValueError("w_scale must be a float32 or uint8 (UE8M0) tensor")
+    _packed("w_scale", w_scale, tuple(w_q.shape[:-2]) + (cols // 128, K // 128), w_scale.dtype, dev)
+    if offsets is not None:
+        if E == 0:
+            raise ValueError("w_q must have at least one expert")
+        _packed("offsets", offsets, (E + 1,), torch.int32, dev)
+    return K, cols // 2 if gated else cols, E, SCALE_UE8M0 if w_scale.dtype is torch.uint8 else SCALE_F32
+
+
+def _fp8_rows(x_q, x_scale):
+    if not isinstance(x_q, torch.Tensor) or x_q.dtype not in _CODES or x_q.dim() != 2:
+        raise ValueError("x_q must be a 2-D tensor of e4m3 codes (uint8 or float8_e4m3fn)")
+    if x_q.device.type != "cuda":
+        raise ValueError(f"x_q must be a GPU tensor (got {x_q.device})")
+    T, K = x_q.shape
+    dev = x_q.get_device()
+    if K % 128:
+        raise ValueError("x_q's columns must be a multiple of 128")
+    _packed("x_scale", x_scale, (T, K // 128), torch.float32, dev)
+    return T, K, dev, _rows("x_q", x_q, T, K, x_q.dtype, dev)
+
+
+def linear_fp8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None, act: int = ACT_NONE,
+               save_pre: bool = False, offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None):
+    """(y, pre): y = act(x w^T + bias) + residual in bf16 from e4m3 codes with their scales, and pre = x w^T + bias when save_pre
+    (else None).  x_q [T,K] and x_scale [T,K/128] as quantize_rows_fp8 and rms_norm_fp8 return them; w_q [N,K] and w_scale
+    [N/128,K/128] (float32, or uint8 UE8M0 exponents).  With offsets [E+1] (int32, as route returns them) expert e multiplies
+    rows offsets[e] .. offsets[e+1]-1 by w_q[e] of [E,N,K]; bias, residual, act and save_pre are for one matrix, and rows of no
+    expert are left as they were in `out`, and unset without it.  See moe_linear_fp8."""
+    T, K, dev, ldx = _fp8_rows(x_q, x_scale)
+    Kw, N, E, fmt = _fp8_weights(w_q, w_scale, offsets, False, dev)
+    if Kw != K:
+        raise ValueError(f"w_q has {Kw} inputs, x_q {K} columns")
+    if bias is not None:
+        _packed("bias", bias, (N,), torch.bfloat16, dev)
+    ldr = 0 if residual is None else _rows("residual", residual, T, N, torch.bfloat16, dev)
+    ldy = 0 if out is None else _rows("out", out, T, N, torch.bfloat16, dev)
+    prob, need = _problem(Fp8Problem, (T, K, N, E, fmt, int(act), ldx, ldy, ldr, 0, 0), "moe_linear_fp8_workspace_size", 0)
+    ws, n = _scratch(workspace, need, x_q, dev)
+    y = x_scale.new_empty((T, N), dtype=torch.bfloat16) if out is None else out
+    pre = x_scale.new_empty((T, N), dtype=torch.bfloat16) if save_pre else None
+    _run(lib().moe_linear_fp8, dev, prob, x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _addr(offsets),
+         _addr(bias), _addr(residual), y.data_ptr(), _addr(pre), _addr(ws), n)
+    return y, pre
+
+
+def gated_linear_fp8(x_q: torch.Tensor, x_scale: torch.Tensor, w_gate_up_q: torch.Tensor, w_scale: torch.Tensor,
+                     act: int = ACT_SILU, save_pre: bool = False, offsets: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(a, pre): [gate | up] = x w_gate_up^T, a = act(gate) * up [T,I] in bf16, and pre = [gate | up] [T,2I] when save_pre (else
+    None).  w_gate_up_q [2I,K], or [E,2I,K] with offsets; operands and offsets as in linear_fp8.  See moe_gated_linear_fp8."""
+    T, K, dev, ldx = _fp8_rows(x_q, x_scale)
+    Kw, I, E, fmt = _fp8_weights(w_gate_up_q, w_scale, offsets, True, dev)
+    if Kw != K:
+        raise ValueError(f"w_gate_up_q has {Kw} inputs, x_q {K} columns")
+    ldy = 0 if out is None else _rows("out", out, T, I, torch.bfloat16, dev)
+    prob, need = _problem(Fp8Problem, (T, K, I, E, fmt, int(act), ldx, ldy, 0, 0, 0), "moe_gated_linear_fp8_workspace_size", 0)
+    ws, n = _scratch(workspace, need, x_q, dev)
+    a = x_scale.new_empty((T, I), dtype=torch.bfloat16) if out is None else out
+    pre = x_scale.new_empty((T, 2 * I), dtype=torch.bfloat16) if save_pre else None
+    _run(lib().moe_gated_linear_fp8, dev, prob, x_q.data_ptr(), x_scale.data_ptr(), w_gate_up_q.data_ptr(), w_scale.data_ptr(),
+         _addr(offsets), a.data_ptr(), _addr(pre), _addr(ws), n)
+    return a, pre
+
+
+def _fp8_backward(name, gated, dy, x, w_q, w_scale, pre, act, offsets, out, workspace, *bias):
+    _, dev = _matrix("x", x)
+    if x.dtype is not torch.bfloat16:
+        raise ValueError("x must be bf16")
+    T, K = x.shape
+    Kw, N, E, fmt = _fp8_weights(w_q, w_scale, offsets, gated, dev)
+    if Kw != K:
+        raise ValueError(f"the weights have {Kw} inputs, x {K} columns")
+    ldp = 0
+    if act == ACT_NONE:
+        pre = None
+    elif pre is None:
+        raise ValueError("an activation's gradient needs pre")
+    else:
+        ldp = _rows("pre", pre, T, 2 * N if gated else N, torch.bfloat16, dev)
+    lddx = 0 if out is None else _rows("out", out, T, K, torch.bfloat16, dev)
+    fields = (T, K, N, E, fmt, int(act), _rows("x", x, T, K, torch.bfloat16, dev), _rows("dy", dy, T, N, torch.bfloat16, dev), 0,
+              ldp, lddx)
+    prob, need = _problem(Fp8Problem, fields, f"moe_{name}_workspace_size", 1 if any(bias) else 2)
+    ws, n = _scratch(workspace, need, x, dev)
+    dx = x.new_empty((T, K)) if out is None else out
+    dw = torch.empty(w_q.shape, dtype=torch.bfloat16, device=w_q.device)
+    db = [x.new_empty(N) if b else None for b in bias]
+    _run(getattr(lib(), f"moe_{name}_backward"), dev, prob, dy.data_ptr(), x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(),
+         _addr(offsets), _addr(pre), dx.data_ptr(), dw.data_ptr(), *[_addr(t) for t in db], _addr(ws), n)
+    return (dx, dw, *db)
+
+
+def linear_fp8_backward(dy: torch.Tensor, x: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor,
+                        pre: Optional[torch.Tensor] = None, act: int = ACT_NONE, need_bias: bool = False,
+                        offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None):
+    """(dx, dw, dbias) of linear_fp8 in bf16, dbias None without need_bias, from dy [T,N] and the rows x [T,K] that were quantised
+    for it (both bf16); pre is what linear_fp8 saved (needed with an activation).  The products run in e4m3 with groups of 128;
+    see moe_linear_fp8_backward.  With offsets, rows of dx of no expert are left as they were in `out`, and unset without it."""
+    return _fp8_backward("linear_fp8", False, dy, x, w_q, w_scale, pre, act, offsets, out, workspace, need_bias)
+
+
+def gated_linear_fp8_backward(da: torch.Tensor, x: torch.Tensor, w_gate_up_q: torch.Tensor, w_scale: torch.Tensor,
+                              pre: torch.Tensor, act: int = ACT_SILU, offsets: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(dx, dw) of gated_linear_fp8 from da [T,I], x [T,K] and the pre it saved; as linear_fp8_backward."""
+    return _fp8_backward("gated_linear_fp8", True, da, x, w_gate_up_q, w_scale, pre, act, offsets, out, workspace)

@@ -1,0 +1,449 @@
+// Tiles of the e4m3 products with scales for blocks and groups of 128 (gfx950).
+//
+// out[m][n] = epilogue(sum_kt sr(m, kt) sc(n, kt) sum_{k in slice kt} r[m][k] c[n][k]), r and c e4m3 codes,
+// a slice 128 k, sums in float32.  One 16x16x128 block-scaled MFMA multiplies a slice of a fragment pair; inside it
+// a slice's products meet with an error of at most 2^-10 of the largest one (1.4e-5 of a
+// typical sum), and adding to its accumulator rounds once in float32.
+//   FOLD : scales are float32 (any weights'): each MFMA starts from zero and its result is added times sr * sc, an FMA
+//          an element.  sc is one value per slice and 128 columns (a weight block's).
+//   else : scales are powers of two, bytes by row: the MFMA applies both (a lane passes the bytes of its two
+//          operand rows) and accumulates itself, so no vector work is left.
+//
+// Operands reach LDS by DMA as 128-byte rows, in either storage order (as in dense_tile.h, for bytes):
+//   along k    : a row's 128 k, its eight 16-byte chunks XOR-permuted by the row; a lane's 32 k are two of them
+//   along rows : a k's 128 rows, chunks XOR-permuted by k; a lane's 32 k are four transposing reads
+//                (ds_read_b64_tr_b8: 16 lanes read eight k of 16 rows, and each gets one row's eight k), so that
+//                gradients need no transposed copies of the weights
+// c sits on the MFMA's row side: a lane ends with four consecutive columns per fragment, and two exchanges between lane
+// groups make them eight.
+//
+// Eight waves in a 2 x 4 grid; a wave's columns are 32 of each half of the tile's 256 (gated: 32 gate and the
+// matching 32 up columns).
+//   NH = 2, 256 rows, two slices in LDS.  A slice is four phases of a quadrant (64 rows x 32 columns, eight
+//   MFMAs); as a phase uses its row fragments for the last time it reads the next phase's into their place:
+//     phase   multiplies   reads                  then
+//     0       R0 x C0      C1(kt)                 (first: DMA of R0, scales, C0 of kt + 2)
+//     1       R0 x C1      R1(kt)                 wait for R0, C0(kt+1); barrier
+//     2       R1 x C0                             (first: DMA of C1, R1 of kt + 2)
+//     3       R1 x C1      R0, C0(kt+1)           wait for C1, R1(kt+1); barrier
+//   Each DMA has a slice and a half to land.
+//   NH = 1, 128 rows, three slices in LDS: phases 0 and 1 alone, one barrier and one wait per slice.
+#pragma once
+
+#include <type_traits>
+
+#include "dense_tile.h"
+#include "fp8_internal.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x2v __attribute__((ext_vector_type(2)));
+
+// 16 rows of a 128-row region from row r0 (a multiple of 16), 128 k
+template <bool KM>
+struct Frag8 {
+  uint32_t off[2];
+  int f;
+  __device__ __forceinline__ Frag8(int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    if constexpr (!KM) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) off[h] = (uint32_t)(i * 128 + (((2 * g + h) ^ ((i >> 1) & 7)) << 4));
+    } else {
+      off[0] = (uint32_t)((32 * g + (i >> 1)) * 128 + (i & 1) * 8);
+      f = (i >> 1) ^ (g & 1);
+    }
+  }
+  __device__ __forceinline__ i32x8 load(const char* region, int r0) const {
+    if constexpr (!KM) {
+      const i32x4 a = *reinterpret_cast<const i32x4*>(region + r0 * 128 + off[0]);
+      const i32x4 b = *reinterpret_cast<const i32x4*>(region + r0 * 128 + off[1]);
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      typedef __attribute__((address_space(3))) i32x2v lds2;
+      const uint32_t p = lds_addr(region) + off[0] + (uint32_t)(((r0 >> 4) ^ f) << 4);
+      i32x8 v;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const i32x2v a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2*)(p + t * 1024));
+        v[2 * t] = a[0];
+        v[2 * t + 1] = a[1];
+      }
+      return v;
+    }
+  }
+};
+
+// This lane's DMA sources for the two instructions of a wave in a region (rows: tile rows of the region, clamped)
+template <bool KM>
+struct Stream8 {
+  uint32_t off[2];
+  static __device__ __forceinline__ int chunk_k(int ins, int lane) {
+    if constexpr (KM) return ins * 8 + (lane >> 3);
+    return ((lane & 7) ^ (((ins * 8 + (lane >> 3)) >> 1) & 7)) * 16;
+  }
+  static __device__ __forceinline__ int chunk_row(int ins, int lane) {
+    if constexpr (!KM) return ins * 8 + (lane >> 3);
+    const int k = chunk_k(ins, lane);
+    return ((lane & 7) ^ ((k & 7) ^ ((k >> 5) & 1))) * 16;
+  }
+  template <typename F>
+  __device__ __forceinline__ void init(int first, int lane, int64_t ld, F&& row_of) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int64_t row = row_of(chunk_row(first + q, lane));
+      off[q] = (uint32_t)(KM ? chunk_k(first + q, lane) * ld + row : row * ld + chunk_k(first + q, lane));
+    }
+  }
+  __device__ __forceinline__ void issue(const char* base, uint32_t lds, int q) const { dma_lds_x4(base, off[q], lds); }
+  // (along rows) last slice, `left` k in it
+  __device__ __forceinline__ void issue_tail(const char* base, uint32_t lds, int q, int first, int lane, int left) const {
+    const char* p = chunk_k(first + q, lane) < left ? base + off[q] : reinterpret_cast<const char*>(zero_chunk);
+    dma_lds_x4_at(p, lds);
+  }
+};
+
+struct Fp8Job {
+  Job j;
+  Fp8Scales rs, cs;
+  int c_blocks;
+  int E;
+  int64_t c_expert, cs_expert;
+  Runs runs;
+};
+
+// 2^(b - 127); 255 is NaN
+__device__ __forceinline__ float ue8m0_value(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+}
+
+// Two fragments' four columns per lane into eight consecutive ones: lane group g holds columns 4 g .. 4 g + 3 of
+// both, and gets 8 g .. 8 g + 7 of the 32
+__device__ __forceinline__ void eight_columns(f32x4& a, f32x4& b) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(a[q]), __float_as_uint(b[q]), false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+    a[q] = __uint_as_float(y[0]);
+    b[q] = __uint_as_float(y[1]);
+  }
+}
+
+constexpr int kMaxSlices = 512;         // K <= 65536
+
+template <int NH>
+struct Ring {
+  static constexpr int SLICES = NH == 2 ? 2 : 3;
+  static constexpr int STAGE = (NH + 2) * REGION;                 // R0 [R1] C0 C1
+  static constexpr int SCALES = (128 * NH + 256) * 4;             // a dword per row of r and, for the MFMA, of c
+  static constexpr int TABLE = SLICES * STAGE + 3 * SCALES;       // FOLD: c's block scales, [2 halves][kMaxSlices]
+  static constexpr int BYTES = TABLE + 2 * kMaxSlices * 4;
+};
+
+// One tile: rows m0 .. of which `rows` exist (tile rows past them repeat the last), columns from tile column nt,
+// slices [0, KT) from contraction index k0 with `left` k in the last; c and its scales from expert e.
+template <bool RK, bool CK, int EPI, int NH, bool FOLD>
+__device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_t m0, int64_t rows, int nt, int e, int64_t k0,
+                                         int64_t kt0, int KT, int left, int split, char* lds) {
+  using Rg = Ring<NH>;
+  const DenseGemm& g = job.g;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const int n0 = nt * (EPI == kGated ? 128 : 256);
+  // tile column -> row of c
+  auto c_row = [&](int col) __attribute__((always_inline)) -> int64_t {
+    if constexpr (EPI == kGated) return min(n0 + (col & 127), g.e.N - 1) + (int64_t)(col >> 7) * g.e.N;
+    return min((int64_t)(n0 + col), (int64_t)job.crows - 1);
+  };
+
+  const char* rbase = static_cast<const char*>(g.r) + (RK ? k0 * g.ldr + m0 : m0 * g.ldr + k0);
+  const char* cbase = static_cast<const char*>(g.c) + e * p.c_expert + (CK ? k0 * g.ldc + n0 : n0 * g.ldc + k0);
+  const int64_t rstep = RK ? 128 * g.ldr : 128, cstep = CK ? 128 * g.ldc : 128;
+  // gated: the second column half is the up projection's rows, N rows on (more than 32-bit offsets reach)
+  const char* const chalf[2] = {cbase, cbase + (EPI == kGated ? (int64_t)g.e.N * g.ldc : 0)};
+  Stream8<RK> sr[NH];
+  Stream8<CK> sc[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h < NH)
+      sr[h].init(wave * 2, lane, g.ldr, [&](int row) -> int64_t { return min((int64_t)(h * 128 + row), rows - (RK ? 16 : 1)); });
+    sc[h].init(wave * 2, lane, g.ldc, [&](int row) -> int64_t {
+      if constexpr (EPI == kGated) return min(row, g.e.N - 1 - n0);
+      return min((int64_t)(h * 128 + row), (int64_t)job.crows - n0 - (CK ? 16 : 1));
+    });
+  }
+  // Scales by row, a dword each (64 a wave): FOLD: r's, by waves 0 .. 2 NH - 1 (the others bring the same again); else waves
+  // 0 .. 3 bring r's and 4 .. 7 c's
+  const bool r_wave = FOLD || wave < 4;
+  const int s_row = r_wave ? (wave % (2 * NH)) * 64 + lane : (wave - 4) * 64 + lane;
+  const Fp8Scales& sp = r_wave ? p.rs : p.cs;
+  constexpr int S_SIZE = FOLD ? 4 : 1;
+  const int64_t s_at = r_wave ? (m0 + min((int64_t)s_row, rows - 1)) * sp.row
+                              : e * p.cs_expert + (p.c_blocks ? c_row(s_row) >> 7 : c_row(s_row)) * sp.row;
+  // (a wave's first lane gives the base, so that a lane's offset fits in 32 bits)
+  const int64_t s_first = ((int64_t)__builtin_amdgcn_readfirstlane((int)(s_at >> 32)) << 32) |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)s_at);
+  const char* sbase = static_cast<const char*>(sp.p) + (s_first + kt0 * sp.slice) * S_SIZE;
+  const uint32_t s_off = (uint32_t)((s_at - s_first) * S_SIZE);
+  const uint32_t s_lds = (uint32_t)(Rg::SLICES * Rg::STAGE + (r_wave ? (wave % (2 * NH)) * 256 : NH * 512 + (wave - 4) * 256));
+  const int64_t s_step = sp.slice * S_SIZE;
+  float* const table = reinterpret_cast<float*>(lds + Rg::TABLE);
+  if constexpr (FOLD) {
+    for (int i = threadIdx.x; i < 2 * KT; i += 512) {
+      const int h = i < KT ? 0 : 1, kt = i - h * KT;
+      const int64_t at = e * p.cs_expert + (c_row(h * 128) >> 7) * p.cs.row + (kt0 + kt) * p.cs.slice;
+      table[h * kMaxSlices + kt] = p.cs.bytes ? ue8m0_value(static_cast<const uint8_t*>(p.cs.p)[at])
+                                              : static_cast<const float*>(p.cs.p)[at];
+    }
+  }
+
+  const uint32_t lds0 = lds_addr(lds);
+  // Where slice kt is in the ring, and its scales; `tail`: kt is the last slice and has fewer than 128 k (along rows)
+  auto stage = [&](int kt) __attribute__((always_inline)) -> int { return (NH == 2 ? (kt & 1) : kt % 3) * Rg::STAGE; };
+  auto issue = [&](auto tail, const auto& from, const char* base, int dst) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if constexpr (decltype(tail)::value) from.issue_tail(base, lds0 + (uint32_t)dst + q * 1024, q, wave * 2, lane, left);
+      else from.issue(base, lds0 + (uint32_t)dst + q * 1024, q);
+    }
+  };
+  auto issue_r = [&](auto tail, int h, int kt) __attribute__((always_inline)) {
+    issue(tail, sr[h], rbase + kt * rstep, stage(kt) + h * REGION + wave * 2048);
+  };
+  auto issue_c = [&](auto tail, int h, int kt) __attribute__((always_inline)) {
+    issue(tail, sc[h], chalf[h] + kt * cstep, stage(kt) + (NH + h) * REGION + wave * 2048);
+  };
+  auto issue_s = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + s_lds + (uint32_t)(kt % 3 * Rg::SCALES);
+    if constexpr (FOLD) dma_lds_x1(sbase + kt * s_step, s_off, dst);
+    else dma_lds_u8(sbase + kt * s_step, s_off, dst);
+  };
+  // a slice's DMAs in two parts: R0, scales, C0 (5 instructions) and C1, R1 (4; one row half: 2)
+  auto issue_a = [&](auto tail, int kt) __attribute__((always_inline)) {
+    issue_r(tail, 0, kt), issue_s(kt), issue_c(tail, 0, kt);
+  };
+  auto issue_b = [&](auto tail, int kt) __attribute__((always_inline)) {
+    issue_c(tail, 1, kt);
+    if constexpr (NH == 2) issue_r(tail, 1, kt);
+  };
+  constexpr bool TAIL = RK && CK;
+  typedef std::integral_constant<bool, false> Whole;
+  typedef std::integral_constant<bool, TAIL> Last;
+  auto issue_first = [&](int kt) __attribute__((always_inline)) {      // (in front of the loop)
+    if (kt == KT - 1) issue_a(Last{}, kt), issue_b(Last{}, kt);
+    else issue_a(Whole{}, kt), issue_b(Whole{}, kt);
+  };
+
+  const Frag8<RK> fr(lane);
+  const Frag8<CK> fc(lane);
+  f32x4 acc[NH][2][4][2];
+#pragma unroll
+  for (int a = 0; a < NH; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[a][b][i][j] = f32x4{};
+  i32x8 r[4], c[2][2];
+  const char* const scales = lds + Rg::SLICES * Rg::STAGE;
+  uint32_t rsc[4], csc[2][2];           // FOLD: a half's columns have one scale, csc[h][0]
+  auto read_r = [&](int i, int h, int kt) __attribute__((always_inline)) {
+    r[i] = fr.load(lds + stage(kt) + h * REGION, wm * 64 + i * 16);
+    rsc[i] = *reinterpret_cast<const uint32_t*>(scales + (kt % 3) * Rg::SCALES + (h * 128 + wm * 64 + i * 16 + l16) * 4);
+  };
+  auto read_c = [&](int h, int kt) __attribute__((always_inline)) {
+    const char* s = scales + (kt % 3) * Rg::SCALES + NH * 512 + (h * 128 + wn * 32) * 4;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      c[h][j] = fc.load(lds + stage(kt) + (NH + h) * REGION, wn * 32 + j * 16);
+      if (!FOLD) csc[h][j] = *reinterpret_cast<const uint32_t*>(s + (j * 16 + l16) * 4);
+    }
+    if (FOLD) csc[h][0] = __float_as_uint(table[h * kMaxSlices + min(kt, kMaxSlices - 1)]);
+  };
+  // a phase's products; after(i) reads into fragment i's place
+  f32x4 pr[2][2];
+  float prs[2] = {0.f, 0.f};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) pr[q][0] = pr[q][1] = f32x4{};
+  auto fold = [&](f32x4 (&a)[2], int at) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) a[j][q] = fmaf(pr[at][j][q], prs[at], a[j][q]);
+  };
+  // (FOLD: a fragment's results are folded in after the next one's products are issued; those of a phase's last fragment in
+  // the next phase, so `before` is the accumulator of the phase before)
+  auto multiply = [&](f32x4 (&a)[4][2], f32x4 (&before)[4][2], int h, auto&& after) __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    const float sb = __uint_as_float(csc[h][0]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (FOLD) {
+        const float s = __uint_as_float(rsc[i]) * sb;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) pr[i & 1][j] = mfma_16x16x128_e4m3(c[h][j], r[i], f32x4{});
+        prs[i & 1] = s;
+        fold(i == 0 ? before[3] : a[(i + 3) & 3], (i + 1) & 1);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          a[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(c[h][j], r[i], a[i][j], 0, 0, 0, (int)csc[h][j], 0, (int)rsc[i]);
+      }
+      after(i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto nothing = [](int) __attribute__((always_inline)) {};
+
+  // The loop's body without branches, for slices behind which one is issued (whole, or the last one) or none: across a branch
+  // the compiler moves products behind the DMAs and keeps all their operands in registers
+  enum { kNone, kWhole, kLast };
+  auto body = [&](auto MORE_, int kt) __attribute__((always_inline)) {
+    constexpr int MORE = decltype(MORE_)::value;
+    typedef std::conditional_t<MORE == kLast, Last, Whole> Tail;
+    if constexpr (NH == 2) {
+      if constexpr (MORE != kNone) issue_a(Tail{}, kt + 2);
+      read_c(1, kt);
+      multiply(acc[0][0], acc[1][1], 0, nothing);
+      multiply(acc[0][1], acc[0][0], 1, [&](int i) __attribute__((always_inline)) { read_r(i, 1, kt); });
+      if constexpr (MORE != kNone) wait_vmcnt<9>();   // R0, C0 of kt + 1; younger: C1, R1 of kt + 1 and R0, scales, C0 of kt + 2
+      else wait_vmcnt<0>();
+      wait_lds();
+      barrier();
+      if constexpr (MORE != kNone) issue_b(Tail{}, kt + 2);
+      multiply(acc[1][0], acc[0][1], 0, nothing);
+      read_c(0, kt + 1);                              // (behind the last slice: what the ring holds, not used)
+      multiply(acc[1][1], acc[1][0], 1, [&](int i) __attribute__((always_inline)) { read_r(i, 0, kt + 1); });
+      if constexpr (MORE != kNone) wait_vmcnt<9>();   // C1, R1 of kt + 1; younger: kt + 2
+      else wait_vmcnt<0>();
+      wait_lds();
+      barrier();
+    } else {
+      read_c(1, kt);
+      multiply(acc[0][0], acc[0][1], 0, nothing);
+      if constexpr (MORE != kNone) wait_vmcnt<7>();   // slice kt + 1; younger: kt + 2
+      else wait_vmcnt<0>();
+      wait_lds();                                     // (and every read of slice kt is done)
+      barrier();
+      if constexpr (MORE != kNone) issue_a(Tail{}, kt + 3), issue_b(Tail{}, kt + 3);
+      read_c(0, kt + 1);
+      multiply(acc[0][1], acc[0][0], 1, [&](int i) __attribute__((always_inline)) { read_r(i, 0, kt + 1); });
+    }
+  };
+  constexpr int AHEAD = NH == 2 ? 2 : 3;
+  if (KT > 0) {
+    issue_first(0);
+    if (KT > 1) issue_first(1);
+    if (NH == 1 && KT > 2) issue_first(2);
+    if (KT >= AHEAD) wait_vmcnt<NH == 2 ? 9 : 14>();
+    else wait_vmcnt<0>();
+    wait_lds();                            // (the table's stores)
+    barrier();                             // slice 0 has landed
+#pragma unroll
+    for (int i = 0; i < 4; ++i) read_r(i, 0, 0);
+    read_c(0, 0);
+    wait_lds();
+    barrier();                             // (the first slice's DMAs refill what was just read)
+    int kt = 0;
+    for (; kt + AHEAD + (TAIL ? 1 : 0) < KT; ++kt) body(std::integral_constant<int, kWhole>{}, kt);
+    if (TAIL && kt + AHEAD < KT) body(std::integral_constant<int, kLast>{}, kt++);
+    for (; kt < KT; ++kt) body(std::integral_constant<int, kNone>{}, kt);
+    if constexpr (FOLD) fold(acc[NH - 1][1][3], 1);
+  }
+
+#pragma unroll
+  for (int a = 0; a < NH; ++a) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) eight_columns(acc[a][b][i][0], acc[a][b][i][1]);
+    const int64_t m = m0 + a * 128 + wm * 64 + l16;
+    const int col = n0 + wn * 32 + 8 * g4;
+    if constexpr (EPI == kGated) {
+      store_rows<uint16_t, EPI>(job, split, m, col, acc[a][0], acc[a][1]);
+    } else {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) store_rows<uint16_t, EPI>(job, split, m, col + b * 128, acc[a][b], acc[a][b]);
+    }
+  }
+}
+
+// Forward and dx: rows in tiles, over one matrix (splits along blockIdx.y) or by runs of rows
+template <bool CK, int EPI, int NH, bool FOLD>
+__global__ __launch_bounds__(512, 1) void fp8_rows_tile_kernel(Fp8Job p) {
+  __shared__ __attribute__((aligned(1024))) char lds[Ring<NH>::BYTES];
+  Job job = p.j;
+  if (p.E) job.mt = p.runs.count[0];
+  int mt, nt;
+  if (!tile_of(job, blockIdx.x, mt, nt)) return;
+  int64_t m0 = (int64_t)mt * 128 * NH, rows = job.g.M - m0;
+  int e = 0;
+  if (p.E) {
+    const RowTile t = p.runs.tiles[mt];
+    m0 = t.row0;
+    rows = t.rows;
+    e = t.expert;
+    job.g.M = m0 + rows;
+  }
+  const int64_t kt0 = (int64_t)blockIdx.y * job.slices;
+  const int KT = (int)min((int64_t)job.slices, job.g.K / 128 - kt0);
+  tile_fp8<false, CK, EPI, NH, FOLD>(p, job, m0, rows, nt, e, kt0 * 128, kt0, KT, 128, blockIdx.y, lds);
+}
+
+// dw: contractions over the rows, all of them (splits along blockIdx.y) or each run's (run blockIdx.y)
+template <int NH>
+__global__ __launch_bounds__(512, 1) void fp8_dw_kernel(Fp8Job p) {
+  __shared__ __attribute__((aligned(1024))) char lds[Ring<NH>::BYTES];
+  Job job = p.j;
+  int mt, nt;
+  if (!tile_of(job, blockIdx.x, mt, nt)) return;
+  const int64_t m0 = (int64_t)mt * 128 * NH;
+  int64_t k0, kt0, k;
+  int split = 0;
+  if (p.E) {
+    const int e = blockIdx.y;
+    k0 = p.runs.start[e];
+    k = p.runs.start[e + 1] - k0;
+    kt0 = p.runs.group[e];
+    job.g.e.out = static_cast<uint16_t*>(job.g.e.out) + (int64_t)e * job.g.M * job.g.e.N;
+  } else {
+    split = blockIdx.y;
+    kt0 = (int64_t)split * job.slices;
+    k0 = kt0 * 128;
+    k = min((int64_t)job.slices * 128, job.g.K - k0);
+  }
+  const int KT = (int)((k + 127) / 128);
+  tile_fp8<true, true, kGrad, NH, false>(p, job, m0, job.g.M - m0, nt, 0, k0, kt0, KT, (int)(k - (int64_t)(KT - 1) * 128), split,
+                                         lds);
+}
+
+inline Fp8Job fp8_job(const Fp8Gemm& g, const Job& job) {
+  Fp8Job p{};
+  p.j = job;
+  p.rs = g.rs;
+  p.cs = g.cs;
+  p.c_blocks = g.c_blocks;
+  p.E = g.E;
+  p.c_expert = g.c_expert;
+  p.cs_expert = g.cs_expert;
+  p.runs = g.runs;
+  return p;
+}
+inline dim3 fp8_grid(const Job& job, int y) {
+  return dim3((unsigned)(((int64_t)job.mt * job.nt + 7) / 8 * 8), (unsigned)y);
+}
+
+// Costs of a tile, as in dense_plan.h, in slices of 128 k
+constexpr TileCost kTilesFp8[] = {{256, 256, 1, 1.25, 1.25, 7.0}, {128, 256, 1, 0.8, 0.8, 4.0}};
+constexpr JoinCost kJoinFp8 = {2.8, 3.36e6};
+
+inline Plan plan_fp8(int64_t M, int64_t N, int64_t K, int gated) {
+  return plan_forward<uint8_t>(kTilesFp8, kJoinFp8, M, N, K, gated);
+}
+
+}  // namespace
+}  // namespace moe
