@@ -97,9 +97,9 @@ BackwardLayout backward_layout(const Size& z, bool bias) {
   L.runs = take(z.E ? runs_bytes(z.T, z.E, fp8_grouped_height(z.T, z.E)) : 0);
   L.zr = take(z.T * z.cols);
   L.zr_scale = take(z.T * (z.cols / 128) * 4);
-  L.zc = take(z.T * z.cols);
+  L.zc = take(L.tiles * 128 * z.cols);
   L.zc_scale = take(L.tiles * z.cols);
-  L.xc = take(z.T * z.K);
+  L.xc = take(L.tiles * 128 * z.K);
   L.xc_scale = take(L.tiles * z.K);
   L.part = take(bias ? L.tiles * z.cols * 4 : 0);
   const size_t dx = fp8_dx_workspace(z.T, z.K, z.cols, z.E), dw = fp8_dw_workspace(z.T, z.K, z.cols, z.E);
@@ -236,7 +236,7 @@ moe_status run_backward(const moe_fp8_problem* p, bool gated, const void* dy, co
     g.E = z.E;
     g.runs = runs;
     g.g.M = z.cols;
-    g.g.K = z.T;
+    g.g.K = L.tiles * 128;
     g.g.e.out = dw;
     g.g.e.ldo = z.K;
     g.g.e.N = (int)z.K;

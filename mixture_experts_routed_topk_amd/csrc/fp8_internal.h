@@ -30,7 +30,8 @@ hipError_t launch_runs(const Runs& r, const int32_t* offsets, int64_t T, int E, 
 
 // ---------------------------------------------------------------------------- quantisers
 // What the backward products read.  dz = dy * act'(pre) (gated: [da * up * act'(gate), da * act(gate)]), [T][cols], in
-// groups of 128 columns (zr, for dx) and of 128 rows of its expert (zc, for dw), x in groups of 128 rows (xc).
+// groups of 128 columns (zr, for dx) and of 128 rows of its expert (zc, for dw), x in groups of 128 rows (xc).  zc and xc are
+// stored by 128-row tiles, each with its own 128 rows (zeros past the run's end), so that dw contracts over whole ones.
 // Scales are powers of two: bytes (UE8M0), or float32 for zr with zr_f32.
 struct GroupsArgs {
   int64_t T;
@@ -44,12 +45,12 @@ struct GroupsArgs {
   uint8_t* zr;                  // [T][cols], null without dx
   void* zr_scale;               // [T][cols / 128]
   int zr_f32;
-  uint8_t* zc;                  // [T][cols], null without dw
+  uint8_t* zc;                  // [128-row tiles][128][cols], null without dw
   uint8_t* zc_scale;            // [128-row tiles][cols]
   const void* x;                // bf16
   int64_t ldx;
   int K;
-  uint8_t* xc;                  // [T][K], null without dw
+  uint8_t* xc;                  // [128-row tiles][128][K], null without dw
   uint8_t* xc_scale;            // [128-row tiles][K]
   float* part;                  // [128-row tiles][cols] sums of dz, null without dbias
   const RowTile* tiles;         // null: one run of T rows
@@ -87,7 +88,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t s);
 // r (codes [T][cols]) along k, c along its rows
 size_t fp8_dx_workspace(int64_t T, int64_t K, int64_t cols, int E);
 hipError_t launch_fp8_dx(const Fp8Gemm& g, void* ws, hipStream_t s);
-// both operands along their rows
+// both operands along their rows; g.g.K: rows of all 128-row tiles
 size_t fp8_dw_workspace(int64_t T, int64_t K, int64_t cols, int E);
 hipError_t launch_fp8_dw(const Fp8Gemm& g, void* ws, hipStream_t s);
 

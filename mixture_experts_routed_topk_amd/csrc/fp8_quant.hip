@@ -44,7 +44,7 @@ struct TileOut {
   uint8_t* row_codes;      // null: not wanted
   void* row_scale;         // [rows][C / 128]
   int row_f32;
-  uint8_t* col_codes;      // null: not wanted
+  uint8_t* col_codes;      // of this tile: [128][C], rows past the tile's are zeros; null: not wanted
   uint8_t* col_scale;      // of this tile: [C]
   float* sums;             // of this tile: [C], null: not wanted
 };
@@ -127,11 +127,10 @@ __device__ __forceinline__ void store_tile(const float (&v)[kRows][8], const Til
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const int r = rr + 32 * u;
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = v[u][i] * f[i];
-    if (r < rows) *reinterpret_cast<uint2*>(o.col_codes + (row0 + r) * C + col) = codes8(w, 1.0f);
+    *reinterpret_cast<uint2*>(o.col_codes + (int64_t)(rr + 32 * u) * C + col) = codes8(w, 1.0f);
   }
 }
 
@@ -169,11 +168,11 @@ __global__ __launch_bounds__(kThreads) void groups_kernel(GroupsArgs a, int dz_b
   if ((int)blockIdx.x >= dz_blocks) {
     const int col = ((int)blockIdx.x - dz_blocks) * 128 + sub * 8;
     load_tile(a.x, a.ldx, row0, rows, col, v);
-    store_tile(v, TileOut{nullptr, nullptr, 0, a.xc, a.xc_scale + (int64_t)tile * a.K, nullptr}, row0, rows, col, a.K, red);
+    store_tile(v, TileOut{nullptr, nullptr, 0, a.xc + (int64_t)tile * 128 * a.K, a.xc_scale + (int64_t)tile * a.K, nullptr}, row0, rows, col, a.K, red);
     return;
   }
   const int col = (int)blockIdx.x * 128 + sub * 8;
-  TileOut o{a.zr, a.zr_scale, a.zr_f32, a.zc, a.zc_scale ? a.zc_scale + tile * cols : nullptr,
+  TileOut o{a.zr, a.zr_scale, a.zr_f32, a.zc ? a.zc + tile * 128 * cols : nullptr, a.zc_scale ? a.zc_scale + tile * cols : nullptr,
             a.part ? a.part + tile * cols : nullptr};
   load_tile(a.dy, a.ldy, row0, rows, col, v);
   if constexpr (GATED) {

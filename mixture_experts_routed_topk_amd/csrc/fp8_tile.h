@@ -21,12 +21,12 @@
 // matching 32 up columns).
 //   NH = 2, 256 rows, two slices in LDS.  A slice is four phases of a quadrant (64 rows x 32 columns, eight
 //   MFMAs); as a phase uses its row fragments for the last time it reads the next phase's into their place:
-//     phase   multiplies   reads                  then
-//     0       R0 x C0      C1(kt)                 (first: DMA of R0, scales, C0 of kt + 2)
-//     1       R0 x C1      R1(kt)                 wait for R0, C0(kt+1); barrier
-//     2       R1 x C0                             (first: DMA of C1, R1 of kt + 2)
-//     3       R1 x C1      R0, C0(kt+1)           wait for C1, R1(kt+1); barrier
-//   Each DMA has a slice and a half to land.
+//     phase   multiplies   half way                                               then reads
+//     0       R0 x C0      wait for C1, R1(kt); barrier; DMA of R0, scales, C0(kt+2)   C1(kt)
+//     1       R0 x C1                                                             R1(kt)
+//     2       R1 x C0      wait for R0, C0(kt+1); barrier; DMA of C1, R1(kt+2)
+//     3       R1 x C1                                                             R0, C0(kt+1)
+//   Each DMA has a slice and a half to land, and a barrier comes when the reads before it have long ended.
 //   NH = 1, 128 rows, three slices in LDS: phases 0 and 1 alone, one barrier and one wait per slice.
 #pragma once
 
@@ -40,7 +40,8 @@ namespace {
 
 typedef int i32x2v __attribute__((ext_vector_type(2)));
 
-// 16 rows of a 128-row region from row r0 (a multiple of 16), 128 k
+// 16 rows of a 128-row region from row r0 (a multiple of 16), 128 k: lane group g has k 16 g .. 16 g + 15 and 64 + 16 g .. (for
+// rows along k its chunks g and 4 + g, whose reads meet no bank twice; with chunks 2 g and 2 g + 1 half of them do)
 template <bool KM>
 struct Frag8 {
   uint32_t off[2];
@@ -49,9 +50,9 @@ struct Frag8 {
     const int g = lane >> 4, i = lane & 15;
     if constexpr (!KM) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) off[h] = (uint32_t)(i * 128 + (((2 * g + h) ^ ((i >> 1) & 7)) << 4));
+      for (int h = 0; h < 2; ++h) off[h] = (uint32_t)(i * 128 + (((4 * h + g) ^ (i >> 1)) << 4));
     } else {
-      off[0] = (uint32_t)((32 * g + (i >> 1)) * 128 + (i & 1) * 8);
+      off[0] = (uint32_t)((16 * g + (i >> 1)) * 128 + (i & 1) * 8);
       f = (i >> 1) ^ (g & 1);
     }
   }
@@ -66,7 +67,7 @@ struct Frag8 {
       i32x8 v;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const i32x2v a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2*)(p + t * 1024));
+        const i32x2v a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2*)(p + (t >> 1) * 8192 + (t & 1) * 1024));
         v[2 * t] = a[0];
         v[2 * t + 1] = a[1];
       }
@@ -86,7 +87,7 @@ struct Stream8 {
   static __device__ __forceinline__ int chunk_row(int ins, int lane) {
     if constexpr (!KM) return ins * 8 + (lane >> 3);
     const int k = chunk_k(ins, lane);
-    return ((lane & 7) ^ ((k & 7) ^ ((k >> 5) & 1))) * 16;
+    return ((lane & 7) ^ ((k & 7) ^ ((k >> 4) & 1))) * 16;
   }
   template <typename F>
   __device__ __forceinline__ void init(int first, int lane, int64_t ld, F&& row_of) {
@@ -95,12 +96,6 @@ struct Stream8 {
       const int64_t row = row_of(chunk_row(first + q, lane));
       off[q] = (uint32_t)(KM ? chunk_k(first + q, lane) * ld + row : row * ld + chunk_k(first + q, lane));
     }
-  }
-  __device__ __forceinline__ void issue(const char* base, uint32_t lds, int q) const { dma_lds_x4(base, off[q], lds); }
-  // (along rows) last slice, `left` k in it
-  __device__ __forceinline__ void issue_tail(const char* base, uint32_t lds, int q, int first, int lane, int left) const {
-    const char* p = chunk_k(first + q, lane) < left ? base + off[q] : reinterpret_cast<const char*>(zero_chunk);
-    dma_lds_x4_at(p, lds);
   }
 };
 
@@ -142,10 +137,10 @@ struct Ring {
 };
 
 // One tile: rows m0 .. of which `rows` exist (tile rows past them repeat the last), columns from tile column nt,
-// slices [0, KT) from contraction index k0 with `left` k in the last; c and its scales from expert e.
+// KT slices from slice kt0 on; c and its scales from expert e.
 template <bool RK, bool CK, int EPI, int NH, bool FOLD>
-__device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_t m0, int64_t rows, int nt, int e, int64_t k0,
-                                         int64_t kt0, int KT, int left, int split, char* lds) {
+__device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_t m0, int64_t rows, int nt, int e, int64_t kt0,
+                                         int KT, int split, char* lds) {
   using Rg = Ring<NH>;
   const DenseGemm& g = job.g;
   const int lane = threadIdx.x & 63;
@@ -153,6 +148,7 @@ __device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_
   const int wm = wave >> 2, wn = wave & 3;
   const int l16 = lane & 15, g4 = lane >> 4;
   const int n0 = nt * (EPI == kGated ? 128 : 256);
+  const int64_t k0 = kt0 * 128;
   // tile column -> row of c
   auto c_row = [&](int col) __attribute__((always_inline)) -> int64_t {
     if constexpr (EPI == kGated) return min(n0 + (col & 127), g.e.N - 1) + (int64_t)(col >> 7) * g.e.N;
@@ -201,40 +197,30 @@ __device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_
   }
 
   const uint32_t lds0 = lds_addr(lds);
-  // Where slice kt is in the ring, and its scales; `tail`: kt is the last slice and has fewer than 128 k (along rows)
+  // Where slice kt is in the ring
   auto stage = [&](int kt) __attribute__((always_inline)) -> int { return (NH == 2 ? (kt & 1) : kt % 3) * Rg::STAGE; };
-  auto issue = [&](auto tail, const auto& from, const char* base, int dst) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if constexpr (decltype(tail)::value) from.issue_tail(base, lds0 + (uint32_t)dst + q * 1024, q, wave * 2, lane, left);
-      else from.issue(base, lds0 + (uint32_t)dst + q * 1024, q);
-    }
+  auto issue_r = [&](int h, int kt, int q) __attribute__((always_inline)) {
+    dma_lds_x4(rbase + kt * rstep, sr[h].off[q], lds0 + (uint32_t)(stage(kt) + h * REGION + wave * 2048 + q * 1024));
   };
-  auto issue_r = [&](auto tail, int h, int kt) __attribute__((always_inline)) {
-    issue(tail, sr[h], rbase + kt * rstep, stage(kt) + h * REGION + wave * 2048);
-  };
-  auto issue_c = [&](auto tail, int h, int kt) __attribute__((always_inline)) {
-    issue(tail, sc[h], chalf[h] + kt * cstep, stage(kt) + (NH + h) * REGION + wave * 2048);
+  auto issue_c = [&](int h, int kt, int q) __attribute__((always_inline)) {
+    dma_lds_x4(chalf[h] + kt * cstep, sc[h].off[q], lds0 + (uint32_t)(stage(kt) + (NH + h) * REGION + wave * 2048 + q * 1024));
   };
   auto issue_s = [&](int kt) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + s_lds + (uint32_t)(kt % 3 * Rg::SCALES);
     if constexpr (FOLD) dma_lds_x1(sbase + kt * s_step, s_off, dst);
     else dma_lds_u8(sbase + kt * s_step, s_off, dst);
   };
-  // a slice's DMAs in two parts: R0, scales, C0 (5 instructions) and C1, R1 (4; one row half: 2)
-  auto issue_a = [&](auto tail, int kt) __attribute__((always_inline)) {
-    issue_r(tail, 0, kt), issue_s(kt), issue_c(tail, 0, kt);
+  // a slice's DMA number n: R0, scales, C0 (0 .. 4), C1 (5, 6), R1 (7, 8; of 256 rows)
+  auto issue_n = [&](int kt, int n) __attribute__((always_inline)) {
+    if (n < 2) issue_r(0, kt, n);
+    else if (n == 2) issue_s(kt);
+    else if (n < 5) issue_c(0, kt, n - 3);
+    else if (n < 7) issue_c(1, kt, n - 5);
+    else if constexpr (NH == 2) issue_r(1, kt, n - 7);
   };
-  auto issue_b = [&](auto tail, int kt) __attribute__((always_inline)) {
-    issue_c(tail, 1, kt);
-    if constexpr (NH == 2) issue_r(tail, 1, kt);
-  };
-  constexpr bool TAIL = RK && CK;
-  typedef std::integral_constant<bool, false> Whole;
-  typedef std::integral_constant<bool, TAIL> Last;
-  auto issue_first = [&](int kt) __attribute__((always_inline)) {      // (in front of the loop)
-    if (kt == KT - 1) issue_a(Last{}, kt), issue_b(Last{}, kt);
-    else issue_a(Whole{}, kt), issue_b(Whole{}, kt);
+  auto issue_slice = [&](int kt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < 5 + 2 * NH; ++n) issue_n(kt, n);
   };
 
   const Frag8<RK> fr(lane);
@@ -299,59 +285,79 @@ __device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_
   };
   auto nothing = [](int) __attribute__((always_inline)) {};
 
-  // The loop's body without branches, for slices behind which one is issued (whole, or the last one) or none: across a branch
-  // the compiler moves products behind the DMAs and keeps all their operands in registers
-  enum { kNone, kWhole, kLast };
-  auto body = [&](auto MORE_, int kt) __attribute__((always_inline)) {
-    constexpr int MORE = decltype(MORE_)::value;
-    typedef std::conditional_t<MORE == kLast, Last, Whole> Tail;
+  // The loop's body without branches, for slices behind which one is issued or none: across a branch the compiler
+  // moves products behind the DMAs and keeps all their operands in registers
+  auto body = [&](auto more, int kt) __attribute__((always_inline)) {
+    constexpr bool MORE = decltype(more)::value;
+    // published: `younger` DMAs of this wave may be in flight, every read so far is done; then for the workgroup
+    auto meet = [&](auto younger) __attribute__((always_inline)) {
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (MORE) wait_vmcnt<decltype(younger)::value>();
+      else wait_vmcnt<0>();
+      wait_lds();
+      barrier();
+    };
+    // DMA n of the slice ahead.  They go out one at a time between products: eight waves' bursts behind a barrier would hold
+    // up every wave's next product until the addresses of all are taken
+    auto ahead = [&](int n) __attribute__((always_inline)) {
+      if constexpr (MORE) issue_n(kt + (NH == 2 ? 2 : 3), n);
+    };
     if constexpr (NH == 2) {
-      if constexpr (MORE != kNone) issue_a(Tail{}, kt + 2);
-      read_c(1, kt);
-      multiply(acc[0][0], acc[1][1], 0, nothing);
-      multiply(acc[0][1], acc[0][0], 1, [&](int i) __attribute__((always_inline)) { read_r(i, 1, kt); });
-      if constexpr (MORE != kNone) wait_vmcnt<9>();   // R0, C0 of kt + 1; younger: C1, R1 of kt + 1 and R0, scales, C0 of kt + 2
-      else wait_vmcnt<0>();
-      wait_lds();
-      barrier();
-      if constexpr (MORE != kNone) issue_b(Tail{}, kt + 2);
-      multiply(acc[1][0], acc[0][1], 0, nothing);
+      multiply(acc[0][0], acc[1][1], 0, [&](int i) __attribute__((always_inline)) {
+        if (i == 0) return;
+        if (i == 1) {
+          meet(std::integral_constant<int, 9>{});     // C1, R1(kt) are here; younger: kt + 1
+          read_c(1, kt);
+        }
+        ahead(i - 1);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      multiply(acc[0][1], acc[0][0], 1, [&](int i) __attribute__((always_inline)) {
+        read_r(i, 1, kt);
+        if (i & 1) ahead(3 + i / 2);
+      });
+      multiply(acc[1][0], acc[0][1], 0, [&](int i) __attribute__((always_inline)) {
+        if (i == 1) meet(std::integral_constant<int, 9>{});   // R0, C0(kt + 1); younger: C1, R1(kt + 1) and R0, scales, C0(kt + 2)
+        if (i & 1) ahead(5 + i / 2);
+        __builtin_amdgcn_sched_barrier(0);
+      });
       read_c(0, kt + 1);                              // (behind the last slice: what the ring holds, not used)
-      multiply(acc[1][1], acc[1][0], 1, [&](int i) __attribute__((always_inline)) { read_r(i, 0, kt + 1); });
-      if constexpr (MORE != kNone) wait_vmcnt<9>();   // C1, R1 of kt + 1; younger: kt + 2
-      else wait_vmcnt<0>();
-      wait_lds();
-      barrier();
+      multiply(acc[1][1], acc[1][0], 1, [&](int i) __attribute__((always_inline)) {
+        read_r(i, 0, kt + 1);
+        if (i & 1) ahead(7 + i / 2);
+      });
     } else {
       read_c(1, kt);
       multiply(acc[0][0], acc[0][1], 0, nothing);
-      if constexpr (MORE != kNone) wait_vmcnt<7>();   // slice kt + 1; younger: kt + 2
-      else wait_vmcnt<0>();
-      wait_lds();                                     // (and every read of slice kt is done)
-      barrier();
-      if constexpr (MORE != kNone) issue_a(Tail{}, kt + 3), issue_b(Tail{}, kt + 3);
-      read_c(0, kt + 1);
-      multiply(acc[0][1], acc[0][0], 1, [&](int i) __attribute__((always_inline)) { read_r(i, 0, kt + 1); });
+      multiply(acc[0][1], acc[0][0], 1, [&](int i) __attribute__((always_inline)) {
+        if (i == 0) return;
+        if (i == 1) {
+          meet(std::integral_constant<int, 7>{});     // slice kt + 1; younger: kt + 2
+          read_c(0, kt + 1);
+          read_r(0, 0, kt + 1);
+        }
+        read_r(i, 0, kt + 1);
+#pragma unroll
+        for (int n = 0; n < 7; ++n)
+          if (n / 3 == i - 1 || (n == 6 && i == 3)) ahead(n);
+      });
     }
   };
   constexpr int AHEAD = NH == 2 ? 2 : 3;
   if (KT > 0) {
-    issue_first(0);
-    if (KT > 1) issue_first(1);
-    if (NH == 1 && KT > 2) issue_first(2);
-    if (KT >= AHEAD) wait_vmcnt<NH == 2 ? 9 : 14>();
+    issue_slice(0);
+    if (KT > 1) issue_slice(1);
+    if (NH == 1 && KT > 2) issue_slice(2);
+    if (KT >= AHEAD) wait_vmcnt<NH == 2 ? 13 : 14>();
     else wait_vmcnt<0>();
     wait_lds();                            // (the table's stores)
-    barrier();                             // slice 0 has landed
+    barrier();                             // slice 0 has landed (of 256 rows, R0 and C0)
 #pragma unroll
     for (int i = 0; i < 4; ++i) read_r(i, 0, 0);
     read_c(0, 0);
-    wait_lds();
-    barrier();                             // (the first slice's DMAs refill what was just read)
     int kt = 0;
-    for (; kt + AHEAD + (TAIL ? 1 : 0) < KT; ++kt) body(std::integral_constant<int, kWhole>{}, kt);
-    if (TAIL && kt + AHEAD < KT) body(std::integral_constant<int, kLast>{}, kt++);
-    for (; kt < KT; ++kt) body(std::integral_constant<int, kNone>{}, kt);
+    for (; kt + AHEAD < KT; ++kt) body(std::true_type{}, kt);
+    for (; kt < KT; ++kt) body(std::false_type{}, kt);
     if constexpr (FOLD) fold(acc[NH - 1][1][3], 1);
   }
 
@@ -391,10 +397,11 @@ __global__ __launch_bounds__(512, 1) void fp8_rows_tile_kernel(Fp8Job p) {
   }
   const int64_t kt0 = (int64_t)blockIdx.y * job.slices;
   const int KT = (int)min((int64_t)job.slices, job.g.K / 128 - kt0);
-  tile_fp8<false, CK, EPI, NH, FOLD>(p, job, m0, rows, nt, e, kt0 * 128, kt0, KT, 128, blockIdx.y, lds);
+  tile_fp8<false, CK, EPI, NH, FOLD>(p, job, m0, rows, nt, e, kt0, KT, blockIdx.y, lds);
 }
 
-// dw: contractions over the rows, all of them (splits along blockIdx.y) or each run's (run blockIdx.y)
+// dw: contractions over the rows in tiles of 128 (a run's last filled up with zeros): all of them (splits along
+// blockIdx.y) or each run's (run blockIdx.y)
 template <int NH>
 __global__ __launch_bounds__(512, 1) void fp8_dw_kernel(Fp8Job p) {
   __shared__ __attribute__((aligned(1024))) char lds[Ring<NH>::BYTES];
@@ -402,23 +409,19 @@ __global__ __launch_bounds__(512, 1) void fp8_dw_kernel(Fp8Job p) {
   int mt, nt;
   if (!tile_of(job, blockIdx.x, mt, nt)) return;
   const int64_t m0 = (int64_t)mt * 128 * NH;
-  int64_t k0, kt0, k;
-  int split = 0;
+  int64_t kt0;
+  int KT, split = 0;
   if (p.E) {
     const int e = blockIdx.y;
-    k0 = p.runs.start[e];
-    k = p.runs.start[e + 1] - k0;
     kt0 = p.runs.group[e];
+    KT = (int)(p.runs.group[e + 1] - kt0);
     job.g.e.out = static_cast<uint16_t*>(job.g.e.out) + (int64_t)e * job.g.M * job.g.e.N;
   } else {
     split = blockIdx.y;
     kt0 = (int64_t)split * job.slices;
-    k0 = kt0 * 128;
-    k = min((int64_t)job.slices * 128, job.g.K - k0);
+    KT = (int)min((int64_t)job.slices, job.g.K / 128 - kt0);
   }
-  const int KT = (int)((k + 127) / 128);
-  tile_fp8<true, true, kGrad, NH, false>(p, job, m0, job.g.M - m0, nt, 0, k0, kt0, KT, (int)(k - (int64_t)(KT - 1) * 128), split,
-                                         lds);
+  tile_fp8<true, true, kGrad, NH, false>(p, job, m0, job.g.M - m0, nt, 0, kt0, KT, split, lds);
 }
 
 inline Fp8Job fp8_job(const Fp8Gemm& g, const Job& job) {
