@@ -12,6 +12,9 @@ hipError_t launch_tiles(const Fp8Job& p, int tile, int y, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Sums that are stored as they are take the gradients' plain store
+bool plain(const DenseEpi& e) { return !e.bias && !e.res && !e.pre && e.act == kActNone; }
+
 }  // namespace
 
 int fp8_grouped_height(int64_t T, int E) { return T >= (int64_t)192 * E ? 256 : 128; }
@@ -32,7 +35,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t s) {
     job.mt = (int)max_row_tiles(g.g.M, g.E, height);
     job.nt = (job.crows + 255) / 256;
     const Fp8Job p = fp8_job(g, job);
-    return g.g.gated ? launch_tiles<kGated>(p, height, 1, s) : launch_tiles<kLinear>(p, height, 1, s);
+    return g.g.gated ? launch_tiles<kGated>(p, height, 1, s) : launch_tiles<kGrad>(p, height, 1, s);
   }
   if (fp8_rows_take(g.g.M, g.g.K)) return launch_fp8_rows(g, s);
   const Plan plan = plan_fp8(g.g.M, g.g.e.N, g.g.K, g.g.gated);
@@ -40,7 +43,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t s) {
     const Fp8Job p = fp8_job(g, job);
     if (epi == kPartial) return launch_tiles<kPartial>(p, plan.tile, job.splits, s);
     if (epi == kGated) return launch_tiles<kGated>(p, plan.tile, 1, s);
-    return launch_tiles<kLinear>(p, plan.tile, 1, s);
+    return plain(g.g.e) ? launch_tiles<kGrad>(p, plan.tile, 1, s) : launch_tiles<kLinear>(p, plan.tile, 1, s);
   });
 }
 

@@ -186,17 +186,19 @@ __device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_
   const uint32_t s_off = (uint32_t)((s_at - s_first) * S_SIZE);
   const uint32_t s_lds = (uint32_t)(Rg::SLICES * Rg::STAGE + (r_wave ? (wave % (2 * NH)) * 256 : NH * 512 + (wave - 4) * 256));
   const int64_t s_step = sp.slice * S_SIZE;
-  float* const table = reinterpret_cast<float*>(lds + Rg::TABLE);
-  if constexpr (FOLD) {
-    for (int i = threadIdx.x; i < 2 * KT; i += 512) {
-      const int h = i < KT ? 0 : 1, kt = i - h * KT;
-      const int64_t at = e * p.cs_expert + (c_row(h * 128) >> 7) * p.cs.row + (kt0 + kt) * p.cs.slice;
-      table[h * kMaxSlices + kt] = p.cs.bytes ? ue8m0_value(static_cast<const uint8_t*>(p.cs.p)[at])
-                                              : static_cast<const float*>(p.cs.p)[at];
-    }
-  }
-
   const uint32_t lds0 = lds_addr(lds);
+  const char* const table = lds + Rg::TABLE;      // FOLD: c's block scales of this tile, [2 halves][kMaxSlices] dwords
+  auto issue_table = [&]() __attribute__((always_inline)) {
+    for (int i0 = wave * 64; i0 < 2 * kMaxSlices; i0 += 512) {
+      const int h = i0 / kMaxSlices;
+      if (i0 - h * kMaxSlices >= KT) continue;
+      const int kt = min(i0 - h * kMaxSlices + lane, KT - 1);
+      const int64_t first = e * p.cs_expert + (c_row(h * 128) >> 7) * p.cs.row + kt0 * p.cs.slice;
+      const uint32_t dst = lds0 + (uint32_t)(Rg::TABLE + i0 * 4);
+      if (p.cs.bytes) dma_lds_u8(static_cast<const uint8_t*>(p.cs.p) + first, (uint32_t)(kt * p.cs.slice), dst);
+      else dma_lds_x1(static_cast<const float*>(p.cs.p) + first, (uint32_t)(kt * p.cs.slice * 4), dst);
+    }
+  };
   // Where slice kt is in the ring
   auto stage = [&](int kt) __attribute__((always_inline)) -> int { return (NH == 2 ? (kt & 1) : kt % 3) * Rg::STAGE; };
   auto issue_r = [&](int h, int kt, int q) __attribute__((always_inline)) {
@@ -248,36 +250,33 @@ __device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_
       c[h][j] = fc.load(lds + stage(kt) + (NH + h) * REGION, wn * 32 + j * 16);
       if (!FOLD) csc[h][j] = *reinterpret_cast<const uint32_t*>(s + (j * 16 + l16) * 4);
     }
-    if (FOLD) csc[h][0] = __float_as_uint(table[h * kMaxSlices + min(kt, kMaxSlices - 1)]);
+    if (FOLD) csc[h][0] = *reinterpret_cast<const uint32_t*>(table + (h * kMaxSlices + min(kt, kMaxSlices - 1)) * 4);
   };
-  // a phase's products; after(i) reads into fragment i's place
-  f32x4 pr[2][2];
-  float prs[2] = {0.f, 0.f};
+  // A phase's products; after(i) reads into fragment i's place.  FOLD: a result is folded in three products after its own, when the
+  // MFMA has long written it (so a phase's last three in the next one: `before` is the accumulator of the phase before)
+  f32x4 pr[4];
+  float prs[4];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) pr[q][0] = pr[q][1] = f32x4{};
-  auto fold = [&](f32x4 (&a)[2], int at) __attribute__((always_inline)) {
+  for (int q = 0; q < 4; ++q) pr[q] = f32x4{}, prs[q] = 0.f;
+  auto fold = [&](f32x4& a, int at, int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) a[j][q] = fmaf(pr[at][j][q], prs[at], a[j][q]);
+    for (int q = 0; q < 4; ++q) a[q] = fmaf(pr[at][q], prs[i], a[q]);
   };
-  // (FOLD: a fragment's results are folded in after the next one's products are issued; those of a phase's last fragment in
-  // the next phase, so `before` is the accumulator of the phase before)
   auto multiply = [&](f32x4 (&a)[4][2], f32x4 (&before)[4][2], int h, auto&& after) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
-    const float sb = __uint_as_float(csc[h][0]);
+    const float sb = FOLD && p.cs.bytes ? ue8m0_value(csc[h][0]) : __uint_as_float(csc[h][0]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (FOLD) {
-        const float s = __uint_as_float(rsc[i]) * sb;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) pr[i & 1][j] = mfma_16x16x128_e4m3(c[h][j], r[i], f32x4{});
-        prs[i & 1] = s;
-        fold(i == 0 ? before[3] : a[(i + 3) & 3], (i + 1) & 1);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (FOLD) {
+          const int n = 2 * i + j, old = (n + 5) & 7;
+          pr[n & 3] = mfma_16x16x128_e4m3(c[h][j], r[i], f32x4{});
+          fold(n < 3 ? before[old >> 1][old & 1] : a[old >> 1][old & 1], old & 3, old >> 1);
+          if (j == 1) prs[i] = __uint_as_float(rsc[i]) * sb;
+        } else {
           a[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(c[h][j], r[i], a[i][j], 0, 0, 0, (int)csc[h][j], 0, (int)rsc[i]);
+        }
       }
       after(i);
     }
@@ -345,12 +344,12 @@ __device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_
   };
   constexpr int AHEAD = NH == 2 ? 2 : 3;
   if (KT > 0) {
+    if constexpr (FOLD) issue_table();
     issue_slice(0);
     if (KT > 1) issue_slice(1);
     if (NH == 1 && KT > 2) issue_slice(2);
     if (KT >= AHEAD) wait_vmcnt<NH == 2 ? 13 : 14>();
     else wait_vmcnt<0>();
-    wait_lds();                            // (the table's stores)
     barrier();                             // slice 0 has landed (of 256 rows, R0 and C0)
 #pragma unroll
     for (int i = 0; i < 4; ++i) read_r(i, 0, 0);
@@ -358,7 +357,10 @@ __device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_
     int kt = 0;
     for (; kt + AHEAD < KT; ++kt) body(std::true_type{}, kt);
     for (; kt < KT; ++kt) body(std::false_type{}, kt);
-    if constexpr (FOLD) fold(acc[NH - 1][1][3], 1);
+    if constexpr (FOLD) {
+#pragma unroll
+      for (int n = 5; n < 8; ++n) fold(acc[NH - 1][1][n >> 1][n & 1], n & 3, n >> 1);
+    }
   }
 
 #pragma unroll
