@@ -17,7 +17,8 @@ struct RowTile {
 struct Runs {
   int32_t* start;       // [E + 1]
   int32_t* group;       // [E + 1]: 128-row tiles before the expert's
-  int32_t* count;       // [2]: tiles, 128-row tiles
+  int32_t* order;       // [E]: the experts with rows, then those without
+  int32_t* count;       // [3]: tiles, 128-row tiles, experts with rows
   RowTile* tiles;       // of `height` rows
   RowTile* groups;      // of 128 rows; the same as tiles with height == 128
   int height;

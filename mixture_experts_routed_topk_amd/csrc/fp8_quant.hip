@@ -297,7 +297,7 @@ __device__ void list_tiles(RowTile* out, const int32_t* start, const int32_t* fi
 }
 
 __global__ __launch_bounds__(kMaxE) void runs_kernel(Runs r, const int32_t* __restrict__ offsets, int T, int E) {
-  __shared__ int32_t sums[16], start[kMaxE + 1], first[kMaxE + 1], group[kMaxE + 1];
+  __shared__ int32_t alive, sums[16], start[kMaxE + 1], first[kMaxE + 1], group[kMaxE + 1];
   const int e = threadIdx.x;
   auto larger = [](int32_t a, int32_t b) { return a > b ? a : b; };
   auto plus = [](int32_t a, int32_t b) { return a + b; };
@@ -312,6 +312,10 @@ __global__ __launch_bounds__(kMaxE) void runs_kernel(Runs r, const int32_t* __re
   if (e < E) first[e + 1] = n, group[e + 1] = n128;
   if (e == 0) first[0] = 0, group[0] = 0;
   __syncthreads();
+  const int32_t live = scan(cnt > 0 ? 1 : 0, sums, plus);       // (threads past E have none)
+  if (e == kMaxE - 1) r.count[2] = alive = live;
+  __syncthreads();
+  if (e < E) r.order[cnt > 0 ? live - 1 : alive + e - live] = e;
   for (int i = e; i <= E; i += kMaxE) r.start[i] = start[i], r.group[i] = group[i];
   if (e == 0) r.count[0] = first[E], r.count[1] = group[E];
   list_tiles(r.tiles, start, first, E, first[E], r.height);
@@ -324,7 +328,7 @@ size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 size_t runs_bytes(int64_t T, int E, int height) {
   if (E == 0) return 0;
-  return up256(4 * (2 * (size_t)(E + 1) + 2)) + up256(sizeof(RowTile) * (size_t)max_row_tiles(T, E, height)) +
+  return up256(4 * (3 * (size_t)(E + 1) + 2)) + up256(sizeof(RowTile) * (size_t)max_row_tiles(T, E, height)) +
          (height == 128 ? 0 : up256(sizeof(RowTile) * (size_t)max_row_tiles(T, E, 128)));
 }
 
@@ -333,8 +337,9 @@ Runs runs_at(void* ws, int64_t T, int E, int height) {
   r.height = height;
   r.start = static_cast<int32_t*>(ws);
   r.group = r.start + E + 1;
-  r.count = r.group + E + 1;
-  char* p = static_cast<char*>(ws) + up256(4 * (2 * (size_t)(E + 1) + 2));
+  r.order = r.group + E + 1;
+  r.count = r.order + E;
+  char* p = static_cast<char*>(ws) + up256(4 * (3 * (size_t)(E + 1) + 2));
   r.tiles = reinterpret_cast<RowTile*>(p);
   r.groups = height == 128 ? r.tiles : reinterpret_cast<RowTile*>(p + up256(sizeof(RowTile) * (size_t)max_row_tiles(T, E, height)));
   return r;

@@ -28,6 +28,8 @@
 //     3       R1 x C1                                                             R0, C0(kt+1)
 //   Each DMA has a slice and a half to land, and a barrier comes when the reads before it have long ended.
 //   NH = 1, 128 rows, three slices in LDS: phases 0 and 1 alone, one barrier and one wait per slice.
+// One workgroup a CU takes one tile after another, and the DMAs run on: the next tile's first slices arrive during a
+// tile's last ones and its stores.  (A workgroup per tile: 2.6 us of first DMAs and 1.8 us between workgroups beside 1.8 us a slice.)
 #pragma once
 
 #include <type_traits>
@@ -76,26 +78,18 @@ struct Frag8 {
   }
 };
 
-// This lane's DMA sources for the two instructions of a wave in a region (rows: tile rows of the region, clamped)
+// Where instruction `ins` (1 KB) of a 128-row region takes lane `lane`'s 16 bytes from: tile row and k (along rows: first row of the
+// chunk and its k)
 template <bool KM>
-struct Stream8 {
-  uint32_t off[2];
-  static __device__ __forceinline__ int chunk_k(int ins, int lane) {
+struct Chunk8 {
+  static __device__ __forceinline__ int k(int ins, int lane) {
     if constexpr (KM) return ins * 8 + (lane >> 3);
     return ((lane & 7) ^ (((ins * 8 + (lane >> 3)) >> 1) & 7)) * 16;
   }
-  static __device__ __forceinline__ int chunk_row(int ins, int lane) {
+  static __device__ __forceinline__ int row(int ins, int lane) {
     if constexpr (!KM) return ins * 8 + (lane >> 3);
-    const int k = chunk_k(ins, lane);
-    return ((lane & 7) ^ ((k & 7) ^ ((k >> 4) & 1))) * 16;
-  }
-  template <typename F>
-  __device__ __forceinline__ void init(int first, int lane, int64_t ld, F&& row_of) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int64_t row = row_of(chunk_row(first + q, lane));
-      off[q] = (uint32_t)(KM ? chunk_k(first + q, lane) * ld + row : row * ld + chunk_k(first + q, lane));
-    }
+    const int kk = k(ins, lane);
+    return ((lane & 7) ^ ((kk & 7) ^ ((kk >> 4) & 1))) * 16;
   }
 };
 
@@ -127,142 +121,249 @@ __device__ __forceinline__ void eight_columns(f32x4& a, f32x4& b) {
 
 constexpr int kMaxSlices = 512;         // K <= 65536
 
+// This lane's number, formed anew (from a zero that the compiler does not know to be one): what follows from it is computed
+// where it is used, once a tile, and not kept in registers through the loop
+__device__ __forceinline__ int lane_again() {
+  int zero = 0;
+  asm volatile("" : "+v"(zero));
+  return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, (uint32_t)zero));
+}
+
+// The kernel's argument (its only one), read from memory again: what a tile needs once does not occupy scalar registers in the loop
+__device__ __forceinline__ const Fp8Job& argument() {
+  auto p = __builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const Fp8Job*)p;
+}
+
+// The values are formed here: products that only later code reads would be moved there, behind branches, and their
+// operands kept in registers until then.  (No instruction: nothing is read.)
+__device__ __forceinline__ void formed(f32x4 (&a)[4][2]) {
+  asm volatile("" : "+v"(a[0][0]), "+v"(a[0][1]), "+v"(a[1][0]), "+v"(a[1][1]), "+v"(a[2][0]), "+v"(a[2][1]), "+v"(a[3][0]), "+v"(a[3][1]));
+}
+
 template <int NH>
 struct Ring {
-  static constexpr int SLICES = NH == 2 ? 2 : 3;
+  static constexpr int SLICES = NH == 2 ? 2 : 3;                  // in LDS, and how far the DMAs are ahead
   static constexpr int STAGE = (NH + 2) * REGION;                 // R0 [R1] C0 C1
   static constexpr int SCALES = (128 * NH + 256) * 4;             // a dword per row of r and, for the MFMA, of c
-  static constexpr int TABLE = SLICES * STAGE + 3 * SCALES;       // FOLD: c's block scales, [2 halves][kMaxSlices]
-  static constexpr int BYTES = TABLE + 2 * kMaxSlices * 4;
+  static constexpr int TABLE = SLICES * STAGE + 3 * SCALES;       // FOLD: c's block scales of NT tiles, [2 halves][slices]
+  static constexpr int BYTES = 160 * 1024;
+  static constexpr int TABLES = BYTES - TABLE;
 };
 
-// One tile: rows m0 .. of which `rows` exist (tile rows past them repeat the last), columns from tile column nt,
-// KT slices from slice kt0 on; c and its scales from expert e.
-template <bool RK, bool CK, int EPI, int NH, bool FOLD>
-__device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_t m0, int64_t rows, int nt, int e, int64_t kt0,
-                                         int KT, int split, char* lds) {
+// What the table kernel wrote: read through the scalar cache (a vector load would have the compiler wait for every DMA in flight)
+__device__ __forceinline__ int table_entry(const void* table, int64_t i) {
+  typedef const __attribute__((address_space(4))) int32_t* Table;
+  return ((Table)(uintptr_t)table)[i];
+}
+
+// A tile of the product: rows m0 .. of which `rows` exist (tile rows past them repeat the last), columns from tile column
+// nt, KT slices from kt0 on; c, its scales and dw's output from expert e
+struct Tile {
+  int64_t m0;
+  int rows, nt, e, split;
+  int kt0, KT;
+};
+// Forward and dx: row tiles of one matrix (with splits of the contraction) or of runs of rows
+struct RowTiles {
+  static __device__ __forceinline__ int count(const Fp8Job& p) {
+    return (p.E ? table_entry(p.runs.count, 0) : p.j.mt * p.j.splits) * p.j.nt;
+  }
+  template <int NH>
+  static __device__ __forceinline__ Tile at(const Fp8Job& p, int t) {
+    Tile x{};
+    Job j = p.j;
+    if (p.E) {
+      j.mt = table_entry(p.runs.count, 0);
+      int mt;
+      tile_at(j, t, mt, x.nt);
+      x.e = table_entry(p.runs.tiles, (int64_t)mt * 4);
+      x.m0 = table_entry(p.runs.tiles, (int64_t)mt * 4 + 1);
+      x.rows = table_entry(p.runs.tiles, (int64_t)mt * 4 + 2);
+      x.KT = j.slices;
+    } else {
+      const int per = j.mt * j.nt;
+      x.split = t / per;
+      int mt;
+      tile_at(j, t - x.split * per, mt, x.nt);
+      x.m0 = (int64_t)mt * 128 * NH;
+      x.rows = (int)min((int64_t)128 * NH, j.g.M - x.m0);
+      x.kt0 = x.split * j.slices;
+      x.KT = min(j.slices, (int)(j.g.K / 128) - x.kt0);
+    }
+    return x;
+  }
+};
+// dw: contractions over 128-row tiles, all of them (with splits) or each run's
+struct DwTiles {
+  static __device__ __forceinline__ int count(const Fp8Job& p) { return (p.E ? table_entry(p.runs.count, 2) : p.j.splits) * p.j.mt * p.j.nt; }
+  template <int NH>
+  static __device__ __forceinline__ Tile at(const Fp8Job& p, int t) {
+    Tile x{};
+    const int per = p.j.mt * p.j.nt, part = t / per;
+    int mt;
+    tile_at(p.j, t - part * per, mt, x.nt);
+    x.m0 = (int64_t)mt * 128 * NH;
+    x.rows = (int)min((int64_t)128 * NH, p.j.g.M - x.m0);
+    if (p.E) {
+      x.e = table_entry(p.runs.order, part);
+      x.kt0 = table_entry(p.runs.group, x.e);
+      x.KT = table_entry(p.runs.group, x.e + 1) - x.kt0;
+    } else {
+      x.split = part;
+      x.kt0 = part * p.j.slices;
+      x.KT = min(p.j.slices, (int)(p.j.g.K / 128) - x.kt0);
+    }
+    return x;
+  }
+};
+
+template <typename TILES, bool RK, bool CK, int EPI, int NH, bool FOLD>
+__device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds) {
   using Rg = Ring<NH>;
-  const DenseGemm& g = job.g;
+  constexpr int AHEAD = Rg::SLICES;
+  constexpr int DMAS = 5 + 2 * NH;             // of a wave and slice
+  const DenseGemm& g = p.j.g;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const int l16 = lane & 15, g4 = lane >> 4;
-  const int n0 = nt * (EPI == kGated ? 128 : 256);
-  const int64_t k0 = kt0 * 128;
-  // tile column -> row of c
-  auto c_row = [&](int col) __attribute__((always_inline)) -> int64_t {
-    if constexpr (EPI == kGated) return min(n0 + (col & 127), g.e.N - 1) + (int64_t)(col >> 7) * g.e.N;
-    return min((int64_t)(n0 + col), (int64_t)job.crows - 1);
-  };
+  const int l16 = lane & 15;
+  // Workgroups go to the eight XCDs in turn: each XCD takes a run of neighbouring tiles of every round, so that the 32 that run
+  // on it together are 8 x 4 and share their operands in its L2
+  const int total = TILES::count(p);
+  const int first = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  if (first >= total) return;
+  const uint32_t lds0 = lds_addr(lds);
 
-  const char* rbase = static_cast<const char*>(g.r) + (RK ? k0 * g.ldr + m0 : m0 * g.ldr + k0);
-  const char* cbase = static_cast<const char*>(g.c) + e * p.c_expert + (CK ? k0 * g.ldc + n0 : n0 * g.ldc + k0);
-  const int64_t rstep = RK ? 128 * g.ldr : 128, cstep = CK ? 128 * g.ldc : 128;
-  // gated: the second column half is the up projection's rows, N rows on (more than 32-bit offsets reach)
-  const char* const chalf[2] = {cbase, cbase + (EPI == kGated ? (int64_t)g.e.N * g.ldc : 0)};
-  Stream8<RK> sr[NH];
-  Stream8<CK> sc[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (h < NH)
-      sr[h].init(wave * 2, lane, g.ldr, [&](int row) -> int64_t { return min((int64_t)(h * 128 + row), rows - (RK ? 16 : 1)); });
-    sc[h].init(wave * 2, lane, g.ldc, [&](int row) -> int64_t {
-      if constexpr (EPI == kGated) return min(row, g.e.N - 1 - n0);
-      return min((int64_t)(h * 128 + row), (int64_t)job.crows - n0 - (CK ? 16 : 1));
-    });
-  }
+  // ------------------------------------------------------------------ DMAs: a cursor over tiles and their slices, on the one issued last
+  int at_tile = first, left;                   // the tile, and how many of its slices are still to be issued
+  const char *rbase, *cbase[2], *sbase;
+  uint32_t roff[NH][2], coff[2][2], soff;
+  int64_t rstep = RK ? 128 * g.ldr : 128, cstep = CK ? 128 * g.ldc : 128;      // bytes from a slice to the next
+  constexpr int S_SIZE = FOLD ? 4 : 1;
   // Scales by row, a dword each (64 a wave): FOLD: r's, by waves 0 .. 2 NH - 1 (the others bring the same again); else waves
   // 0 .. 3 bring r's and 4 .. 7 c's
   const bool r_wave = FOLD || wave < 4;
-  const int s_row = r_wave ? (wave % (2 * NH)) * 64 + lane : (wave - 4) * 64 + lane;
-  const Fp8Scales& sp = r_wave ? p.rs : p.cs;
-  constexpr int S_SIZE = FOLD ? 4 : 1;
-  const int64_t s_at = r_wave ? (m0 + min((int64_t)s_row, rows - 1)) * sp.row
-                              : e * p.cs_expert + (p.c_blocks ? c_row(s_row) >> 7 : c_row(s_row)) * sp.row;
-  // (a wave's first lane gives the base, so that a lane's offset fits in 32 bits)
-  const int64_t s_first = ((int64_t)__builtin_amdgcn_readfirstlane((int)(s_at >> 32)) << 32) |
-                          (uint32_t)__builtin_amdgcn_readfirstlane((int)s_at);
-  const char* sbase = static_cast<const char*>(sp.p) + (s_first + kt0 * sp.slice) * S_SIZE;
-  const uint32_t s_off = (uint32_t)((s_at - s_first) * S_SIZE);
+  int64_t s_step = (r_wave ? p.rs.slice : p.cs.slice) * S_SIZE;
   const uint32_t s_lds = (uint32_t)(Rg::SLICES * Rg::STAGE + (r_wave ? (wave % (2 * NH)) * 256 : NH * 512 + (wave - 4) * 256));
-  const int64_t s_step = sp.slice * S_SIZE;
-  const uint32_t lds0 = lds_addr(lds);
-  const char* const table = lds + Rg::TABLE;      // FOLD: c's block scales of this tile, [2 halves][kMaxSlices] dwords
-  auto issue_table = [&]() __attribute__((always_inline)) {
-    for (int i0 = wave * 64; i0 < 2 * kMaxSlices; i0 += 512) {
-      const int h = i0 / kMaxSlices;
-      if (i0 - h * kMaxSlices >= KT) continue;
-      const int kt = min(i0 - h * kMaxSlices + lane, KT - 1);
-      const int64_t first = e * p.cs_expert + (c_row(h * 128) >> 7) * p.cs.row + kt0 * p.cs.slice;
-      const uint32_t dst = lds0 + (uint32_t)(Rg::TABLE + i0 * 4);
-      if (p.cs.bytes) dma_lds_u8(static_cast<const uint8_t*>(p.cs.p) + first, (uint32_t)(kt * p.cs.slice), dst);
-      else dma_lds_x1(static_cast<const float*>(p.cs.p) + first, (uint32_t)(kt * p.cs.slice * 4), dst);
+  int table_at = 0;                            // FOLD: where the next tile's block scales go (dwords), as table_of below
+  auto table_next = [&](int at, int KT) __attribute__((always_inline)) -> int {
+    const int next = at + 2 * ((KT + 63) & ~63);           // (whole DMAs of 64)
+    return next + 2 * ((KT + 63) & ~63) > Rg::TABLES / 4 ? 0 : next;
+  };
+  auto open = [&]() __attribute__((always_inline)) {         // addresses of tile at_tile
+    const Fp8Job& p = argument();
+    const DenseGemm& g = p.j.g;
+    const Tile x = TILES::template at<NH>(p, at_tile);
+    const int lane = lane_again();
+    left = x.KT;
+    const int n0 = x.nt * (EPI == kGated ? 128 : 256);
+    const int64_t k0 = (int64_t)x.kt0 * 128;
+    // tile column -> row of c
+    auto c_row = [&](int col) __attribute__((always_inline)) -> int64_t {
+      if constexpr (EPI == kGated) return min(n0 + (col & 127), g.e.N - 1) + (int64_t)(col >> 7) * g.e.N;
+      return min((int64_t)(n0 + col), (int64_t)p.j.crows - 1);
+    };
+    rbase = static_cast<const char*>(g.r) + (RK ? k0 * g.ldr + x.m0 : x.m0 * g.ldr + k0) - rstep;
+    cbase[0] = static_cast<const char*>(g.c) + x.e * p.c_expert + (CK ? k0 * g.ldc + n0 : n0 * g.ldc + k0) - cstep;
+    // gated: the second column half is the up projection's rows, N rows on (more than 32-bit offsets reach)
+    cbase[1] = cbase[0] + (EPI == kGated ? (int64_t)g.e.N * g.ldc : 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int ins = wave * 2 + q;
+        if (h < NH) {
+          const int row = min(h * 128 + Chunk8<RK>::row(ins, lane), x.rows - (RK ? 16 : 1));
+          roff[h][q] = (uint32_t)(RK ? Chunk8<RK>::k(ins, lane) * g.ldr + row : row * g.ldr + Chunk8<RK>::k(ins, lane));
+        }
+        int col = Chunk8<CK>::row(ins, lane);
+        if constexpr (EPI == kGated) col = min(col, g.e.N - 1 - n0);
+        else col = min(h * 128 + col, p.j.crows - n0 - (CK ? 16 : 1));
+        coff[h][q] = (uint32_t)(CK ? Chunk8<CK>::k(ins, lane) * g.ldc + col : col * g.ldc + Chunk8<CK>::k(ins, lane));
+      }
+    const int s_row = (r_wave ? wave % (2 * NH) : wave - 4) * 64 + lane;
+    const int64_t s_at = r_wave ? (x.m0 + min(s_row, x.rows - 1)) * p.rs.row
+                                : x.e * p.cs_expert + (p.c_blocks ? c_row(s_row) >> 7 : c_row(s_row)) * p.cs.row;
+    // (a wave's first lane gives the base, so that a lane's offset fits in 32 bits)
+    const int64_t s_first = ((int64_t)__builtin_amdgcn_readfirstlane((int)(s_at >> 32)) << 32) |
+                            (uint32_t)__builtin_amdgcn_readfirstlane((int)s_at);
+    sbase = static_cast<const char*>(r_wave ? p.rs.p : p.cs.p) + (s_first + x.kt0 * (r_wave ? p.rs.slice : p.cs.slice)) * S_SIZE - s_step;
+    soff = (uint32_t)((s_at - s_first) * S_SIZE);
+    if constexpr (FOLD) {                      // c's block scales of the whole tile
+      const int half = (x.KT + 63) >> 6;
+      for (int i = wave; i < 2 * half; i += 8) {
+        const int h = i >= half;
+        const int kt = min((i - h * half) * 64 + lane, x.KT - 1);
+        const int64_t from = x.e * p.cs_expert + (c_row(h * 128) >> 7) * p.cs.row + x.kt0 * p.cs.slice;
+        const uint32_t dst = lds0 + (uint32_t)(Rg::TABLE + (table_at + i * 64) * 4);
+        if (p.cs.bytes) dma_lds_u8(static_cast<const uint8_t*>(p.cs.p) + from, (uint32_t)(kt * p.cs.slice), dst);
+        else dma_lds_x1(static_cast<const float*>(p.cs.p) + from, (uint32_t)(kt * p.cs.slice * 4), dst);
+      }
+      table_at = table_next(table_at, x.KT);
     }
   };
-  // Where slice kt is in the ring
-  auto stage = [&](int kt) __attribute__((always_inline)) -> int { return (NH == 2 ? (kt & 1) : kt % 3) * Rg::STAGE; };
-  auto issue_r = [&](int h, int kt, int q) __attribute__((always_inline)) {
-    dma_lds_x4(rbase + kt * rstep, sr[h].off[q], lds0 + (uint32_t)(stage(kt) + h * REGION + wave * 2048 + q * 1024));
+  // DMA number n of the cursor's slice into the ring at `stage`, its scales at `place`: R0, scales, C0 (0 .. 4), C1 (5, 6), R1 (7, 8; of 256 rows)
+  auto issue = [&](int n, int stage, int place) __attribute__((always_inline)) {
+    const uint32_t to = lds0 + (uint32_t)(stage + wave * 2048);
+    if (n < 2) dma_lds_x4(rbase, roff[0][n], to + n * 1024);
+    else if (n == 2) {
+      const uint32_t dst = lds0 + s_lds + (uint32_t)place;
+      if constexpr (FOLD) dma_lds_x1(sbase, soff, dst);
+      else dma_lds_u8(sbase, soff, dst);
+    }
+    else if (n < 5) dma_lds_x4(cbase[0], coff[0][n - 3], to + NH * REGION + (n - 3) * 1024);
+    else if (n < 7) dma_lds_x4(cbase[1], coff[1][n - 5], to + (NH + 1) * REGION + (n - 5) * 1024);
+    else if constexpr (NH == 2) dma_lds_x4(rbase, roff[1][n - 7], to + REGION + (n - 7) * 1024);
   };
-  auto issue_c = [&](int h, int kt, int q) __attribute__((always_inline)) {
-    dma_lds_x4(chalf[h] + kt * cstep, sc[h].off[q], lds0 + (uint32_t)(stage(kt) + (NH + h) * REGION + wave * 2048 + q * 1024));
-  };
-  auto issue_s = [&](int kt) __attribute__((always_inline)) {
-    const uint32_t dst = lds0 + s_lds + (uint32_t)(kt % 3 * Rg::SCALES);
-    if constexpr (FOLD) dma_lds_x1(sbase + kt * s_step, s_off, dst);
-    else dma_lds_u8(sbase + kt * s_step, s_off, dst);
-  };
-  // a slice's DMA number n: R0, scales, C0 (0 .. 4), C1 (5, 6), R1 (7, 8; of 256 rows)
-  auto issue_n = [&](int kt, int n) __attribute__((always_inline)) {
-    if (n < 2) issue_r(0, kt, n);
-    else if (n == 2) issue_s(kt);
-    else if (n < 5) issue_c(0, kt, n - 3);
-    else if (n < 7) issue_c(1, kt, n - 5);
-    else if constexpr (NH == 2) issue_r(1, kt, n - 7);
-  };
-  auto issue_slice = [&](int kt) __attribute__((always_inline)) {
-#pragma unroll
-    for (int n = 0; n < 5 + 2 * NH; ++n) issue_n(kt, n);
+  auto step = [&]() __attribute__((always_inline)) { rbase += rstep, cbase[0] += cstep, cbase[1] += cstep, sbase += s_step; };
+  // Behind a slice's DMAs.  (Behind the last tile's last slice the cursor stays on it: what it brings again is not read.)
+  auto advance = [&]() __attribute__((always_inline)) {
+    if (--left > 0) return;
+    if (at_tile + (int)gridDim.x < total) {
+      at_tile += gridDim.x;
+      open();
+    } else {
+      rstep = cstep = s_step = 0;
+      left = 0x7fffffff;
+    }
   };
 
+  // ------------------------------------------------------------------ products
   const Frag8<RK> fr(lane);
   const Frag8<CK> fc(lane);
   f32x4 acc[NH][2][4][2];
-#pragma unroll
-  for (int a = 0; a < NH; ++a)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[a][b][i][j] = f32x4{};
   i32x8 r[4], c[2][2];
-  const char* const scales = lds + Rg::SLICES * Rg::STAGE;
-  uint32_t rsc[4], csc[2][2];           // FOLD: a half's columns have one scale, csc[h][0]
-  auto read_r = [&](int i, int h, int kt) __attribute__((always_inline)) {
-    r[i] = fr.load(lds + stage(kt) + h * REGION, wm * 64 + i * 16);
-    rsc[i] = *reinterpret_cast<const uint32_t*>(scales + (kt % 3) * Rg::SCALES + (h * 128 + wm * 64 + i * 16 + l16) * 4);
+  uint32_t rsc[4], csc[2][2];                  // FOLD: a half's columns have one scale, csc[h][0]
+  int now = 0, sp = 0;                         // where the current slice is in the ring, and its scales (bytes)
+  const char* table = lds + Rg::TABLE;         // FOLD: block scales of the current tile from the current slice on
+  int table_half = 0;                          // and from one half to the other (bytes)
+  auto after = [](int place, int size, int n) __attribute__((always_inline)) -> int {
+    return n == 2 ? place ^ size : place == (n - 1) * size ? 0 : place + size;
   };
-  auto read_c = [&](int h, int kt) __attribute__((always_inline)) {
-    const char* s = scales + (kt % 3) * Rg::SCALES + NH * 512 + (h * 128 + wn * 32) * 4;
+  auto read_r = [&](int i, int h, int stage, int s) __attribute__((always_inline)) {
+    r[i] = fr.load(lds + stage + h * REGION, wm * 64 + i * 16);
+    rsc[i] = *reinterpret_cast<const uint32_t*>(lds + Rg::SLICES * Rg::STAGE + s + (h * 128 + wm * 64 + i * 16 + l16) * 4);
+  };
+  auto read_c = [&](int h, int stage, int s, const char* t) __attribute__((always_inline)) {
+    const char* from = lds + Rg::SLICES * Rg::STAGE + s + NH * 512 + (h * 128 + wn * 32) * 4;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      c[h][j] = fc.load(lds + stage(kt) + (NH + h) * REGION, wn * 32 + j * 16);
-      if (!FOLD) csc[h][j] = *reinterpret_cast<const uint32_t*>(s + (j * 16 + l16) * 4);
+      c[h][j] = fc.load(lds + stage + (NH + h) * REGION, wn * 32 + j * 16);
+      if (!FOLD) csc[h][j] = *reinterpret_cast<const uint32_t*>(from + (j * 16 + l16) * 4);
     }
-    if (FOLD) csc[h][0] = *reinterpret_cast<const uint32_t*>(table + (h * kMaxSlices + min(kt, kMaxSlices - 1)) * 4);
+    if (FOLD) csc[h][0] = *reinterpret_cast<const uint32_t*>(t + h * table_half);
   };
-  // A phase's products; after(i) reads into fragment i's place.  FOLD: a result is folded in three products after its own, when the
+  // A phase's products; then(i) reads into fragment i's place.  FOLD: a result is folded in three products after its own, when the
   // MFMA has long written it (so a phase's last three in the next one: `before` is the accumulator of the phase before)
   f32x4 pr[4];
   float prs[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) pr[q] = f32x4{}, prs[q] = 0.f;
   auto fold = [&](f32x4& a, int at, int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) a[q] = fmaf(pr[at][q], prs[i], a[q]);
   };
-  auto multiply = [&](f32x4 (&a)[4][2], f32x4 (&before)[4][2], int h, auto&& after) __attribute__((always_inline)) {
+  auto multiply = [&](f32x4 (&a)[4][2], f32x4 (&before)[4][2], int h, auto&& then) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     const float sb = FOLD && p.cs.bytes ? ue8m0_value(csc[h][0]) : __uint_as_float(csc[h][0]);
 #pragma unroll
@@ -278,152 +379,166 @@ __device__ __forceinline__ void tile_fp8(const Fp8Job& p, const Job& job, int64_
           a[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(c[h][j], r[i], a[i][j], 0, 0, 0, (int)csc[h][j], 0, (int)rsc[i]);
         }
       }
-      after(i);
+      then(i);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto nothing = [](int) __attribute__((always_inline)) {};
 
-  // The loop's body without branches, for slices behind which one is issued or none: across a branch the compiler
-  // moves products behind the DMAs and keeps all their operands in registers
-  auto body = [&](auto more, int kt) __attribute__((always_inline)) {
-    constexpr bool MORE = decltype(more)::value;
-    // published: `younger` DMAs of this wave may be in flight, every read so far is done; then for the workgroup
+  // A slice, without branches
+  auto body = [&]() __attribute__((always_inline)) {
+    const int next = after(now, Rg::STAGE, Rg::SLICES), sn = after(sp, Rg::SCALES, 3), s2 = after(sn, Rg::SCALES, 3);
+    // published: `younger` DMAs (or stores) of this wave may be in flight, every read so far is done; then for the workgroup
     auto meet = [&](auto younger) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (MORE) wait_vmcnt<decltype(younger)::value>();
-      else wait_vmcnt<0>();
+      wait_vmcnt<decltype(younger)::value>();
       wait_lds();
       barrier();
     };
-    // DMA n of the slice ahead.  They go out one at a time between products: eight waves' bursts behind a barrier would hold
-    // up every wave's next product until the addresses of all are taken
-    auto ahead = [&](int n) __attribute__((always_inline)) {
-      if constexpr (MORE) issue_n(kt + (NH == 2 ? 2 : 3), n);
-    };
+    // DMA n of the slice ahead, into the current one's place.  They go out one at a time between products: eight waves'
+    // bursts behind a barrier would hold up every wave's next product until the addresses of all are taken
+    auto ahead = [&](int n) __attribute__((always_inline)) { issue(n, now, NH == 2 ? s2 : sp); };
     if constexpr (NH == 2) {
       multiply(acc[0][0], acc[1][1], 0, [&](int i) __attribute__((always_inline)) {
-        if (i == 0) return;
+        if (i == 0) {
+          step();
+          return;
+        }
         if (i == 1) {
-          meet(std::integral_constant<int, 9>{});     // C1, R1(kt) are here; younger: kt + 1
-          read_c(1, kt);
+          meet(std::integral_constant<int, 9>{});     // C1, R1 of this slice are here; younger: the next slice
+          read_c(1, now, sp, table);
         }
         ahead(i - 1);
         __builtin_amdgcn_sched_barrier(0);
       });
       multiply(acc[0][1], acc[0][0], 1, [&](int i) __attribute__((always_inline)) {
-        read_r(i, 1, kt);
+        read_r(i, 1, now, sp);
         if (i & 1) ahead(3 + i / 2);
       });
       multiply(acc[1][0], acc[0][1], 0, [&](int i) __attribute__((always_inline)) {
-        if (i == 1) meet(std::integral_constant<int, 9>{});   // R0, C0(kt + 1); younger: C1, R1(kt + 1) and R0, scales, C0(kt + 2)
+        if (i == 1) meet(std::integral_constant<int, 9>{});   // the next slice's R0, C0; younger: its C1, R1 and R0, scales, C0 of the one ahead
         if (i & 1) ahead(5 + i / 2);
         __builtin_amdgcn_sched_barrier(0);
       });
-      read_c(0, kt + 1);                              // (behind the last slice: what the ring holds, not used)
+      read_c(0, next, sn, table + 4);                 // (behind the last slice: what the ring holds, not used)
       multiply(acc[1][1], acc[1][0], 1, [&](int i) __attribute__((always_inline)) {
-        read_r(i, 0, kt + 1);
+        read_r(i, 0, next, sn);
         if (i & 1) ahead(7 + i / 2);
       });
     } else {
-      read_c(1, kt);
-      multiply(acc[0][0], acc[0][1], 0, nothing);
+      read_c(1, now, sp, table);
+      multiply(acc[0][0], acc[0][1], 0, [&](int i) __attribute__((always_inline)) {
+        if (i == 0) step();
+      });
       multiply(acc[0][1], acc[0][0], 1, [&](int i) __attribute__((always_inline)) {
         if (i == 0) return;
         if (i == 1) {
-          meet(std::integral_constant<int, 7>{});     // slice kt + 1; younger: kt + 2
-          read_c(0, kt + 1);
-          read_r(0, 0, kt + 1);
+          meet(std::integral_constant<int, 7>{});     // the next slice; younger: the one behind it
+          read_c(0, next, sn, table + 4);
+          read_r(0, 0, next, sn);
         }
-        read_r(i, 0, kt + 1);
+        read_r(i, 0, next, sn);
 #pragma unroll
         for (int n = 0; n < 7; ++n)
           if (n / 3 == i - 1 || (n == 6 && i == 3)) ahead(n);
       });
     }
-  };
-  constexpr int AHEAD = NH == 2 ? 2 : 3;
-  if (KT > 0) {
-    if constexpr (FOLD) issue_table();
-    issue_slice(0);
-    if (KT > 1) issue_slice(1);
-    if (NH == 1 && KT > 2) issue_slice(2);
-    if (KT >= AHEAD) wait_vmcnt<NH == 2 ? 13 : 14>();
-    else wait_vmcnt<0>();
-    barrier();                             // slice 0 has landed (of 256 rows, R0 and C0)
+    now = next;
+    sp = sn;
+    table += 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) read_r(i, 0, 0);
-    read_c(0, 0);
-    int kt = 0;
-    for (; kt + AHEAD < KT; ++kt) body(std::true_type{}, kt);
-    for (; kt < KT; ++kt) body(std::false_type{}, kt);
+    for (int a = 0; a < NH; ++a) formed(acc[a][0]), formed(acc[a][1]);
+    if constexpr (FOLD) asm volatile("" : "+v"(pr[1]), "+v"(pr[2]), "+v"(pr[3]));
+  };
+
+  open();
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) {
+    step();
+#pragma unroll
+    for (int n = 0; n < DMAS; ++n) issue(n, a * Rg::STAGE, a * Rg::SCALES);
+    advance();
+  }
+  wait_vmcnt<0>();                             // (the first slices)
+  barrier();
+  int table_of = 0;
+  for (int t = first; t < total; t += gridDim.x) {
+    const Tile x = TILES::template at<NH>(argument(), t);
+    const int n0 = x.nt * (EPI == kGated ? 128 : 256);
+    if constexpr (FOLD) {
+      table = lds + Rg::TABLE + table_of * 4;
+      table_half = ((x.KT + 63) & ~63) * 4;
+      table_of = table_next(table_of, x.KT);
+    }
+#pragma unroll
+    for (int a = 0; a < NH; ++a)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[a][b][i][j] = f32x4{};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) pr[q] = f32x4{}, prs[q] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) read_r(i, 0, now, sp);
+    read_c(0, now, sp, table);
+    for (int kt = 0; kt < x.KT; ++kt) {
+      body();
+      advance();
+    }
     if constexpr (FOLD) {
 #pragma unroll
       for (int n = 5; n < 8; ++n) fold(acc[NH - 1][1][n >> 1][n & 1], n & 3, n >> 1);
     }
-  }
-
-#pragma unroll
-  for (int a = 0; a < NH; ++a) {
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) eight_columns(acc[a][b][i][0], acc[a][b][i][1]);
-    const int64_t m = m0 + a * 128 + wm * 64 + l16;
-    const int col = n0 + wn * 32 + 8 * g4;
-    if constexpr (EPI == kGated) {
-      store_rows<uint16_t, EPI>(job, split, m, col, acc[a][0], acc[a][1]);
-    } else {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) store_rows<uint16_t, EPI>(job, split, m, col + b * 128, acc[a][b], acc[a][b]);
+    const Fp8Job& q = argument();
+    Job job = q.j;
+    job.g.M = x.m0 + x.rows;
+    job.g.e.out_f32 = 0;                       // (what is known of these products' epilogue)
+    job.g.e.vec = 1;
+    if constexpr (EPI == kGated) job.g.e.bias = job.g.e.res = nullptr;
+    if constexpr (std::is_same_v<TILES, DwTiles>) {
+      job.g.M = q.j.g.M;
+      if (q.E) job.g.e.out = static_cast<uint16_t*>(job.g.e.out) + (int64_t)x.e * job.g.M * job.g.e.N;
+    } else if (!q.E) {
+      job.g.M = q.j.g.M;
     }
+#pragma unroll
+    for (int a = 0; a < NH; ++a)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) eight_columns(acc[a][b][i][0], acc[a][b][i][1]);
+        if (EPI == kGated && b == 0) continue;
+        __builtin_amdgcn_sched_barrier(0);
+        const int who = lane_again();
+        const int64_t m = x.m0 + a * 128 + wm * 64 + (who & 15);
+        const int col = n0 + wn * 32 + 8 * (who >> 4);
+        if constexpr (EPI == kGated) store_rows<uint16_t, EPI>(job, x.split, m, col, acc[a][0], acc[a][1]);
+        else store_rows<uint16_t, EPI>(job, x.split, m, col + b * 128, acc[a][b], acc[a][b]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
   }
+  wait_vmcnt<0>();                             // no DMA outlives the workgroup's LDS
 }
 
-// Forward and dx: rows in tiles, over one matrix (splits along blockIdx.y) or by runs of rows
+// One workgroup a CU
 template <bool CK, int EPI, int NH, bool FOLD>
 __global__ __launch_bounds__(512, 1) void fp8_rows_tile_kernel(Fp8Job p) {
   __shared__ __attribute__((aligned(1024))) char lds[Ring<NH>::BYTES];
-  Job job = p.j;
-  if (p.E) job.mt = p.runs.count[0];
-  int mt, nt;
-  if (!tile_of(job, blockIdx.x, mt, nt)) return;
-  int64_t m0 = (int64_t)mt * 128 * NH, rows = job.g.M - m0;
-  int e = 0;
-  if (p.E) {
-    const RowTile t = p.runs.tiles[mt];
-    m0 = t.row0;
-    rows = t.rows;
-    e = t.expert;
-    job.g.M = m0 + rows;
-  }
-  const int64_t kt0 = (int64_t)blockIdx.y * job.slices;
-  const int KT = (int)min((int64_t)job.slices, job.g.K / 128 - kt0);
-  tile_fp8<false, CK, EPI, NH, FOLD>(p, job, m0, rows, nt, e, kt0, KT, blockIdx.y, lds);
+  run_tiles<RowTiles, false, CK, EPI, NH, FOLD>(p, lds);
 }
 
-// dw: contractions over the rows in tiles of 128 (a run's last filled up with zeros): all of them (splits along
-// blockIdx.y) or each run's (run blockIdx.y)
 template <int NH>
 __global__ __launch_bounds__(512, 1) void fp8_dw_kernel(Fp8Job p) {
   __shared__ __attribute__((aligned(1024))) char lds[Ring<NH>::BYTES];
-  Job job = p.j;
-  int mt, nt;
-  if (!tile_of(job, blockIdx.x, mt, nt)) return;
-  const int64_t m0 = (int64_t)mt * 128 * NH;
-  int64_t kt0;
-  int KT, split = 0;
-  if (p.E) {
-    const int e = blockIdx.y;
-    kt0 = p.runs.group[e];
-    KT = (int)(p.runs.group[e + 1] - kt0);
-    job.g.e.out = static_cast<uint16_t*>(job.g.e.out) + (int64_t)e * job.g.M * job.g.e.N;
-  } else {
-    split = blockIdx.y;
-    kt0 = (int64_t)split * job.slices;
-    KT = (int)min((int64_t)job.slices, job.g.K / 128 - kt0);
+  run_tiles<DwTiles, true, true, kGrad, NH, false>(p, lds);
+  if (!p.E) return;
+  // experts without rows: zeros
+  const int64_t size = p.j.g.M * p.j.g.e.N / 8;            // 16-byte pieces of one expert's dw
+  for (int i = p.runs.count[2]; i < p.E; ++i) {
+    i32x4* out = reinterpret_cast<i32x4*>(p.j.g.e.out) + p.runs.order[i] * size;
+    for (int64_t k = (int64_t)blockIdx.x * 512 + threadIdx.x; k < size; k += (int64_t)gridDim.x * 512) out[k] = i32x4{};
   }
-  tile_fp8<true, true, kGrad, NH, false>(p, job, m0, job.g.M - m0, nt, 0, kt0, KT, split, lds);
 }
 
 inline Fp8Job fp8_job(const Fp8Gemm& g, const Job& job) {
@@ -438,8 +553,10 @@ inline Fp8Job fp8_job(const Fp8Gemm& g, const Job& job) {
   p.runs = g.runs;
   return p;
 }
-inline dim3 fp8_grid(const Job& job, int y) {
-  return dim3((unsigned)(((int64_t)job.mt * job.nt + 7) / 8 * 8), (unsigned)y);
+// `parts`: splits, or experts of dw
+inline dim3 fp8_grid(const Job& job, int64_t parts) {
+  const int64_t tiles = ((int64_t)job.mt * job.nt * parts + 7) / 8 * 8;
+  return dim3((unsigned)(tiles < 256 ? tiles : 256));
 }
 
 // Costs of a tile, as in dense_plan.h, in slices of 128 k
