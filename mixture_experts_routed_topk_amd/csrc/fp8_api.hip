@@ -75,7 +75,7 @@ Fp8Gemm forward_gemm(const Size& z) {
 ForwardLayout forward_layout(const Size& z) {
   ForwardLayout L{};
   if (z.T == 0) return L;
-  L.gemm = z.E ? up256(runs_bytes(z.T, z.E, fp8_grouped_height(z.T, z.E))) : 0;
+  L.gemm = z.E ? up256(runs_bytes(z.T, z.E, fp8_grouped_height(z.T, z.E, z.K, z.cols))) : 0;
   L.total = L.gemm + fp8_gemm_workspace(forward_gemm(z));
   return L;
 }
@@ -94,7 +94,7 @@ BackwardLayout backward_layout(const Size& z, bool bias) {
     o = up256(o + bytes);
     return at;
   };
-  L.runs = take(z.E ? runs_bytes(z.T, z.E, fp8_grouped_height(z.T, z.E)) : 0);
+  L.runs = take(z.E ? runs_bytes(z.T, z.E, fp8_dx_height(z.T, z.E)) : 0);
   L.zr = take(z.T * z.cols);
   L.zr_scale = take(z.T * (z.cols / 128) * 4);
   L.zc = take(L.tiles * 128 * z.cols);
@@ -102,8 +102,7 @@ BackwardLayout backward_layout(const Size& z, bool bias) {
   L.xc = take(L.tiles * 128 * z.K);
   L.xc_scale = take(L.tiles * z.K);
   L.part = take(bias ? L.tiles * z.cols * 4 : 0);
-  const size_t dx = fp8_dx_workspace(z.T, z.K, z.cols, z.E), dw = fp8_dw_workspace(z.T, z.K, z.cols, z.E);
-  L.gemm = take(dx > dw ? dx : dw);    // (one after the other)
+  L.gemm = take(fp8_gradients_workspace(z.T, z.K, z.cols, z.E));
   L.total = o;
   return L;
 }
@@ -144,7 +143,7 @@ moe_status run_forward(const moe_fp8_problem* p, bool gated, const uint8_t* x_q,
   g.g.e.act = z.act;
   g.g.e.vec = 1;
   if (z.E) {
-    g.runs = runs_at(ws, z.T, z.E, fp8_grouped_height(z.T, z.E));
+    g.runs = runs_at(ws, z.T, z.E, fp8_grouped_height(z.T, z.E, z.K, z.cols));
     MOE_HIP_CHECK(launch_runs(g.runs, offsets, z.T, z.E, s));
   }
   MOE_HIP_CHECK(launch_fp8_gemm(g, ws + L.gemm, s));
@@ -176,7 +175,7 @@ moe_status run_backward(const moe_fp8_problem* p, bool gated, const void* dy, co
   auto bytes = [&](size_t at) { return reinterpret_cast<uint8_t*>(ws + at); };
   Runs runs{};
   if (z.E) {
-    runs = runs_at(ws + L.runs, z.T, z.E, fp8_grouped_height(z.T, z.E));
+    runs = runs_at(ws + L.runs, z.T, z.E, fp8_dx_height(z.T, z.E));
     MOE_HIP_CHECK(launch_runs(runs, offsets, z.T, z.E, s));
   }
   GroupsArgs a{};
@@ -208,8 +207,9 @@ moe_status run_backward(const moe_fp8_problem* p, bool gated, const void* dy, co
   a.max_tiles = L.tiles;
   MOE_HIP_CHECK(launch_groups(a, s));
   if (dbias) MOE_HIP_CHECK(launch_column_sum(a.part, L.tiles, z.cols, dbias, false, s));
+  Fp8Gemm gx{}, gw{};
   if (dx) {
-    Fp8Gemm g{};
+    Fp8Gemm& g = gx;
     g.g.r = a.zr;
     g.g.ldr = z.cols;
     g.rs = Fp8Scales{a.zr_scale, z.cols / 128, 1, z.ue8m0};
@@ -221,10 +221,9 @@ moe_status run_backward(const moe_fp8_problem* p, bool gated, const void* dy, co
     g.g.e.N = (int)z.K;
     g.g.e.vec = 1;
     g.runs = runs;
-    MOE_HIP_CHECK(launch_fp8_dx(g, ws + L.gemm, s));
   }
   if (dw) {
-    Fp8Gemm g{};
+    Fp8Gemm& g = gw;
     g.g.r = a.zc;
     g.g.ldr = z.cols;
     g.g.r_kmajor = 1;
@@ -241,8 +240,8 @@ moe_status run_backward(const moe_fp8_problem* p, bool gated, const void* dy, co
     g.g.e.ldo = z.K;
     g.g.e.N = (int)z.K;
     g.g.e.vec = 1;
-    MOE_HIP_CHECK(launch_fp8_dw(g, ws + L.gemm, s));
   }
+  if (dx || dw) MOE_HIP_CHECK(launch_fp8_gradients(dx ? &gx : nullptr, dw ? &gw : nullptr, ws + L.gemm, s));
   return MOE_OK;
 }
 

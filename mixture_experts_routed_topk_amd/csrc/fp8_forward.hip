@@ -6,9 +6,10 @@ namespace moe {
 namespace {
 
 template <int EPI>
-hipError_t launch_tiles(const Fp8Job& p, int tile, int y, hipStream_t s) {
-  if (tile == 256) hipLaunchKernelGGL((fp8_rows_tile_kernel<false, EPI, 2, true>), fp8_grid(p.j, y), dim3(512), 0, s, p);
-  else hipLaunchKernelGGL((fp8_rows_tile_kernel<false, EPI, 1, true>), fp8_grid(p.j, y), dim3(512), 0, s, p);
+hipError_t launch_tiles(const Fp8Job& p, int tile, hipStream_t s) {
+  const dim3 grid = fp8_grid((int64_t)p.j.mt * p.j.nt * p.j.splits);
+  if (tile == 256) hipLaunchKernelGGL((fp8_forward_kernel<EPI, 2>), grid, dim3(512), 0, s, p);
+  else hipLaunchKernelGGL((fp8_forward_kernel<EPI, 1>), grid, dim3(512), 0, s, p);
   return hipGetLastError();
 }
 
@@ -17,7 +18,19 @@ bool plain(const DenseEpi& e) { return !e.bias && !e.res && !e.pre && e.act == k
 
 }  // namespace
 
-int fp8_grouped_height(int64_t T, int E) { return T >= (int64_t)192 * E ? 256 : 128; }
+// The height whose rounds of tiles take less, with half a tile of every run empty.  Over 90 products of 8 to 64 runs of 32 to 512 rows on
+// average this takes 0.9% longer than the better height (28% at most, where the uneven runs fill one round more or less);
+// 256 rows from 192 a run on would take 2.9% longer, from 400 on 1.4%.
+int fp8_grouped_height(int64_t T, int E, int64_t K, int64_t cols) {
+  double best = 1e30;
+  int rows = 0;
+  for (const TileCost& t : kTilesFp8) {
+    const double tiles = fmax((double)T / t.rows + 0.5 * E, (double)(T < E ? T : E)) * ((cols + 255) / 256);
+    const double us = ceil(tiles / 256) * ((K / 128) * t.alone + t.fixed);
+    if (us < best) best = us, rows = t.rows;
+  }
+  return rows;
+}
 
 size_t fp8_gemm_workspace(const Fp8Gemm& g) {
   if (g.g.M == 0 || g.E || fp8_rows_take(g.g.M, g.g.K)) return 0;
@@ -35,15 +48,15 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t s) {
     job.mt = (int)max_row_tiles(g.g.M, g.E, height);
     job.nt = (job.crows + 255) / 256;
     const Fp8Job p = fp8_job(g, job);
-    return g.g.gated ? launch_tiles<kGated>(p, height, 1, s) : launch_tiles<kGrad>(p, height, 1, s);
+    return g.g.gated ? launch_tiles<kGated>(p, height, s) : launch_tiles<kGrad>(p, height, s);
   }
   if (fp8_rows_take(g.g.M, g.g.K)) return launch_fp8_rows(g, s);
   const Plan plan = plan_fp8(g.g.M, g.g.e.N, g.g.K, g.g.gated);
   return run_forward<uint16_t>(g.g, plan, 256, ws, s, [&](const Job& job, int epi) {
     const Fp8Job p = fp8_job(g, job);
-    if (epi == kPartial) return launch_tiles<kPartial>(p, plan.tile, job.splits, s);
-    if (epi == kGated) return launch_tiles<kGated>(p, plan.tile, 1, s);
-    return plain(g.g.e) ? launch_tiles<kGrad>(p, plan.tile, 1, s) : launch_tiles<kLinear>(p, plan.tile, 1, s);
+    if (epi == kPartial) return launch_tiles<kPartial>(p, plan.tile, s);
+    if (epi == kGated) return launch_tiles<kGated>(p, plan.tile, s);
+    return plain(g.g.e) ? launch_tiles<kGrad>(p, plan.tile, s) : launch_tiles<kLinear>(p, plan.tile, s);
   });
 }
 

@@ -12,7 +12,10 @@ constexpr int kFp8Group = 128;        // elements that share a scale, and k of a
 // Where each expert's rows are, and the rows cut into tiles that do not cross experts.  Made on the
 // device from offsets [E + 1], whose values are taken into [0, T] and made non-decreasing, so that no table leads outside.
 struct RowTile {
-  int32_t expert, row0, rows, pad;
+  int32_t expert;
+  int32_t start, end;   // the expert's rows
+  int32_t first, count; // its tiles
+  int32_t pad[3];
 };
 struct Runs {
   int32_t* start;       // [E + 1]
@@ -82,16 +85,14 @@ struct Fp8Gemm {
   int64_t cs_expert;            // entries
   Runs runs;
 };
-// Rows of the tiles that a grouped product of T rows takes
-int fp8_grouped_height(int64_t T, int E);
+// Rows of the tiles that a product by runs takes: forward, K x cols weights an expert, and dx
+int fp8_grouped_height(int64_t T, int E, int64_t K, int64_t cols);
+int fp8_dx_height(int64_t T, int E);
 size_t fp8_gemm_workspace(const Fp8Gemm& g);
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t s);
-// r (codes [T][cols]) along k, c along its rows
-size_t fp8_dx_workspace(int64_t T, int64_t K, int64_t cols, int E);
-hipError_t launch_fp8_dx(const Fp8Gemm& g, void* ws, hipStream_t s);
-// both operands along their rows; g.g.K: rows of all 128-row tiles
-size_t fp8_dw_workspace(int64_t T, int64_t K, int64_t cols, int E);
-hipError_t launch_fp8_dw(const Fp8Gemm& g, void* ws, hipStream_t s);
+// dx: r (codes [T][cols]) along k, c along its rows; dw: both along their rows, g.K: rows of all 128-row tiles.  Either may be null.
+size_t fp8_gradients_workspace(int64_t T, int64_t N, int64_t cols, int E);
+hipError_t launch_fp8_gradients(const Fp8Gemm* dx, const Fp8Gemm* dw, void* ws, hipStream_t s);
 
 // forward products of few rows
 bool fp8_rows_take(int64_t M, int64_t K);

@@ -159,8 +159,9 @@ __global__ __launch_bounds__(kThreads) void groups_kernel(GroupsArgs a, int dz_b
   int rows = (int)min((int64_t)128, a.T - row0);
   if (a.tiles) {
     if (tile >= a.count[0]) return;
-    row0 = a.tiles[tile].row0;
-    rows = a.tiles[tile].rows;
+    const RowTile t = a.tiles[tile];
+    row0 = t.start + (tile - t.first) * 128;
+    rows = min(128, t.end - (int)row0);
   }
   const int sub = threadIdx.x & 15;
   const int64_t cols = GATED ? 2 * (int64_t)a.N : a.N;
@@ -284,15 +285,14 @@ __device__ __forceinline__ int32_t scan(int32_t v, int32_t* lds, F&& join) {
   return v;
 }
 
-__device__ void list_tiles(RowTile* out, const int32_t* start, const int32_t* first, int E, int n, int height) {
+__device__ void list_tiles(RowTile* out, const int32_t* start, const int32_t* first, int E, int n) {
   for (int i = threadIdx.x; i < n; i += kMaxE) {
     int lo = 0, hi = E - 1;           // the last expert whose first tile is at most i, and which has one
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (first[mid] <= i) lo = mid; else hi = mid - 1;
     }
-    const int row0 = start[lo] + (i - first[lo]) * height;
-    out[i] = RowTile{lo, row0, min(height, start[lo + 1] - row0), 0};
+    out[i] = RowTile{lo, start[lo], start[lo + 1], first[lo], first[lo + 1] - first[lo], {}};
   }
 }
 
@@ -318,8 +318,8 @@ __global__ __launch_bounds__(kMaxE) void runs_kernel(Runs r, const int32_t* __re
   if (e < E) r.order[cnt > 0 ? live - 1 : alive + e - live] = e;
   for (int i = e; i <= E; i += kMaxE) r.start[i] = start[i], r.group[i] = group[i];
   if (e == 0) r.count[0] = first[E], r.count[1] = group[E];
-  list_tiles(r.tiles, start, first, E, first[E], r.height);
-  if (r.height != 128) list_tiles(r.groups, start, group, E, group[E], 128);
+  list_tiles(r.tiles, start, first, E, first[E]);
+  if (r.height != 128) list_tiles(r.groups, start, group, E, group[E]);
 }
 
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }

@@ -129,11 +129,13 @@ __device__ __forceinline__ int lane_again() {
   return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, (uint32_t)zero));
 }
 
-// The kernel's argument (its only one), read from memory again: what a tile needs once does not occupy scalar registers in the loop
+// The kernel's argument number J, read from memory again: what a tile needs once does not occupy scalar registers in the loop.
+// (Kernels take one or two of these and nothing in front of them.)
+template <int J>
 __device__ __forceinline__ const Fp8Job& argument() {
   auto p = __builtin_amdgcn_kernarg_segment_ptr();
   asm volatile("" : "+s"(p));
-  return *(const Fp8Job*)p;
+  return ((const Fp8Job*)p)[J];
 }
 
 // The values are formed here: products that only later code reads would be moved there, behind branches, and their
@@ -175,12 +177,15 @@ struct RowTiles {
     Tile x{};
     Job j = p.j;
     if (p.E) {
-      j.mt = table_entry(p.runs.count, 0);
+      // an expert's tiles follow one another: entry t / nt of the list is one of its row tiles
+      const int64_t at = (int64_t)(t / j.nt) * (sizeof(RowTile) / 4);
+      x.e = table_entry(p.runs.tiles, at);
+      const int start = table_entry(p.runs.tiles, at + 1), end = table_entry(p.runs.tiles, at + 2);
+      j.mt = table_entry(p.runs.tiles, at + 4);
       int mt;
-      tile_at(j, t, mt, x.nt);
-      x.e = table_entry(p.runs.tiles, (int64_t)mt * 4);
-      x.m0 = table_entry(p.runs.tiles, (int64_t)mt * 4 + 1);
-      x.rows = table_entry(p.runs.tiles, (int64_t)mt * 4 + 2);
+      tile_at(j, t - table_entry(p.runs.tiles, at + 3) * j.nt, mt, x.nt);
+      x.m0 = start + mt * 128 * NH;
+      x.rows = min(128 * NH, end - (int)x.m0);
       x.KT = j.slices;
     } else {
       const int per = j.mt * j.nt;
@@ -219,8 +224,32 @@ struct DwTiles {
   }
 };
 
-template <typename TILES, bool RK, bool CK, int EPI, int NH, bool FOLD>
-__device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds) {
+// Which tiles of a job a workgroup takes: each by itself would go round all G workgroups.  Where another job's last round
+// leaves `heavy` of them with a tile more, the others take `extra` tiles of this one first; the last rounds then
+// begin at the less loaded ones.
+struct Share {
+  int G, heavy, early, at;      // early: tiles that go to the others first; at: this workgroup's place in the full rounds
+  __device__ __forceinline__ Share(int q, int workgroups, int heavy_, int extra, bool others_first) {
+    G = workgroups;
+    heavy = heavy_;
+    early = heavy ? extra * (G - heavy) : 0;
+    at = !others_first ? q : q < heavy ? q + G - heavy : q - heavy;
+  }
+  __device__ __forceinline__ int first(int q) const { return q >= heavy && early > 0 ? q - heavy : early + at; }
+  __device__ __forceinline__ int next(int t) const {
+    if (t >= early) return t + G;
+    t += G - heavy;
+    return t < early ? t : early + at;
+  }
+};
+
+// Workgroups go to the eight XCDs in turn: each XCD takes a run of neighbouring tiles of every round, so that the 32 that run
+// on it together are 8 x 4 and share their operands in its L2
+__device__ __forceinline__ int place_in_round() { return (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3); }
+
+// This workgroup's tiles of job J
+template <typename TILES, int J, bool RK, bool CK, int EPI, int NH, bool FOLD>
+__device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds, const Share& share) {
   using Rg = Ring<NH>;
   constexpr int AHEAD = Rg::SLICES;
   constexpr int DMAS = 5 + 2 * NH;             // of a wave and slice
@@ -229,12 +258,11 @@ __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int l16 = lane & 15;
-  // Workgroups go to the eight XCDs in turn: each XCD takes a run of neighbouring tiles of every round, so that the 32 that run
-  // on it together are 8 x 4 and share their operands in its L2
   const int total = TILES::count(p);
-  const int first = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const int first = share.first(place_in_round());
   if (first >= total) return;
   const uint32_t lds0 = lds_addr(lds);
+  barrier();                                   // (a job before may still be read)
 
   // ------------------------------------------------------------------ DMAs: a cursor over tiles and their slices, on the one issued last
   int at_tile = first, left;                   // the tile, and how many of its slices are still to be issued
@@ -253,7 +281,7 @@ __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds) {
     return next + 2 * ((KT + 63) & ~63) > Rg::TABLES / 4 ? 0 : next;
   };
   auto open = [&]() __attribute__((always_inline)) {         // addresses of tile at_tile
-    const Fp8Job& p = argument();
+    const Fp8Job& p = argument<J>();
     const DenseGemm& g = p.j.g;
     const Tile x = TILES::template at<NH>(p, at_tile);
     const int lane = lane_again();
@@ -321,8 +349,9 @@ __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds) {
   // Behind a slice's DMAs.  (Behind the last tile's last slice the cursor stays on it: what it brings again is not read.)
   auto advance = [&]() __attribute__((always_inline)) {
     if (--left > 0) return;
-    if (at_tile + (int)gridDim.x < total) {
-      at_tile += gridDim.x;
+    const int next = share.next(at_tile);
+    if (next < total) {
+      at_tile = next;
       open();
     } else {
       rstep = cstep = s_step = 0;
@@ -461,8 +490,8 @@ __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds) {
   wait_vmcnt<0>();                             // (the first slices)
   barrier();
   int table_of = 0;
-  for (int t = first; t < total; t += gridDim.x) {
-    const Tile x = TILES::template at<NH>(argument(), t);
+  for (int t = first; t < total; t = share.next(t)) {
+    const Tile x = TILES::template at<NH>(argument<J>(), t);
     const int n0 = x.nt * (EPI == kGated ? 128 : 256);
     if constexpr (FOLD) {
       table = lds + Rg::TABLE + table_of * 4;
@@ -490,7 +519,7 @@ __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds) {
 #pragma unroll
       for (int n = 5; n < 8; ++n) fold(acc[NH - 1][1][n >> 1][n & 1], n & 3, n >> 1);
     }
-    const Fp8Job& q = argument();
+    const Fp8Job& q = argument<J>();
     Job job = q.j;
     job.g.M = x.m0 + x.rows;
     job.g.e.out_f32 = 0;                       // (what is known of these products' epilogue)
@@ -522,21 +551,32 @@ __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds) {
 }
 
 // One workgroup a CU
-template <bool CK, int EPI, int NH, bool FOLD>
-__global__ __launch_bounds__(512, 1) void fp8_rows_tile_kernel(Fp8Job p) {
+template <int EPI, int NH>
+__global__ __launch_bounds__(512, 1) void fp8_forward_kernel(Fp8Job p) {
   __shared__ __attribute__((aligned(1024))) char lds[Ring<NH>::BYTES];
-  run_tiles<RowTiles, false, CK, EPI, NH, FOLD>(p, lds);
+  run_tiles<RowTiles, 0, false, false, EPI, NH, true>(p, lds, Share(place_in_round(), gridDim.x, 0, 0, false));
 }
 
-template <int NH>
-__global__ __launch_bounds__(512, 1) void fp8_dw_kernel(Fp8Job p) {
-  __shared__ __attribute__((aligned(1024))) char lds[Ring<NH>::BYTES];
-  run_tiles<DwTiles, true, true, kGrad, NH, false>(p, lds);
-  if (!p.E) return;
+// Both gradients: the product with the shorter tiles fills the other's uneven end
+struct Fill {
+  int dw;             // which product fills
+  int extra;          // tiles of it that take as long as one of the other's
+  int others_first;
+};
+template <int NX, int NW, bool FOLD>
+__global__ __launch_bounds__(512, 1) void fp8_gradients_kernel(Fp8Job dx, Fp8Job dw, Fill fill) {
+  __shared__ __attribute__((aligned(1024))) char lds[Ring<2>::BYTES];
+  static_assert(Ring<1>::BYTES == Ring<2>::BYTES, "one buffer for both");
+  const int G = gridDim.x, q = place_in_round();
+  const int heavy = (fill.dw ? RowTiles::count(argument<0>()) : DwTiles::count(argument<1>())) % G;
+  const bool others = fill.others_first && heavy;
+  run_tiles<DwTiles, 1, true, true, kGrad, NW, false>(argument<1>(), lds, Share(q, G, fill.dw ? heavy : 0, fill.extra, fill.dw && others));
+  run_tiles<RowTiles, 0, false, true, kGrad, NX, FOLD>(argument<0>(), lds, Share(q, G, fill.dw ? 0 : heavy, fill.extra, !fill.dw && others));
+  if (!dw.E || !dw.j.nt) return;
   // experts without rows: zeros
-  const int64_t size = p.j.g.M * p.j.g.e.N / 8;            // 16-byte pieces of one expert's dw
-  for (int i = p.runs.count[2]; i < p.E; ++i) {
-    i32x4* out = reinterpret_cast<i32x4*>(p.j.g.e.out) + p.runs.order[i] * size;
+  const int64_t size = dw.j.g.M * dw.j.g.e.N / 8;          // 16-byte pieces of one expert's dw
+  for (int i = dw.runs.count[2]; i < dw.E; ++i) {
+    i32x4* out = reinterpret_cast<i32x4*>(dw.j.g.e.out) + dw.runs.order[i] * size;
     for (int64_t k = (int64_t)blockIdx.x * 512 + threadIdx.x; k < size; k += (int64_t)gridDim.x * 512) out[k] = i32x4{};
   }
 }
@@ -553,15 +593,12 @@ inline Fp8Job fp8_job(const Fp8Gemm& g, const Job& job) {
   p.runs = g.runs;
   return p;
 }
-// `parts`: splits, or experts of dw
-inline dim3 fp8_grid(const Job& job, int64_t parts) {
-  const int64_t tiles = ((int64_t)job.mt * job.nt * parts + 7) / 8 * 8;
-  return dim3((unsigned)(tiles < 256 ? tiles : 256));
-}
+inline dim3 fp8_grid(int64_t tiles) { return dim3((unsigned)(tiles < 256 ? (tiles + 7) / 8 * 8 : 256)); }
 
-// Costs of a tile, as in dense_plan.h, in slices of 128 k
-constexpr TileCost kTilesFp8[] = {{256, 256, 1, 1.25, 1.25, 7.0}, {128, 256, 1, 0.8, 0.8, 4.0}};
-constexpr JoinCost kJoinFp8 = {2.8, 3.36e6};
+// Costs of a forward product's tiles, as in dense_plan.h, in slices of 128 k.  Fitted to 68 products of 40 to 16384 rows, each
+// measured with both heights and every split (rms error 10%; the choices take 1.1% longer than the best measured, 14% at most).
+constexpr TileCost kTilesFp8[] = {{256, 256, 1, 1.55, 1.55, 5.3}, {128, 256, 1, 0.96, 0.96, 3.8}};
+constexpr JoinCost kJoinFp8 = {5.6, 3.9e6};
 
 inline Plan plan_fp8(int64_t M, int64_t N, int64_t K, int gated) {
   return plan_forward<uint8_t>(kTilesFp8, kJoinFp8, M, N, K, gated);
