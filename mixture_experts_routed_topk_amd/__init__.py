@@ -740,7 +740,7 @@ def _positions(inv: torch.Tensor, T: int, dev: int) -> int:
     """Checks the sorted positions of T tokens' slots; returns the slots of a token."""
     if not isinstance(inv, torch.Tensor) or inv.dtype is not torch.int32:
         raise ValueError("inv must be an int32 tensor")
-    if inv.get_device() != dev or inv.device.type != "cuda":
+    if inv.get_device() != dev:
         raise ValueError(f"inv is on {inv.device}, the call's other tensors on cuda:{dev}")
     if not inv.is_contiguous():
         raise ValueError("inv must be contiguous")
@@ -804,10 +804,13 @@ def unpermute(y: torch.Tensor, inv: torch.Tensor, topk_w: torch.Tensor) -> torch
 def _unpermute(name, y, inv, topk_w, T):
     dt, dev = _matrix(name, y)
     rows, H = y.shape
+    ld, inner = y.stride()
+    if inner != 1 or ld < H or rows <= 1:
+        ld = _rows(name, y, rows, H, y.dtype, dev)
     k = _positions(inv, T, dev)
     if topk_w is not None:
         _packed("topk_w", topk_w, (T, topk_w.shape[1] if T == 0 else k), torch.float32, dev)
-    prob, _ = _problem(PermuteProblem, (T, rows, H, k, dt, 0, _rows(name, y, rows, H, y.dtype, dev)))
+    prob, _ = _problem(PermuteProblem, (T, rows, H, k, dt, 0, ld))
     out = y.new_empty((T, H))
     _run(lib().moe_unpermute, dev, prob, y.data_ptr(), inv.data_ptr(), _addr(topk_w), out.data_ptr())
     return out
@@ -849,13 +852,13 @@ def quantize_blocks_fp8(w: torch.Tensor, ue8m0: bool = False):
     if not isinstance(w, torch.Tensor) or w.dtype not in _ACT or w.dim() not in (2, 3):
         raise ValueError("w must be a bf16 or float32 tensor of two or three dimensions")
     _need_gpu("w", w)
-    N, K = w.shape[-2:]
+    shape = w.shape
+    N, K = shape[-2:]
     if N % 128 or K % 128:
         raise ValueError("both sides of a weight matrix must be multiples of 128")
-    count = w.shape[0] if w.dim() == 3 else 1
-    q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
-    scales = torch.empty(w.shape[:-2] + (N // 128, K // 128), dtype=torch.uint8 if ue8m0 else torch.float32, device=w.device)
-    _run(lib().moe_quantize_blocks_fp8, w.get_device(), w.data_ptr(), _ACT[w.dtype], count, N, K,
+    q = w.new_empty(shape, dtype=torch.uint8)
+    scales = w.new_empty((*shape[:-2], N // 128, K // 128), dtype=torch.uint8 if ue8m0 else torch.float32)
+    _run(lib().moe_quantize_blocks_fp8, w.get_device(), w.data_ptr(), _ACT[w.dtype], shape[0] if len(shape) == 3 else 1, N, K,
          SCALE_UE8M0 if ue8m0 else SCALE_F32, q.data_ptr(), scales.data_ptr())
     return q, scales
 
@@ -894,6 +897,42 @@ def _fp8_rows(x_q, x_scale):
     return T, K, dev, _rows("x_q", x_q, T, K, x_q.dtype, dev)
 
 
+@functools.lru_cache(maxsize=4096)
+def _fp8_sizes(gated: bool, x: tuple, xt, ldx: int, xs: tuple, xst, w: tuple, wt, ws: tuple, wst):
+    """(T, K, N, E, scale_fmt, row pitch) of a forward call's operands, or None where the checks one by one have something to say.  (These
+    calls can take less time on the GPU than their checks here, which are therefore made once for a set of shapes and types.)"""
+    experts = w[:-2]
+    cols, K = w[-2:]
+    if not (len(x) == 2 and len(w) in (2, 3) and xt in _CODES and wt in _CODES and xst is torch.float32 and x[1] == K and K % 128 == 0 and
+            cols % (256 if gated else 128) == 0 and xs == (x[0], K // 128) and ws == (*experts, cols // 128, K // 128) and
+            wst in (torch.float32, torch.uint8) and 0 not in experts and (x[0] <= 1 or ldx >= K)):
+        return None
+    return (x[0], K, cols // 2 if gated else cols, *(experts or (0,)), SCALE_UE8M0 if wst is torch.uint8 else SCALE_F32,
+            ldx if x[0] > 1 else K)
+
+
+def _fp8_operands(gated: bool, x_q, x_scale, w_q, w_scale, offsets):
+    """Those sizes, and the GPU."""
+    try:
+        dev = x_q.get_device()
+        ldx, inner = x_q.stride()
+        if (dev >= 0 and inner == 1 and x_scale.get_device() == dev and w_q.get_device() == dev and w_scale.get_device() == dev and
+                x_scale.is_contiguous() and w_q.is_contiguous() and w_scale.is_contiguous()):
+            sizes = _fp8_sizes(gated, x_q.shape, x_q.dtype, ldx, x_scale.shape, x_scale.dtype, w_q.shape, w_q.dtype, w_scale.shape,
+                               w_scale.dtype)
+            if sizes is not None and (offsets is None) == (sizes[3] == 0):
+                if offsets is not None:
+                    _packed("offsets", offsets, (sizes[3] + 1,), torch.int32, dev)
+                return sizes, dev
+    except (AttributeError, TypeError, ValueError):
+        pass
+    T, K, dev, ldx = _fp8_rows(x_q, x_scale)
+    Kw, N, E, fmt = _fp8_weights(w_q, w_scale, offsets, gated, dev)
+    if Kw != K:
+        raise ValueError(f"the weights have {Kw} inputs, x_q {K} columns")
+    return (T, K, N, E, fmt, ldx), dev
+
+
 def linear_fp8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor, w_scale: torch.Tensor,
                bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None, act: int = ACT_NONE,
                save_pre: bool = False, offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -903,10 +942,7 @@ def linear_fp8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor, w_sc
     [N/128,K/128] (float32, or uint8 UE8M0 exponents).  With offsets [E+1] (int32, as route returns them) expert e multiplies
     rows offsets[e] .. offsets[e+1]-1 by w_q[e] of [E,N,K]; bias, residual, act and save_pre are for one matrix, and rows of no
     expert are left as they were in `out`, and unset without it.  See moe_linear_fp8."""
-    T, K, dev, ldx = _fp8_rows(x_q, x_scale)
-    Kw, N, E, fmt = _fp8_weights(w_q, w_scale, offsets, False, dev)
-    if Kw != K:
-        raise ValueError(f"w_q has {Kw} inputs, x_q {K} columns")
+    (T, K, N, E, fmt, ldx), dev = _fp8_operands(False, x_q, x_scale, w_q, w_scale, offsets)
     if bias is not None:
         _packed("bias", bias, (N,), torch.bfloat16, dev)
     ldr = 0 if residual is None else _rows("residual", residual, T, N, torch.bfloat16, dev)
@@ -925,10 +961,7 @@ def gated_linear_fp8(x_q: torch.Tensor, x_scale: torch.Tensor, w_gate_up_q: torc
                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """(a, pre): [gate | up] = x w_gate_up^T, a = act(gate) * up [T,I] in bf16, and pre = [gate | up] [T,2I] when save_pre (else
     None).  w_gate_up_q [2I,K], or [E,2I,K] with offsets; operands and offsets as in linear_fp8.  See moe_gated_linear_fp8."""
-    T, K, dev, ldx = _fp8_rows(x_q, x_scale)
-    Kw, I, E, fmt = _fp8_weights(w_gate_up_q, w_scale, offsets, True, dev)
-    if Kw != K:
-        raise ValueError(f"w_gate_up_q has {Kw} inputs, x_q {K} columns")
+    (T, K, I, E, fmt, ldx), dev = _fp8_operands(True, x_q, x_scale, w_gate_up_q, w_scale, offsets)
     ldy = 0 if out is None else _rows("out", out, T, I, torch.bfloat16, dev)
     prob, need = _problem(Fp8Problem, (T, K, I, E, fmt, int(act), ldx, ldy, 0, 0, 0), "moe_gated_linear_fp8_workspace_size", 0)
     ws, n = _scratch(workspace, need, x_q, dev)
