@@ -39,6 +39,22 @@ __device__ __forceinline__ uint2 codes8(const float v[8], float f) {
   return make_uint2(lo, hi);
 }
 
+// The largest of 16 neighbouring lanes, for each of them (rotations by DPP: no trip through LDS)
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xf, 0xf, false)));   // by 8
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xf, 0xf, false)));
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xf, 0xf, false)));
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xf, 0xf, false)));
+}
+// join(v, v of the lane 16 on), then of the lane 32 on, for each lane
+template <typename F>
+__device__ __forceinline__ float across_rows(float v, F&& join) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = join(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return join(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
 // Codes of a 128 x 128 tile.  col: first of this thread's eight columns in the outputs of pitch C
 struct TileOut {
   uint8_t* row_codes;      // null: not wanted
@@ -58,8 +74,7 @@ __device__ __forceinline__ void store_tile(const float (&v)[kRows][8], const Til
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[u][i]));
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 16));
+      top = row_max(top);
       const int b = pow2_over(top);
       if (r < rows) {
         *reinterpret_cast<uint2*>(o.row_codes + (row0 + r) * C + col) = codes8(v[u], pow2(254 - b));
@@ -72,22 +87,26 @@ __device__ __forceinline__ void store_tile(const float (&v)[kRows][8], const Til
     }
   }
   if (!o.col_codes && !o.sums) return;
-  float top[8], sum[8];
+  float top[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    top[i] = 0.f, sum[i] = 0.f;
+    top[i] = 0.f;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) top[i] = fmaxf(top[i], fabsf(v[u][i])), sum[i] += v[u][i];
-#pragma unroll
-    for (int d = 16; d < 64; d <<= 1) {
-      top[i] = fmaxf(top[i], __shfl_xor(top[i], d, 64));
-      sum[i] += __shfl_xor(sum[i], d, 64);
-    }
+    for (int u = 0; u < kRows; ++u) top[i] = fmaxf(top[i], fabsf(v[u][i]));
+    top[i] = across_rows(top[i], [](float a, float b) { return fmaxf(a, b); });
   }
   __syncthreads();                     // (red may still be read from the tile's other half)
-  if ((threadIdx.x & 48) == 0) {
-    Piece<float>::store(red[0][wave], sub * 8, top);
-    if (o.sums) Piece<float>::store(red[1][wave], sub * 8, sum);
+  if ((threadIdx.x & 48) == 0) Piece<float>::store(red[0][wave], sub * 8, top);
+  if (o.sums) {
+    float sum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sum[i] = 0.f;
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) sum[i] += v[u][i];
+      sum[i] = across_rows(sum[i], [](float a, float b) { return a + b; });
+    }
+    if ((threadIdx.x & 48) == 0) Piece<float>::store(red[1][wave], sub * 8, sum);
   }
   __syncthreads();
   if (o.sums && threadIdx.x < 16) {
@@ -134,24 +153,17 @@ __device__ __forceinline__ void store_tile(const float (&v)[kRows][8], const Til
   }
 }
 
-// Rows past the tile's are zeros
-__device__ __forceinline__ void load_tile(const void* p, int64_t ld, int64_t row0, int rows, int col, float (&v)[kRows][8]) {
+// A thread's values as they are stored; rows past the tile's are zeros
+__device__ __forceinline__ void load_tile(const void* p, int64_t ld, int64_t row0, int rows, int col, i32x4 (&raw)[kRows]) {
   const int rr = threadIdx.x >> 4;
-  i32x4 raw[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) raw[u] = Piece<uint16_t>::raw(p, (row0 + min(rr + 32 * u, rows - 1)) * ld + col);
 #pragma unroll
-  for (int u = 0; u < kRows; ++u) {
-    Piece<uint16_t>::widen(raw[u], v[u]);
-    if (rr + 32 * u >= rows) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-    }
-  }
+  for (int u = 0; u < kRows; ++u) raw[u] &= rr + 32 * u < rows ? -1 : 0;
 }
 
 // Workgroup (x, y): column block x of dz, or behind those of x; row tile y
-template <bool ACT, bool GATED>
+template <int ACT, bool GATED>
 __global__ __launch_bounds__(kThreads) void groups_kernel(GroupsArgs a, int dz_blocks) {
   __shared__ float red[2][kWaves][128];
   const int tile = blockIdx.y;
@@ -166,39 +178,64 @@ __global__ __launch_bounds__(kThreads) void groups_kernel(GroupsArgs a, int dz_b
   const int sub = threadIdx.x & 15;
   const int64_t cols = GATED ? 2 * (int64_t)a.N : a.N;
   float v[kRows][8];
+  i32x4 raw[kRows];
   if ((int)blockIdx.x >= dz_blocks) {
     const int col = ((int)blockIdx.x - dz_blocks) * 128 + sub * 8;
-    load_tile(a.x, a.ldx, row0, rows, col, v);
+    load_tile(a.x, a.ldx, row0, rows, col, raw);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) Piece<uint16_t>::widen(raw[u], v[u]);
     store_tile(v, TileOut{nullptr, nullptr, 0, a.xc + (int64_t)tile * 128 * a.K, a.xc_scale + (int64_t)tile * a.K, nullptr}, row0, rows, col, a.K, red);
     return;
   }
   const int col = (int)blockIdx.x * 128 + sub * 8;
   TileOut o{a.zr, a.zr_scale, a.zr_f32, a.zc ? a.zc + tile * 128 * cols : nullptr, a.zc_scale ? a.zc_scale + tile * cols : nullptr,
             a.part ? a.part + tile * cols : nullptr};
-  load_tile(a.dy, a.ldy, row0, rows, col, v);
+  load_tile(a.dy, a.ldy, row0, rows, col, raw);
   if constexpr (GATED) {
-    float z[kRows][8], up[kRows][8];
-    load_tile(a.pre, a.ldp, row0, rows, col, z);
+    // one half after the other, from the operands as they were loaded: both halves' float32 values would take the registers of a workgroup
+    i32x4 gate[kRows], up[kRows];
+    load_tile(a.pre, a.ldp, row0, rows, col, gate);
     load_tile(a.pre, a.ldp, row0, rows, a.N + col, up);
 #pragma unroll
-    for (int u = 0; u < kRows; ++u)
+    for (int u = 0; u < kRows; ++u) {
+      float da[8], ug[8], z[8];
+      Piece<uint16_t>::widen(gate[u], z);
+      Piece<uint16_t>::widen(raw[u], da);
+      Piece<uint16_t>::widen(up[u], ug);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const ActPair p = act_pair<true>(a.act, z[u][i]);
-        const float da = v[u][i];
-        v[u][i] = times_slope(a.act, da * up[u][i], p.slope);
-        z[u][i] = da * p.value;
-      }
+      for (int i = 0; i < 8; ++i) v[u][i] = times_slope(ACT, da[i] * ug[i], act_pair<true>(ACT, z[i]).slope);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     store_tile(v, o, row0, rows, col, (int)cols, red);
-    store_tile(z, o, row0, rows, a.N + col, (int)cols, red);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) asm volatile("" : "+v"(gate[u]), "+v"(raw[u]));
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      float da[8], z[8];
+      Piece<uint16_t>::widen(gate[u], z);
+      Piece<uint16_t>::widen(raw[u], da);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = da[i] * act_pair<true>(ACT, z[i]).value;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    store_tile(v, o, row0, rows, a.N + col, (int)cols, red);
   } else {
-    if constexpr (ACT) {
-      float z[kRows][8];
-      load_tile(a.pre, a.ldp, row0, rows, col, z);
+    if constexpr (ACT != kActNone) {
+      i32x4 pre[kRows];
+      load_tile(a.pre, a.ldp, row0, rows, col, pre);
 #pragma unroll
-      for (int u = 0; u < kRows; ++u)
+      for (int u = 0; u < kRows; ++u) {
+        float z[8];
+        Piece<uint16_t>::widen(pre[u], z);
+        Piece<uint16_t>::widen(raw[u], v[u]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = times_slope(a.act, v[u][i], act_pair<true>(a.act, z[u][i]).slope);
+        for (int i = 0; i < 8; ++i) v[u][i] = times_slope(ACT, v[u][i], act_pair<true>(ACT, z[i]).slope);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) Piece<uint16_t>::widen(raw[u], v[u]);
     }
     store_tile(v, o, row0, rows, col, (int)cols, red);
   }
@@ -353,9 +390,17 @@ hipError_t launch_runs(const Runs& r, const int32_t* offsets, int64_t T, int E, 
 hipError_t launch_groups(const GroupsArgs& a, hipStream_t s) {
   const int dz_blocks = a.zr || a.zc || a.part ? a.N / 128 : 0, x_blocks = a.xc ? a.K / 128 : 0;
   const dim3 grid((unsigned)(dz_blocks + x_blocks), (unsigned)a.max_tiles);
-  if (a.gated) hipLaunchKernelGGL((groups_kernel<false, true>), grid, dim3(kThreads), 0, s, a, dz_blocks);
-  else if (a.pre) hipLaunchKernelGGL((groups_kernel<true, false>), grid, dim3(kThreads), 0, s, a, dz_blocks);
-  else hipLaunchKernelGGL((groups_kernel<false, false>), grid, dim3(kThreads), 0, s, a, dz_blocks);
+  auto launch = [&](auto act, auto gated) {
+    hipLaunchKernelGGL((groups_kernel<decltype(act)::value, decltype(gated)::value>), grid, dim3(kThreads), 0, s, a, dz_blocks);
+  };
+  auto by_act = [&](auto gated) {
+    if (a.act == kActSilu) launch(std::integral_constant<int, kActSilu>{}, gated);
+    else if (a.act == kActGelu) launch(std::integral_constant<int, kActGelu>{}, gated);
+    else launch(std::integral_constant<int, kActRelu>{}, gated);
+  };
+  if (a.gated) by_act(std::true_type{});
+  else if (a.pre) by_act(std::false_type{});
+  else launch(std::integral_constant<int, kActNone>{}, std::false_type{});
   return hipGetLastError();
 }
 
