@@ -144,16 +144,41 @@ __device__ __forceinline__ void formed(f32x4 (&a)[4][2]) {
   asm volatile("" : "+v"(a[0][0]), "+v"(a[0][1]), "+v"(a[1][0]), "+v"(a[1][1]), "+v"(a[2][0]), "+v"(a[2][1]), "+v"(a[3][0]), "+v"(a[3][1]));
 }
 
-template <int NH>
+template <int NH, bool FOLD>
 struct Ring {
   static constexpr int SLICES = NH == 2 ? 2 : 3;                  // in LDS, and how far the DMAs are ahead
   static constexpr int STAGE = (NH + 2) * REGION;                 // R0 [R1] C0 C1
   static constexpr int SCALES = (128 * NH + 256) * 4;             // a dword per row of r and, for the MFMA, of c
   static constexpr int TABLE = SLICES * STAGE + 3 * SCALES;       // FOLD: c's block scales of NT tiles, [2 halves][slices]
   static constexpr int BYTES = 160 * 1024;
-  static constexpr int TABLES = BYTES - TABLE;
+  // 1 KB a wave through which results turn into rows (Patch); 128-row tiles leave no room for it beside the longest tables
+  static constexpr bool PATCHED = NH == 2 || !FOLD;
+  static constexpr int PATCH = BYTES - (PATCHED ? 8 * 1024 : 0);
+  static constexpr int TABLES = PATCH - TABLE;
 };
 
+// 16 x 32 bf16 results of a wave, turned in LDS: lane l has row l & 15, columns 4 (l >> 4) and 16 further on, and gets row l >> 2, eight columns from
+// 8 (l & 3) on.  Four neighbouring lanes then store 64 bytes of a row, where the results as they are formed would go out in
+// pieces of 8 or, exchanged between lane groups, 16.  A row's four 16-byte pieces are XOR-permuted by row / 4 (no bank conflicts).  LDS executes
+// a wave's accesses in order, so that nothing waits but the store.
+struct Patch {
+  char *to, *to16;
+  const char* from;
+  __device__ __forceinline__ Patch(char* patch, int lane) {
+    const uint32_t at = (lane & 15) * 64 + ((((lane >> 5) ^ (lane >> 2)) & 3) << 4) + (lane >> 4 & 1) * 8;
+    to = patch + at;
+    to16 = patch + (at ^ 32);
+    from = patch + (lane >> 2) * 64 + (((lane ^ (lane >> 4)) & 3) << 4);
+  }
+  __device__ __forceinline__ i32x4 turn(const f32x4 (&z)[2]) const {
+    *reinterpret_cast<i32x2v*>(to) = i32x2v{(int)pack_bf16x2(z[0][0], z[0][1]), (int)pack_bf16x2(z[0][2], z[0][3])};
+    *reinterpret_cast<i32x2v*>(to16) = i32x2v{(int)pack_bf16x2(z[1][0], z[1][1]), (int)pack_bf16x2(z[1][2], z[1][3])};
+    __builtin_amdgcn_wave_barrier();
+    const i32x4 v = *reinterpret_cast<const i32x4*>(from);
+    __builtin_amdgcn_wave_barrier();
+    return v;
+  }
+};
 // What the table kernel wrote: read through the scalar cache (a vector load would have the compiler wait for every DMA in flight)
 __device__ __forceinline__ int table_entry(const void* table, int64_t i) {
   typedef const __attribute__((address_space(4))) int32_t* Table;
@@ -250,7 +275,7 @@ __device__ __forceinline__ int place_in_round() { return (blockIdx.x & 7) * (gri
 // This workgroup's tiles of job J
 template <typename TILES, int J, bool RK, bool CK, int EPI, int NH, bool FOLD>
 __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds, const Share& share) {
-  using Rg = Ring<NH>;
+  using Rg = Ring<NH, FOLD>;
   constexpr int AHEAD = Rg::SLICES;
   constexpr int DMAS = 5 + 2 * NH;             // of a wave and slice
   const DenseGemm& g = p.j.g;
@@ -531,21 +556,42 @@ __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds, const Shar
     } else if (!q.E) {
       job.g.M = q.j.g.M;
     }
+    if (Rg::PATCHED && EPI == kGrad && !job.part) {
+      const int who = lane_again();
+      const Patch patch(lds + Rg::PATCH + wave * 1024, who);
 #pragma unroll
-    for (int a = 0; a < NH; ++a)
+      for (int a = 0; a < NH; ++a)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 2; ++b) {
+          const int col = n0 + b * 128 + wn * 32;
+          if (col >= job.g.e.N) continue;
+          const int64_t m = x.m0 + a * 128 + wm * 64 + (who >> 2);
+          uint16_t* out = static_cast<uint16_t*>(job.g.e.out) + col + 8 * (who & 3);
+          i32x4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) eight_columns(acc[a][b][i][0], acc[a][b][i][1]);
-        if (EPI == kGated && b == 0) continue;
-        __builtin_amdgcn_sched_barrier(0);
-        const int who = lane_again();
-        const int64_t m = x.m0 + a * 128 + wm * 64 + (who & 15);
-        const int col = n0 + wn * 32 + 8 * (who >> 4);
-        if constexpr (EPI == kGated) store_rows<uint16_t, EPI>(job, x.split, m, col, acc[a][0], acc[a][1]);
-        else store_rows<uint16_t, EPI>(job, x.split, m, col + b * 128, acc[a][b], acc[a][b]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+          for (int i = 0; i < 4; ++i) v[i] = patch.turn(acc[a][b][i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (m + 16 * i < job.g.M) *reinterpret_cast<i32x4*>(out + (m + 16 * i) * job.g.e.ldo) = v[i];
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    } else {
+#pragma unroll
+      for (int a = 0; a < NH; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) eight_columns(acc[a][b][i][0], acc[a][b][i][1]);
+          if (EPI == kGated && b == 0) continue;
+          __builtin_amdgcn_sched_barrier(0);
+          const int who = lane_again();
+          const int64_t m = x.m0 + a * 128 + wm * 64 + (who & 15);
+          const int col = n0 + wn * 32 + 8 * (who >> 4);
+          if constexpr (EPI == kGated) store_rows<uint16_t, EPI>(job, x.split, m, col, acc[a][0], acc[a][1]);
+          else store_rows<uint16_t, EPI>(job, x.split, m, col + b * 128, acc[a][b], acc[a][b]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    }
   }
   wait_vmcnt<0>();                             // no DMA outlives the workgroup's LDS
 }
@@ -553,7 +599,7 @@ __device__ __forceinline__ void run_tiles(const Fp8Job& p, char* lds, const Shar
 // One workgroup a CU
 template <int EPI, int NH>
 __global__ __launch_bounds__(512, 1) void fp8_forward_kernel(Fp8Job p) {
-  __shared__ __attribute__((aligned(1024))) char lds[Ring<NH>::BYTES];
+  __shared__ __attribute__((aligned(1024))) char lds[Ring<NH, true>::BYTES];
   run_tiles<RowTiles, 0, false, false, EPI, NH, true>(p, lds, Share(place_in_round(), gridDim.x, 0, 0, false));
 }
 
@@ -565,8 +611,8 @@ struct Fill {
 };
 template <int NX, int NW, bool FOLD>
 __global__ __launch_bounds__(512, 1) void fp8_gradients_kernel(Fp8Job dx, Fp8Job dw, Fill fill) {
-  __shared__ __attribute__((aligned(1024))) char lds[Ring<2>::BYTES];
-  static_assert(Ring<1>::BYTES == Ring<2>::BYTES, "one buffer for both");
+  __shared__ __attribute__((aligned(1024))) char lds[Ring<2, true>::BYTES];
+  static_assert(Ring<1, true>::BYTES == Ring<2, true>::BYTES, "one buffer for both");
   const int G = gridDim.x, q = place_in_round();
   const int heavy = (fill.dw ? RowTiles::count(argument<0>()) : DwTiles::count(argument<1>())) % G;
   const bool others = fill.others_first && heavy;
