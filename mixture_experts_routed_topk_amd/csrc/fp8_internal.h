@@ -18,7 +18,6 @@ struct RowTile {
   int32_t pad[3];
 };
 struct Runs {
-  int32_t* start;       // [E + 1]
   int32_t* group;       // [E + 1]: 128-row tiles before the expert's
   int32_t* order;       // [E]: the experts with rows, then those without
   int32_t* count;       // [3]: tiles, 128-row tiles, experts with rows

@@ -307,19 +307,28 @@ __global__ __launch_bounds__(kThreads) void blocks_kernel(const void* __restrict
 // ---------------------------------------------------------------------------- runs of rows
 constexpr int kMaxE = 1024;
 
-// Inclusive scan over v[0 .. kMaxE) by one workgroup of kMaxE threads
-template <typename F>
-__device__ __forceinline__ int32_t scan(int32_t v, int32_t* lds, F&& join) {
+// Inclusive scans over N values of each of a workgroup's kMaxE threads, side by side
+template <int N, typename F>
+__device__ __forceinline__ void scan(int32_t (&v)[N], int32_t (&lds)[N][16], F&& join) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+#pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int32_t o = __shfl_up(v, d, 64);
-    if (lane >= d) v = join(v, o);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int32_t o = __shfl_up(v[n], d, 64);
+      if (lane >= d) v[n] = join(v[n], o);
+    }
   }
-  __syncthreads();                    // (lds may still be read from the last scan)
-  if (lane == 63) lds[wave] = v;
+  if (lane == 63) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) lds[n][wave] = v[n];
+  }
   __syncthreads();
-  for (int w = 0; w < wave; ++w) v = join(v, lds[w]);
-  return v;
+#pragma unroll
+  for (int w = 0; w < 15; ++w) {                // (no value is negative)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = join(v[n], w < wave ? lds[n][w] : 0);
+  }
 }
 
 __device__ void list_tiles(RowTile* out, const int32_t* start, const int32_t* first, int E, int n) {
@@ -334,27 +343,23 @@ __device__ void list_tiles(RowTile* out, const int32_t* start, const int32_t* fi
 }
 
 __global__ __launch_bounds__(kMaxE) void runs_kernel(Runs r, const int32_t* __restrict__ offsets, int T, int E) {
-  __shared__ int32_t alive, sums[16], start[kMaxE + 1], first[kMaxE + 1], group[kMaxE + 1];
+  __shared__ int32_t alive, ends[1][16], sums[3][16], start[kMaxE + 1], first[kMaxE + 1], group[kMaxE + 1];
   const int e = threadIdx.x;
-  auto larger = [](int32_t a, int32_t b) { return a > b ? a : b; };
-  auto plus = [](int32_t a, int32_t b) { return a + b; };
-  const int32_t end = scan(e < E ? min(max(offsets[e + 1], 0), T) : 0, sums, larger);
   const int32_t begin0 = min(max(offsets[0], 0), T);
-  if (e < E) start[e + 1] = max(end, begin0);
-  if (e == 0) start[0] = begin0;
+  int32_t end[1] = {e < E ? min(max(offsets[e + 1], begin0), T) : 0};
+  scan(end, ends, [](int32_t a, int32_t b) { return a > b ? a : b; });
+  if (e < E) start[e + 1] = end[0];
+  if (e == 0) start[0] = begin0, first[0] = 0, group[0] = 0;
   __syncthreads();
-  const int cnt = e < E ? start[e + 1] - start[e] : 0;
-  const int32_t n = scan((cnt + r.height - 1) / r.height, sums, plus);
-  const int32_t n128 = scan((cnt + 127) / 128, sums, plus);
-  if (e < E) first[e + 1] = n, group[e + 1] = n128;
-  if (e == 0) first[0] = 0, group[0] = 0;
+  const int cnt = e < E ? end[0] - start[e] : 0;
+  // row tiles, 128-row tiles and experts with rows, up to this one (threads past E have none)
+  int32_t sum[3] = {(cnt + r.height - 1) / r.height, (cnt + 127) / 128, cnt > 0 ? 1 : 0};
+  scan(sum, sums, [](int32_t a, int32_t b) { return a + b; });
+  if (e < E) first[e + 1] = sum[0], group[e + 1] = sum[1];
+  if (e == kMaxE - 1) r.count[0] = sum[0], r.count[1] = sum[1], r.count[2] = alive = sum[2];
   __syncthreads();
-  const int32_t live = scan(cnt > 0 ? 1 : 0, sums, plus);       // (threads past E have none)
-  if (e == kMaxE - 1) r.count[2] = alive = live;
-  __syncthreads();
-  if (e < E) r.order[cnt > 0 ? live - 1 : alive + e - live] = e;
-  for (int i = e; i <= E; i += kMaxE) r.start[i] = start[i], r.group[i] = group[i];
-  if (e == 0) r.count[0] = first[E], r.count[1] = group[E];
+  if (e < E) r.order[cnt > 0 ? sum[2] - 1 : alive + e - sum[2]] = e;
+  for (int i = e; i <= E; i += kMaxE) r.group[i] = group[i];
   list_tiles(r.tiles, start, first, E, first[E]);
   if (r.height != 128) list_tiles(r.groups, start, group, E, group[E]);
 }
@@ -365,18 +370,17 @@ size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 size_t runs_bytes(int64_t T, int E, int height) {
   if (E == 0) return 0;
-  return up256(4 * (3 * (size_t)(E + 1) + 2)) + up256(sizeof(RowTile) * (size_t)max_row_tiles(T, E, height)) +
+  return up256(4 * (2 * (size_t)E + 4)) + up256(sizeof(RowTile) * (size_t)max_row_tiles(T, E, height)) +
          (height == 128 ? 0 : up256(sizeof(RowTile) * (size_t)max_row_tiles(T, E, 128)));
 }
 
 Runs runs_at(void* ws, int64_t T, int E, int height) {
   Runs r{};
   r.height = height;
-  r.start = static_cast<int32_t*>(ws);
-  r.group = r.start + E + 1;
+  r.group = static_cast<int32_t*>(ws);
   r.order = r.group + E + 1;
   r.count = r.order + E;
-  char* p = static_cast<char*>(ws) + up256(4 * (3 * (size_t)(E + 1) + 2));
+  char* p = static_cast<char*>(ws) + up256(4 * (2 * (size_t)E + 4));
   r.tiles = reinterpret_cast<RowTile*>(p);
   r.groups = height == 128 ? r.tiles : reinterpret_cast<RowTile*>(p + up256(sizeof(RowTile) * (size_t)max_row_tiles(T, E, height)));
   return r;
