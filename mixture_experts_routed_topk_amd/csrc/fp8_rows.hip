@@ -1,87 +1,98 @@
 // e4m3 products with block scales on few rows (decode steps), forward (gfx950).
 //
-// One pass over the weights, as in dense_rows.hip: a workgroup takes 16 weight rows (gated: 8 gate rows and the matching
-// 8 up rows), its waves share the contraction in contiguous runs of 128-k slices, and codes go from memory
-// straight into the MFMA's registers, 32 bytes a lane.  A slice's result is folded in times the row's and the
-// block's scale.  The waves' float32 sums meet in LDS and are added in wave order.
-#include "dense_device.h"
-#include "fp8_internal.h"
+// One pass over the weights: a workgroup takes 16 weight rows (gated: 8 gate rows and the matching 8 up rows), its waves
+// every NW-th slice of 128 k.  A wave brings a slice's codes into LDS of its own by DMA, eight whole 128-byte lines an
+// instruction, several slices ahead and without a barrier.  (Straight into the MFMA's registers a lane would read 16 bytes
+// of a row and its neighbours other rows: those loads kept a CU's address unit busy for 120 cycles a slice.)  A slice's result
+// is folded in times the row's and the block's scale; the waves' float32 sums meet in LDS and are added in wave order.
+#include "dense_tile.h"
+#include "fp8_tile.h"
 
 namespace moe {
 namespace {
 
-// U slices from kt on, all their loads before the first product; slices from `end` on are not counted (they repeat the
-// last one, times zero)
-template <int MT, int U, bool UE8>
-__device__ __forceinline__ void slices(const uint8_t* const (&rp)[MT], const uint8_t* cp, const float* const (&sp)[MT],
-                                       const void* bp, int kt, int end, f32x4 (&acc)[MT]) {
-  i32x4 c[U][2], r[U][MT][2];
-  float sr[U][MT], sb[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int at = min(kt + u, end - 1);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) c[u][h] = *reinterpret_cast<const i32x4*>(cp + (int64_t)at * 128 + h * 16);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) r[u][i][h] = *reinterpret_cast<const i32x4*>(rp[i] + (int64_t)at * 128 + h * 16);
-      sr[u][i] = sp[i][at];
-    }
-    if constexpr (UE8) {
-      const uint32_t b = static_cast<const uint8_t*>(bp)[at];
-      sb[u] = __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
-    } else {
-      sb[u] = static_cast<const float*>(bp)[at];
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const i32x8 cv = __builtin_shufflevector(c[u][0], c[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const i32x8 rv = __builtin_shufflevector(r[u][i][0], r[u][i][1], 0, 1, 2, 3, 4, 5, 6, 7);
-      const f32x4 p = mfma_16x16x128_e4m3(cv, rv, f32x4{});
-      const float s = sr[u][i] * sb[u];
-      if (kt + u < end) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(p[q], s, acc[i][q]);
-      }
-    }
-  }
-}
+constexpr int kLong = 4096;           // K from which on eight waves share a contraction (of up to 32 rows)
+// Rows times slices
+constexpr int kMaxScales = 4096;
+constexpr int max_scales(int RD, int NW) { return RD == 8 || NW == 8 ? kMaxScales : RD * 8 * kLong / 128; }
 
-template <int MT, bool GATED, int NW, bool UE8>
+// RD: groups of eight rows of r, 1, 2, 4 or 8
+template <int RD, bool GATED, int NW, bool UE8>
 __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Gemm p) {
-  constexpr int U = MT == 2 && NW == 16 ? 2 : 4;     // (what fits in the registers of so many waves)
+  constexpr int MT = (RD + 1) / 2;                 // fragments of 16 rows
+  constexpr int U = MT == 4 ? 3 : MT == 2 ? 2 : 4; // slices of a wave in flight (160 KB of LDS hold one workgroup, or two of four waves and up to 32 rows)
+  constexpr int SLICE = (1 + MT) * 2048;
+  constexpr int DMAS = 2 + RD;
   constexpr int COLS = GATED ? 8 : 16;
+  __shared__ __attribute__((aligned(1024))) char ring[NW * U * SLICE];
+  __shared__ float sr[max_scales(RD, NW)], sb[2][kMaxSlices];
   __shared__ f32x4 red[MT][NW][64];
   const DenseGemm& g = p.g;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int grp = lane >> 4, i16 = lane & 15;
   const int n0 = blockIdx.x * COLS, N = g.e.N;
   const int KT = (int)(g.K / 128);
-  const int per = (KT + NW - 1) / NW;
-  const int first = wave * per, end = min(KT, first + per);
+  const int mine = (KT - wave + NW - 1) / NW;      // slices wave, wave + NW, ..
 
-  const int64_t crow = n0 + i16 % COLS + (GATED ? (int64_t)(i16 / COLS) * N : 0);
-  const uint8_t* cp = static_cast<const uint8_t*>(g.c) + crow * g.ldc + grp * 32;
-  // the block of this lane's result columns 4 grp .. 4 grp + 3 (gated: lane groups 2 and 3 hold the up rows)
-  const int64_t block = (n0 >> 7) + (GATED ? (int64_t)(grp >> 1) * (N >> 7) : 0);
-  const void* bp = static_cast<const char*>(p.cs.p) + block * p.cs.row * (UE8 ? 1 : 4);
-  const uint8_t* rp[MT];
-  const float* sp[MT];
-  f32x4 acc[MT];
+  // lane's piece of rows 0 .. 7 and 8 .. 15 of c (gated: of gate and up), and of r's; rows past the matrix repeat its last one and are not stored
+  const char* src[DMAS];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {       // rows past the matrix repeat its last one and are not stored
-    const int64_t m = min((int64_t)(i * 16 + i16), g.M - 1);
-    rp[i] = static_cast<const uint8_t*>(g.r) + m * g.ldr + grp * 32;
-    sp[i] = static_cast<const float*>(p.rs.p) + m * p.rs.row;
-    acc[i] = f32x4{};
+  for (int d = 0; d < DMAS; ++d) {
+    const int ins = d & 1;
+    const int64_t row = ins * 8 + (lane >> 3);
+    if (d < 2) src[d] = static_cast<const char*>(g.c) + (GATED ? n0 + (lane >> 3) + (int64_t)ins * N : n0 + row) * g.ldc;
+    else src[d] = static_cast<const char*>(g.r) + min((int64_t)((d - 2) / 2 * 16) + row, g.M - 1) * g.ldr;
+    src[d] += Chunk8<false>::k(ins, lane) + wave * 128;
   }
-  for (int kt = first; kt < end; kt += U) {
-    if (end - kt > U / 2) slices<MT, U, UE8>(rp, cp, sp, bp, kt, end, acc);
-    else slices<MT, U / 2, UE8>(rp, cp, sp, bp, kt, end, acc);
+  char* own = ring + wave * U * SLICE;
+  auto issue = [&](int u) __attribute__((always_inline)) {
+    const uint32_t to = lds_addr(own) + (uint32_t)(u % U * SLICE);
+#pragma unroll
+    for (int d = 0; d < DMAS; ++d) dma_lds_x4_at(src[d] + (int64_t)u * NW * 128, to + d * 1024);
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (u < mine) issue(u);
+
+  // all scales (x's are packed)
+  for (int i = threadIdx.x; i < (int)g.M * KT; i += NW * 64) sr[i] = static_cast<const float*>(p.rs.p)[i];
+  for (int i = threadIdx.x; i < (GATED ? 2 : 1) * KT; i += NW * 64) {
+    const int h = i >= KT, kt = i - h * KT;
+    const int64_t at = ((n0 >> 7) + h * (int64_t)(N >> 7)) * p.cs.row + kt;
+    sb[h][kt] = UE8 ? ue8m0_value(static_cast<const uint8_t*>(p.cs.p)[at]) : static_cast<const float*>(p.cs.p)[at];
+  }
+  __syncthreads();
+
+  const Frag8<false> frag(lane);
+  f32x4 acc[MT];
+  const float* my_sr[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    acc[i] = f32x4{};
+    my_sr[i] = sr + min((int64_t)(i * 16 + i16), g.M - 1) * KT;
+  }
+  const float* my_sb = sb[GATED ? grp >> 1 : 0];   // (result columns 4 grp .. 4 grp + 3; gated: lane groups 2 and 3 hold the up rows)
+  for (int u = 0; u < mine; ++u) {
+    const int behind = mine - 1 - u;               // slices in flight behind this one, at most U - 1
+    if (behind >= U - 1) wait_vmcnt<(U - 1) * DMAS>();
+    else if (U > 3 && behind == 2) wait_vmcnt<2 * DMAS>();
+    else if (U > 2 && behind == 1) wait_vmcnt<DMAS>();
+    else wait_vmcnt<0>();
+    const char* at = own + u % U * SLICE;
+    const i32x8 c = frag.load(at, 0);
+    const int kt = wave + u * NW;
+    const float b = my_sb[kt];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const f32x4 z = mfma_16x16x128_e4m3(c, frag.load(at, (i + 1) * 16), f32x4{});
+      const float s = my_sr[i][kt] * b;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(z[q], s, acc[i][q]);
+    }
+    if (u + U < mine) {
+      wait_lds();                                  // the place has been read
+      issue(u + U);
+    }
   }
 
 #pragma unroll
@@ -101,26 +112,33 @@ __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Gemm p) {
   }
 }
 
-template <int MT, int NW, bool UE8>
+template <int RD, int NW, bool UE8>
 void launch_rows(const Fp8Gemm& g, hipStream_t s) {
   const dim3 grid((unsigned)(g.g.gated ? g.g.e.N / 8 : g.g.e.N / 16));
-  if (g.g.gated) hipLaunchKernelGGL((fp8_rows_kernel<MT, true, NW, UE8>), grid, dim3(NW * 64), 0, s, g);
-  else hipLaunchKernelGGL((fp8_rows_kernel<MT, false, NW, UE8>), grid, dim3(NW * 64), 0, s, g);
+  if (g.g.gated) hipLaunchKernelGGL((fp8_rows_kernel<RD, true, NW, UE8>), grid, dim3(NW * 64), 0, s, g);
+  else hipLaunchKernelGGL((fp8_rows_kernel<RD, false, NW, UE8>), grid, dim3(NW * 64), 0, s, g);
 }
-template <int MT, bool UE8>
+template <int RD, bool UE8>
 void launch_waves(const Fp8Gemm& g, hipStream_t s) {
-  if (g.g.K > 4096) launch_rows<MT, 16, UE8>(g, s);
-  else launch_rows<MT, 8, UE8>(g, s);
+  if constexpr (RD == 8) launch_rows<RD, 4, UE8>(g, s);
+  else if (g.g.K > kLong) launch_rows<RD, 8, UE8>(g, s);
+  else launch_rows<RD, 4, UE8>(g, s);
 }
 template <bool UE8>
 void launch_heights(const Fp8Gemm& g, hipStream_t s) {
-  if (g.g.M <= 16) launch_waves<1, UE8>(g, s);
-  else launch_waves<2, UE8>(g, s);
+  // (one row in 7168 -> 2 x 2048: 5.3 us, 8 rows 5.6, 16 6.7, 32 8.2, 64 14.6)
+  if (g.g.M <= 8) launch_waves<1, UE8>(g, s);
+  else if (g.g.M <= 16) launch_waves<2, UE8>(g, s);
+  else if (g.g.M <= 32) launch_waves<4, UE8>(g, s);
+  else launch_waves<8, UE8>(g, s);
 }
 
 }  // namespace
 
-bool fp8_rows_take(int64_t M, int64_t K) { return M <= 32 && M * K <= 131072; }
+// What LDS holds the scales of.  us a call, rows against tiles (fp8_tile.h), 32 rows: 2048 -> 8192 6.0 / 14.1, 7168 -> 2048 6.4 / 16.6, 512 -> 512
+// 3.9 / 9.0; 64 rows: 12.2 / 18.7, 11.9 / 19.9, 4.7 / 9.3; gated 2048 -> 2 x 1408 6.6 / 17.0, 2 x 8192 22.8 / 23.2, 1024 -> 2 x 7168 15.2 / 13.2 (the only one
+// of 18 shapes where tiles win).
+bool fp8_rows_take(int64_t M, int64_t K) { return M <= 64 && M * (K / 128) <= kMaxScales; }
 
 hipError_t launch_fp8_rows(const Fp8Gemm& g, hipStream_t s) {
   if (g.cs.bytes) launch_heights<true>(g, s);
