@@ -20,13 +20,16 @@ constexpr int max_scales(int RD, int NW) { return RD == 8 || NW == 8 ? kMaxScale
 template <int RD, bool GATED, int NW, bool UE8>
 __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Gemm p) {
   constexpr int MT = (RD + 1) / 2;                 // fragments of 16 rows
-  constexpr int U = MT == 4 ? 3 : MT == 2 ? 2 : 4; // slices of a wave in flight (160 KB of LDS hold one workgroup, or two of four waves and up to 32 rows)
-  constexpr int SLICE = (1 + MT) * 2048;
+  // Slices of a wave in flight: what lets the 160 KB of a CU hold three workgroups of four waves and up to 32 rows (2 x 5632 columns are
+  // 704 workgroups, which 512 places would take in two rounds: 16 rows of 2048 7.0 us, 5.4 so), or one of the others
+  constexpr int U = MT == 4 ? 3 : MT == 2 ? 2 : RD == 2 && NW == 4 ? 3 : 4;
+  constexpr int SLICE = (2 + RD) * 1024;
   constexpr int DMAS = 2 + RD;
   constexpr int COLS = GATED ? 8 : 16;
   __shared__ __attribute__((aligned(1024))) char ring[NW * U * SLICE];
-  __shared__ float sr[max_scales(RD, NW)], sb[2][kMaxSlices];
-  __shared__ f32x4 red[MT][NW][64];
+  __shared__ float sr[max_scales(RD, NW)], sb[2][RD == 8 || NW == 8 ? kMaxSlices : kLong / 128];
+  static_assert(U * SLICE >= MT * 1024, "the sums take the ring's place");
+  f32x4 (*red)[NW][64] = reinterpret_cast<f32x4 (*)[NW][64]>(ring);
   const DenseGemm& g = p.g;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int grp = lane >> 4, i16 = lane & 15;
@@ -63,7 +66,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Gemm p) {
   }
   __syncthreads();
 
-  const Frag8<false> frag(lane);
+  const Frag8<false> frag(lane), r_frag(RD == 1 ? lane & ~8 : lane);     // (eight rows: twice)
   f32x4 acc[MT];
   const float* my_sr[MT];
 #pragma unroll
@@ -84,7 +87,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Gemm p) {
     const float b = my_sb[kt];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const f32x4 z = mfma_16x16x128_e4m3(c, frag.load(at, (i + 1) * 16), f32x4{});
+      const f32x4 z = mfma_16x16x128_e4m3(c, r_frag.load(at, (i + 1) * 16), f32x4{});
       const float s = my_sr[i][kt] * b;
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(z[q], s, acc[i][q]);
@@ -95,6 +98,7 @@ __global__ __launch_bounds__(NW * 64) void fp8_rows_kernel(Fp8Gemm p) {
     }
   }
 
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < MT; ++i) red[i][wave][lane] = acc[i];
   __syncthreads();
