@@ -1,0 +1,120 @@
+"""The e4m3 products where the choice of a kernel, a tile height or a split changes with the sizes: few rows and their scales in LDS, both
+gradients of one launch with every pair of heights and with splits, runs in tiles of 256 rows."""
+
+import pytest
+import torch
+
+import fp8_ref as ref
+import mixture_experts_routed_topk_amd as m
+from test_gpu_fp8 import ACT, BF16, by_expert, rnd, rows, runs, weights
+
+pytestmark = pytest.mark.gpu
+
+
+# rows to 8, 16, 32 and 64 to a kernel; four waves to 4096 inputs, eight beyond; rows x slices to 4096
+FEW = [(8, 128, 128), (9, 512, 256), (16, 4096, 128), (16, 4224, 128), (31, 4096, 256), (33, 4096, 128), (47, 1152, 384), (64, 8192, 128),
+       (64, 8320, 128), (65, 256, 128), (32, 16384, 128), (32, 16512, 128), (8, 65536, 128), (9, 65536, 128)]
+
+
+@pytest.mark.parametrize("ue8m0", [False, True], ids=["f32", "ue8m0"])
+@pytest.mark.parametrize("T,K,N", FEW)
+def test_few_rows(T, K, N, ue8m0):
+    q, s = rows(60, T, K)
+    x = ref.wide_rows(q, s)
+    wq, ws = weights(61, (N, K), ue8m0)
+    res = rnd(62, (T, N))
+    y, _ = m.linear_fp8(q, s, wq, ws, residual=res)
+    ref.check(y, *ref.linear(x, ref.wide(wq, ws), None, res, "none")[0], "y")
+    gq, gs = weights(63, (2 * N, K), ue8m0)
+    a, pre = m.gated_linear_fp8(q, s, gq, gs, save_pre=True)
+    want, wpre = ref.gated(x, ref.wide(gq, gs), "silu")
+    ref.check(a, *want, "a")
+    ref.check(pre, *wpre, "pre")
+
+
+def test_rows_that_are_not_there_hold_nothing():
+    """What calls with NaN in every row left on the chip enters no row of a later call with fewer rows."""
+    K, N = 2048, 512
+    wq, ws = weights(64, (N, K), False)
+    gq, gs = weights(65, (2 * N, K), False)
+    bad = torch.full((64, K), 0x7f, dtype=torch.uint8, device="cuda")
+    nan = torch.full((64, K // 128), float("nan"), device="cuda")
+    for T in (1, 3, 9, 17, 33):
+        q, s = rows(66 + T, T, K)
+        for n in (8, 16, 32, 64):
+            assert m.linear_fp8(bad[:n], nan[:n], wq, ws)[0].isnan().all()
+        y, _ = m.linear_fp8(q, s, wq, ws)
+        a, _ = m.gated_linear_fp8(q, s, gq, gs)
+        x = ref.wide_rows(q, s)
+        ref.check(y, *ref.linear(x, ref.wide(wq, ws), None, None, "none")[0], f"{T} rows y")
+        ref.check(a, *ref.gated(x, ref.wide(gq, gs), "silu")[0], f"{T} rows a")
+
+
+# contractions in splits, tiles of 128 and of 256 rows with a ragged end
+TILED = [(100, 7168, 256), (257, 4096, 512), (700, 7168, 256), (2731, 1024, 2816), (4099, 512, 2048)]
+
+
+@pytest.mark.parametrize("T,K,N", TILED)
+def test_forward_splits_and_heights(T, K, N):
+    q, s = rows(70, T, K)
+    x = ref.wide_rows(q, s)
+    wq, ws = weights(71, (N, K), False)
+    w = ref.wide(wq, ws)
+    bias = rnd(72, (N,))
+    ref.check(m.linear_fp8(q, s, wq, ws)[0], *ref.linear(x, w, None, None, "none")[0], "y")
+    ref.check(m.linear_fp8(q, s, wq, ws, bias=bias, act=ACT["gelu"])[0], *ref.linear(x, w, bias, None, "gelu")[0], "gelu y")
+    a, pre = m.gated_linear_fp8(q, s, wq, ws, save_pre=True)
+    want, wpre = ref.gated(x, w, "silu")
+    ref.check(a, *want, "a")
+    ref.check(pre, *wpre, "pre")
+
+
+# dx and dw: both of 256 rows; 128 and 256; 256 and 128; 128 and 128; splits of one, the other and both
+PAIRED = [(2000, 4096, 2048), (300, 5120, 1536), (4099, 1024, 1408), (1000, 2048, 1024), (136, 1024, 5632), (2983, 1024, 1024), (16384, 512, 512),
+          (811, 512, 2048), (60, 512, 4096)]
+
+
+@pytest.mark.parametrize("ue8m0", [False, True], ids=["f32", "ue8m0"])
+@pytest.mark.parametrize("T,K,N", PAIRED)
+def test_gradients_share_a_launch(T, K, N, ue8m0):
+    wq, ws = weights(73, (N, K), ue8m0)
+    x, dy = rnd(74, (T, K)), rnd(75, (T, N), BF16, 1e-3)
+    got = m.linear_fp8_backward(dy, x, wq, ws, need_bias=True)
+    want = ref.backward(*ref.dz_linear(dy, None, "none"), x, ref.wide(wq, ws), bias=True)
+    for g, (r, b), what in zip(got, want, ("dx", "dw", "db")):
+        ref.check(g, r, b, what)
+
+
+def test_runs_in_tiles_of_256_rows():
+    T, K, N, E = 9000, 128, 1280, 4
+    q, s = rows(76, T, K)
+    off = runs(77, T, E, 8900)
+    wq, ws = weights(78, (E, N, K), False)
+    gq, gs = weights(79, (E, 2 * N, K), True)
+    y = torch.full((T, N), 5.0, dtype=BF16, device="cuda")
+    a = torch.full((T, N), 6.0, dtype=BF16, device="cuda")
+    m.linear_fp8(q, s, wq, ws, offsets=off, out=y)
+    m.gated_linear_fp8(q, s, gq, gs, offsets=off, out=a)
+    last = int(off[-1])
+    assert (y[last:] == 5.0).all() and (a[last:] == 6.0).all()
+    for e, lo, hi in by_expert(off):
+        x = ref.wide_rows(q[lo:hi], s[lo:hi])
+        ref.check(y[lo:hi], *ref.linear(x, ref.wide(wq[e], ws[e]), None, None, "none")[0], f"expert {e}")
+        ref.check(a[lo:hi], *ref.gated(x, ref.wide(gq[e], gs[e]), "silu")[0], f"expert {e} a")
+
+
+@pytest.mark.parametrize("T,K,N,E", [(40, 4096, 128, 3), (64, 128, 256, 1024), (3000, 256, 128, 2)])
+def test_one_expert_has_all_rows(T, K, N, E):
+    """All rows in the last run, the others empty: also gradients, zeros for the experts without rows."""
+    q, s = rows(80, T, K)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = T
+    wq, ws = weights(81, (E, N, K), False)
+    y, _ = m.linear_fp8(q, s, wq, ws, offsets=off)
+    ref.check(y, *ref.linear(ref.wide_rows(q, s), ref.wide(wq[-1], ws[-1]), None, None, "none")[0], "y")
+    x, dy = rnd(82, (T, K)), rnd(83, (T, N), BF16, 1e-3)
+    dx, dw, _ = m.linear_fp8_backward(dy, x, wq, ws, offsets=off)
+    want = ref.backward(*ref.dz_linear(dy, None, "none"), x, ref.wide(wq[-1], ws[-1]))
+    ref.check(dx, *want[0], "dx")
+    ref.check(dw[-1], *want[1], "dw")
+    assert not dw[:-1].any()
