@@ -3,6 +3,9 @@
 // dx = dz w reads the weights along their rows, as they are stored, and applies their block scales; dw = dz^T x reads
 // both operands along their rows.  dz's and x's scales are powers of two, so dw's MFMAs apply all scales
 // themselves, and dx's too with UE8M0 weights.
+//
+// One launch: the product with the shorter tiles fills the CUs that the other's last round leaves (Fill, Share).  2731 rows, 2048 <- 5632:
+// 91 us, against 62 and 43 in two launches.
 #include "dense_tile.h"
 #include "fp8_tile.h"
 

@@ -10,7 +10,8 @@
 // A workgroup takes 128 rows x 128 columns: one group of each kind per row and column.  Its values are read once
 // and held in registers (a thread: four rows, eight columns); row maxima go over 16 lanes, column maxima over a
 // wave's four rows and the eight waves.  Memory-bound: two bytes read and two written per element of dz, two and
-// one of x.
+// one of x.  16384 rows of 32 runs, dz 2 x 2048 and x 7168 columns with silu: 0.69 GB in 157 us (4.4 TB/s).  2731 rows, dz 5632 and x 2048 columns
+// with GELU: 0.11 GB in 32 us; there the erf's polynomial and the maxima keep the vector units busy for about 22.
 #include "dense_device.h"
 #include "fp8_internal.h"
 
@@ -242,6 +243,7 @@ __global__ __launch_bounds__(kThreads) void groups_kernel(GroupsArgs a, int dz_b
 }
 
 // ---------------------------------------------------------------------------- weights
+// One pass: a block is held in registers between its maximum and its codes.  60 x 2816 x 2048 bf16: 190 us, 1.04 GB at 5.5 TB/s.
 // Workgroup (x, y, z): block (y, x) of matrix z.  The float32 scale follows the rule of the row quantiser: amax / 448
 // correctly rounded, codes as the float32 quotient rounds.
 template <typename T, bool UE8>

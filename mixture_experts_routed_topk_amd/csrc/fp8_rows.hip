@@ -5,6 +5,9 @@
 // instruction, several slices ahead and without a barrier.  (Straight into the MFMA's registers a lane would read 16 bytes
 // of a row and its neighbours other rows: those loads kept a CU's address unit busy for 120 cycles a slice.)  A slice's result
 // is folded in times the row's and the block's scale; the waves' float32 sums meet in LDS and are added in wave order.
+//
+// Bound by the launch (3.4 us of an empty shape), then by the weights' bytes.  Calls back to back, weights in the caches: 16 rows, 1408 -> 2048 4.0 us;
+// one row, 2048 -> 2 x 5632 4.9 us (7.0 from HBM: 3.3 TB/s), 11008 -> 2 x 4096 17.6 us (5.1 TB/s); 64 rows, 7168 -> 2048 12.1 us.
 #include "dense_tile.h"
 #include "fp8_tile.h"
 
