@@ -38,9 +38,10 @@ double shared_time(const int64_t (&tiles)[2], const double (&us)[2], Fill* fill)
   if (!tiles[1]) f.dw = 0;
   const int a = !f.dw, b = f.dw;                  // b fills
   const int64_t G = fp8_grid(tiles[0] + tiles[1]).x, heavy = tiles[a] % G;
-  f.extra = heavy ? (int)(us[a] / us[b] + 0.5) : 0;
-  f.others_first = heavy && f.extra * us[b] <= us[a];
+  f.extra = (int)(us[a] / us[b] + 0.5);
+  f.others_first = f.extra * us[b] <= us[a];
   *fill = f;
+  if (!heavy) f = Fill{f.dw, 0, 0};               // (as the kernel has it, which counts a's tiles itself)
   const int64_t early = f.extra * (G - heavy), late = tiles[b] > early ? tiles[b] - early : 0;
   const double whole = (tiles[a] / G) * us[a], rounds = (late / G) * us[b];
   const int64_t rest = late % G, firsts = f.others_first ? G - heavy : heavy;    // workgroups that the last round begins with
