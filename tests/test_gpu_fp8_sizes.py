@@ -1,6 +1,8 @@
 """The e4m3 products where the choice of a kernel, a tile height or a split changes with the sizes: few rows and their scales in LDS, both
 gradients of one launch with every pair of heights and with splits, runs in tiles of 256 rows."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -118,3 +120,52 @@ def test_one_expert_has_all_rows(T, K, N, E):
     ref.check(dx, *want[0], "dx")
     ref.check(dw[-1], *want[1], "dw")
     assert not dw[:-1].any()
+
+
+@pytest.mark.parametrize("T,K,N,E", [(2983, 1024, 1024, 0), (811, 512, 2048, 0), (136, 1024, 5632, 0), (257, 4096, 512, 0), (1500, 256, 640, 3)])
+def test_workspaces_of_exactly_the_size(T, K, N, E):
+    """A workspace of the size asked for is enough for a call and each subset of its gradients, and what lies behind it stays."""
+    shape = (E, N, K) if E else (N, K)
+    off = runs(84, T, E) if E else None      # (all rows belong to experts)
+    x, dy = rnd(85, (T, K)), rnd(86, (T, N), BF16, 1e-3)
+    q, s = rows(87, T, K)
+    stream = torch.cuda.current_stream().cuda_stream
+    for ue8m0 in (False, True):
+        wq, ws = weights(88, shape, ue8m0)
+        p = m.Fp8Problem(T, K, N, E, m.SCALE_UE8M0 if ue8m0 else m.SCALE_F32, m.ACT_NONE, 0, 0, 0, 0, 0)
+        addr = off.data_ptr() if E else None
+
+        def space(kind):
+            n = ctypes.c_size_t()
+            assert getattr(m.lib(), "moe_linear_fp8_workspace_size")(ctypes.byref(p), kind, ctypes.byref(n)) == 0
+            t = torch.full((n.value + 4096,), 0xa5, dtype=torch.uint8, device="cuda")
+            return t, n.value
+
+        work, n = space(0)
+        y = torch.empty((T, N), dtype=BF16, device="cuda")
+        assert m.lib().moe_linear_fp8(ctypes.byref(p), q.data_ptr(), s.data_ptr(), wq.data_ptr(), ws.data_ptr(), addr, None, None,
+                                      y.data_ptr(), None, work.data_ptr(), n, stream) == 0
+        assert (work[n:] == 0xa5).all()
+        assert torch.equal(y, m.linear_fp8(q, s, wq, ws, offsets=off)[0])
+        want = m.linear_fp8_backward(dy, x, wq, ws, offsets=off)
+        spans = by_expert(off) if E else [(0, 0, T)]
+        w = ref.wide(wq, ws).reshape(-1, N, K)
+        sizes = torch.zeros((T, K), dtype=torch.float64, device="cuda"), torch.zeros((max(E, 1), N, K), dtype=torch.float64, device="cuda")
+        for e, lo, hi in spans:
+            sizes[0][lo:hi] = dy[lo:hi].double().abs() @ w[e].abs()
+            sizes[1][e] = dy[lo:hi].double().abs().T @ x[lo:hi].double().abs()
+        sizes = sizes[0], sizes[1].reshape(shape)
+        work, n = space(2)
+        for dx_too, dw_too in ((True, True), (True, False), (False, True)):
+            dx = torch.empty((T, K), dtype=BF16, device="cuda") if dx_too else None
+            dw = torch.empty(shape, dtype=BF16, device="cuda") if dw_too else None
+            assert m.lib().moe_linear_fp8_backward(ctypes.byref(p), dy.data_ptr(), x.data_ptr(), wq.data_ptr(), ws.data_ptr(), addr, None,
+                                                   dx.data_ptr() if dx_too else None, dw.data_ptr() if dw_too else None, None,
+                                                   work.data_ptr(), n, stream) == 0
+            assert (work[n:] == 0xa5).all()
+            # A gradient alone may be split another way: the same at most 128 slices' results, each sum of them off by 2^-24 of
+            # what has been added, then two roundings to bf16 of 2^-8 each.  (The codes' own rounding adds at most 2^-4 to each factor.)
+            for got, full, size in ((dx, want[0], sizes[0]), (dw, want[1], sizes[1])):
+                if got is not None:
+                    bound = 2.0 ** -7 * full.double().abs() + 2 * 128 * 2.0 ** -24 * 1.13 * size
+                    assert ((got.double() - full.double()).abs() <= bound).all()
