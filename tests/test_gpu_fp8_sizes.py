@@ -169,3 +169,50 @@ def test_workspaces_of_exactly_the_size(T, K, N, E):
                 if got is not None:
                     bound = 2.0 ** -7 * full.double().abs() + 2 * 128 * 2.0 ** -24 * 1.13 * size
                     assert ((got.double() - full.double()).abs() <= bound).all()
+
+
+def test_refusals_on_the_gpu():
+    """Operands that do not fit are refused on the host, before and after a call whose sizes are known."""
+    T, K, N, E = 5, 256, 128, 3
+    q, s = rows(90, T, K)
+    wq, ws = weights(91, (N, K), False)
+    gq, gs = weights(92, (E, 2 * N, K), True)
+    off = runs(93, T, E)
+    half = torch.empty((T, 2 * K), dtype=torch.uint8, device="cuda")
+    bad = [
+        lambda: m.linear_fp8(q[:, :128], s, wq, ws),                                     # inputs
+        lambda: m.linear_fp8(q[:4], s, wq, ws),                                          # rows
+        lambda: m.linear_fp8(q.cpu(), s, wq, ws),
+        lambda: m.linear_fp8(q, s.cpu(), wq, ws),
+        lambda: m.linear_fp8(q, s, wq, ws.cpu()),
+        lambda: m.linear_fp8(q, s.double(), wq, ws),
+        lambda: m.linear_fp8(q, s, wq, ws.int()),
+        lambda: m.linear_fp8(q, s, wq.float(), ws),
+        lambda: m.linear_fp8(q.int(), s, wq, ws),
+        lambda: m.linear_fp8(q, s, wq, ws.T),                                            # blocks the other way round
+        lambda: m.linear_fp8(q, s, wq.T.contiguous().T, ws),
+        lambda: m.linear_fp8(q.T.contiguous().T, s, wq, ws),
+        lambda: m.linear_fp8(q[:1].expand(T, K), s, wq, ws),                             # rows that overlap
+        lambda: m.linear_fp8(half[:, 1:K + 1], s, wq, ws),                               # not on 16 bytes
+        lambda: m.linear_fp8(q, s, wq, ws, offsets=off),                                 # one matrix with offsets
+        lambda: m.linear_fp8(q, s, wq[None], ws[None]),                                  # experts without
+        lambda: m.linear_fp8(q, s, wq, ws, out=torch.empty((T, N), device="cuda")),
+        lambda: m.linear_fp8(q, s, wq, ws, bias=rnd(94, (N + 8,))),
+        lambda: m.linear_fp8(q, s, wq, ws, act=4),
+        lambda: m.linear_fp8(q, s, wq, ws, residual=rnd(95, (T, N)), workspace=torch.empty(16)),
+        lambda: m.gated_linear_fp8(q, s, wq, ws),                                        # 128 rows are no two halves
+        lambda: m.gated_linear_fp8(q, s, gq, gs),
+        lambda: m.gated_linear_fp8(q, s, gq, gs, offsets=off[:-1]),
+        lambda: m.gated_linear_fp8(q, s, gq, gs, offsets=off.long()),
+        lambda: m.gated_linear_fp8(q, s, gq, gs, offsets=off.cpu()),
+        lambda: m.gated_linear_fp8(q, s, gq, gs, offsets=off, act=m.ACT_NONE),
+        lambda: m.linear_fp8(None, s, wq, ws),
+        lambda: m.linear_fp8(q, s, None, ws),
+    ]
+    for _ in range(2):
+        for i, call in enumerate(bad):
+            with pytest.raises(ValueError):
+                call()
+                print("not refused:", i)
+        y, _ = m.linear_fp8(q, s, wq, ws)
+        ref.check(y, *ref.linear(ref.wide_rows(q, s), ref.wide(wq, ws), None, None, "none")[0], "y")
