@@ -75,7 +75,7 @@ Fp8Gemm forward_gemm(const Size& z) {
 ForwardLayout forward_layout(const Size& z) {
   ForwardLayout L{};
   if (z.T == 0) return L;
-  L.gemm = z.E ? up256(runs_bytes(z.T, z.E, fp8_grouped_height(z.T, z.E, z.K, z.cols))) : 0;
+  L.gemm = z.E && !fp8_rows_take(z.T, z.K, z.E, z.gated) ? up256(runs_bytes(z.T, z.E, fp8_grouped_height(z.T, z.E, z.K, z.cols))) : 0;
   L.total = L.gemm + fp8_gemm_workspace(forward_gemm(z));
   return L;
 }
@@ -142,7 +142,8 @@ moe_status run_forward(const moe_fp8_problem* p, bool gated, const uint8_t* x_q,
   g.g.e.ldp = pitch(p->ldp, z.cols);
   g.g.e.act = z.act;
   g.g.e.vec = 1;
-  if (z.E) {
+  g.offsets = offsets;
+  if (z.E && !fp8_rows_take(z.T, z.K, z.E, z.gated)) {
     g.runs = runs_at(ws, z.T, z.E, fp8_grouped_height(z.T, z.E, z.K, z.cols));
     MOE_HIP_CHECK(launch_runs(g.runs, offsets, z.T, z.E, s));
   }

@@ -82,6 +82,7 @@ struct Fp8Gemm {
   int E;                        // 0: none
   int64_t c_expert;             // bytes from an expert's c to the next one's
   int64_t cs_expert;            // entries
+  const int32_t* offsets;       // few rows: the runs themselves, without tables
   Runs runs;
 };
 // Rows of the tiles that a product by runs takes: forward, K x cols weights an expert, and dx
@@ -93,8 +94,8 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t s);
 size_t fp8_gradients_workspace(int64_t T, int64_t N, int64_t cols, int E);
 hipError_t launch_fp8_gradients(const Fp8Gemm* dx, const Fp8Gemm* dw, void* ws, hipStream_t s);
 
-// forward products of few rows
-bool fp8_rows_take(int64_t M, int64_t K);
+// forward products of few rows, M in all (E: over the runs)
+bool fp8_rows_take(int64_t M, int64_t K, int E, bool gated);
 hipError_t launch_fp8_rows(const Fp8Gemm& g, hipStream_t s);
 
 }  // namespace moe

@@ -216,3 +216,53 @@ def test_refusals_on_the_gpu():
                 print("not refused:", i)
         y, _ = m.linear_fp8(q, s, wq, ws)
         ref.check(y, *ref.linear(ref.wide_rows(q, s), ref.wide(wq, ws), None, None, "none")[0], "y")
+
+
+# rows of experts in single-token steps: runs of more and fewer than eight rows, more experts than a wave has lanes
+FEW_BY_EXPERT = [(1, 256, 128, 60), (5, 256, 128, 3), (17, 4224, 128, 2), (32, 65536, 128, 2), (33, 512, 256, 4), (40, 128, 128, 1024), (64, 4096, 128, 130),
+                 (64, 384, 256, 1), (65, 384, 256, 5)]
+
+
+@pytest.mark.parametrize("ue8m0", [False, True], ids=["f32", "ue8m0"])
+@pytest.mark.parametrize("T,K,N,E", FEW_BY_EXPERT)
+def test_few_rows_by_expert(T, K, N, E, ue8m0):
+    q, s = rows(100, T, K)
+    off = runs(101, T, E, max(T - 2, 1))
+    wq, ws = weights(102, (E, N, K), ue8m0)
+    gq, gs = weights(103, (E, 2 * N, K), ue8m0)
+    y = torch.full((T, N), 5.0, dtype=BF16, device="cuda")
+    a = torch.full((T, N), 6.0, dtype=BF16, device="cuda")
+    m.linear_fp8(q, s, wq, ws, offsets=off, out=y)
+    _, pre = m.gated_linear_fp8(q, s, gq, gs, act=m.ACT_GELU, save_pre=True, offsets=off, out=a)
+    last = int(off[-1])
+    assert (y[last:] == 5.0).all() and (a[last:] == 6.0).all()
+    for e, lo, hi in by_expert(off):
+        x = ref.wide_rows(q[lo:hi], s[lo:hi])
+        ref.check(y[lo:hi], *ref.linear(x, ref.wide(wq[e], ws[e]), None, None, "none")[0], f"expert {e}")
+        want, wpre = ref.gated(x, ref.wide(gq[e], gs[e]), "gelu")
+        ref.check(a[lo:hi], *want, f"expert {e} a")
+        ref.check(pre[lo:hi], *wpre, f"expert {e} pre")
+
+
+@pytest.mark.parametrize("T", [30, 300])
+def test_offsets_are_taken_into_the_rows_and_into_order(T):
+    """Few rows and many read the same runs out of offsets that do not fit."""
+    K, N, E = 256, 128, 70
+    q, s = rows(104, T, K)
+    wq, ws = weights(105, (E, N, K), False)
+    off = torch.randint(-5, T + 40, (E + 1,), generator=torch.Generator().manual_seed(106)).tolist()
+    off = sorted(off)[:50] + off[50:]                       # (in order at first, then not)
+    off[0], off[3], off[40], off[E] = 4, -2 ** 31, T // 2, 2 ** 31 - 1
+    start, spans = min(max(off[0], 0), T), []
+    for e in range(E):
+        end = max(start, min(max(off[e + 1], 0), T))
+        if end > start:
+            spans.append((e, start, end))
+        start = end
+    assert len(spans) > 5
+    y = torch.full((T, N), 5.0, dtype=BF16, device="cuda")
+    m.linear_fp8(q, s, wq, ws, offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), out=y)
+    assert (y[:4] == 5.0).all()
+    for e, lo, hi in spans:
+        x = ref.wide_rows(q[lo:hi], s[lo:hi])
+        ref.check(y[lo:hi], *ref.linear(x, ref.wide(wq[e], ws[e]), None, None, "none")[0], f"expert {e}")
