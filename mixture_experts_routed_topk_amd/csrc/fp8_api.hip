@@ -94,7 +94,7 @@ BackwardLayout backward_layout(const Size& z, bool bias) {
     o = up256(o + bytes);
     return at;
   };
-  L.runs = take(z.E ? runs_bytes(z.T, z.E, fp8_dx_height(z.T, z.E)) : 0);
+  L.runs = take(z.E ? runs_bytes(z.T, z.E, fp8_dx_height(z.T, z.E, z.cols, z.ue8m0)) : 0);
   L.zr = take(z.T * z.cols);
   L.zr_scale = take(z.T * (z.cols / 128) * 4);
   L.zc = take(L.tiles * 128 * z.cols);
@@ -176,7 +176,7 @@ moe_status run_backward(const moe_fp8_problem* p, bool gated, const void* dy, co
   auto bytes = [&](size_t at) { return reinterpret_cast<uint8_t*>(ws + at); };
   Runs runs{};
   if (z.E) {
-    runs = runs_at(ws + L.runs, z.T, z.E, fp8_dx_height(z.T, z.E));
+    runs = runs_at(ws + L.runs, z.T, z.E, fp8_dx_height(z.T, z.E, z.cols, z.ue8m0));
     MOE_HIP_CHECK(launch_runs(runs, offsets, z.T, z.E, s));
   }
   GroupsArgs a{};

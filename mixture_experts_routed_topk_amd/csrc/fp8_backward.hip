@@ -82,6 +82,7 @@ Gradients plan_of(int64_t T, int64_t N, int64_t cols, bool dx, bool dw, bool fol
           us[i] = g.slices[i] * kSlice[kind_of(i, fold)][g.height[i] == 128] + kFixed[g.height[i] == 128];
           if (g.splits[i] > 1) joined += (double)M[i] * N * 4 * (g.splits[i] + 1);
         }
+        if (fold && g.height[0] == 128 && g.slices[0] > kLongestShortTile) ok = false;      // (its block scales do not fit)
         if (!ok) continue;
         double time = shared_time(tiles, us, &g.fill);
         if (joined > 0) time += kJoinGradients.us + joined / kJoinGradients.bytes_per_us;
@@ -95,7 +96,9 @@ size_t part_bytes(const Gradients& p, int i, int64_t M, int64_t N) {
 
 }  // namespace
 
-int fp8_dx_height(int64_t T, int E) { return T >= (int64_t)384 * E ? 256 : 128; }
+int fp8_dx_height(int64_t T, int E, int64_t cols, bool ue8m0) {
+  return T >= (int64_t)384 * E || (!ue8m0 && cols / 128 > kLongestShortTile) ? 256 : 128;
+}
 
 size_t fp8_gradients_workspace(int64_t T, int64_t N, int64_t cols, int E) {
   if (T == 0 || E) return 0;

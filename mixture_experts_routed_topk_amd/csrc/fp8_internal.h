@@ -87,7 +87,7 @@ struct Fp8Gemm {
 };
 // Rows of the tiles that a product by runs takes: forward, K x cols weights an expert, and dx
 int fp8_grouped_height(int64_t T, int E, int64_t K, int64_t cols);
-int fp8_dx_height(int64_t T, int E);
+int fp8_dx_height(int64_t T, int E, int64_t cols, bool ue8m0);
 size_t fp8_gemm_workspace(const Fp8Gemm& g);
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t s);
 // dx: r (codes [T][cols]) along k, c along its rows; dw: both along their rows, g.K: rows of all 128-row tiles.  Either may be null.

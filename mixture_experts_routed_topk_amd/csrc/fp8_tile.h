@@ -127,6 +127,7 @@ __device__ __forceinline__ void eight_columns(f32x4& a, f32x4& b) {
 }
 
 constexpr int kMaxSlices = 512;         // K <= 65536
+constexpr int kMaxDxSlices = 1024;      // of dx, which contracts over up to 2 x 65536 columns
 
 // This lane's number, formed anew (from a zero that the compiler does not know to be one): what follows from it is computed
 // where it is used, once a tile, and not kept in registers through the loop
@@ -162,7 +163,12 @@ struct Ring {
   static constexpr bool PATCHED = NH == 2 || !FOLD;
   static constexpr int PATCH = BYTES - (PATCHED ? 8 * 1024 : 0);
   static constexpr int TABLES = PATCH - TABLE;
+  // Slices of the longest contraction whose block scales TABLES holds for two tiles: the next one's arrive while a tile's last slices
+  // still read theirs
+  static constexpr int LONGEST = TABLES / 4 / 4 / 64 * 64;
 };
+static_assert(Ring<1, true>::LONGEST >= kMaxSlices && Ring<2, true>::LONGEST >= kMaxDxSlices, "two tiles' block scales");
+constexpr int kLongestShortTile = Ring<1, true>::LONGEST;      // 704: longer contractions with float32 block scales take 256-row tiles
 
 // 16 x 32 bf16 results of a wave, turned in LDS: lane l has row l & 15, columns 4 (l >> 4) and 16 further on, and gets row l >> 2, eight columns from
 // 8 (l & 3) on.  Four neighbouring lanes then store 64 bytes of a row, where the results as they are formed would go out in
