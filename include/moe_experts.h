@@ -567,7 +567,8 @@ typedef struct {
 } moe_fp8_problem;
 
 /*
- * Weights to e4m3 with one scale per 128 x 128 block, for `count` matrices [N, K] (N, K multiples of 128) one after the other.
+ * Weights to e4m3 with one scale per 128 x 128 block, for `count` matrices [N, K] one after the other: up to 1024 of them and
+ * 2^34 elements in all; N and K multiples of 128, 128 .. 65536, and N also twice such a number (gate and up rows).
  * The block's scale is amax / 448: float32, correctly rounded (MOE_SCALE_F32), or the smallest power of two that is not
  * below it, at least 2^-126 (MOE_SCALE_UE8M0); 1 for a block of zeros.  Codes as in moe_quantize_rows_fp8.
  *

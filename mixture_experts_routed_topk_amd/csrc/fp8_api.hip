@@ -266,7 +266,8 @@ moe_status moe_quantize_blocks_fp8(const void* w, int32_t dtype, int32_t count, 
                                    uint8_t* q, void* scales, void* stream) {
   if ((dtype != MOE_F32 && dtype != MOE_BF16) || (scale_fmt != MOE_SCALE_F32 && scale_fmt != MOE_SCALE_UE8M0))
     return MOE_ERR_UNSUPPORTED;
-  if (count < 0 || count > kMaxExperts || !width_ok(N) || !width_ok(K) || (int64_t)count * N * K > kMaxElements)
+  const bool rows_ok = width_ok(N) || (N % 2 == 0 && width_ok(N / 2));      // (gate and up rows)
+  if (count < 0 || count > kMaxExperts || !rows_ok || !width_ok(K) || (int64_t)count * N * K > kMaxElements)
     return MOE_ERR_BAD_SHAPE;
   if (count == 0) return MOE_OK;
   if (!w || !q || !scales) return MOE_ERR_NULL_ARG;

@@ -1,5 +1,6 @@
 """Gradients of gated e4m3 products whose dz is so wide that dx's contraction has more than 704 slices: the float32 scales of two tiles' blocks
-do not fit in LDS beside the slices of 128-row tiles.  The blocks' scales are small but for the last slices', which differ from tile to tile."""
+do not fit in LDS beside the slices of 128-row tiles.  The blocks' scales are small but for the last slices', which differ from tile to tile.
+And such a gate's weights to e4m3 blocks."""
 
 import ctypes
 
@@ -56,3 +57,15 @@ def test_dx_of_a_wide_gate(T, K, I, E, ue8m0):
         want, err = ref.product(zr, w.t().contiguous(), chained=True)
         err = err + er @ w.abs() * (1 + ref.BLOCK)
         ref.check(dx[rows][:, some], want, err + ref.HALF[BF16] * (want.abs() + err), f"expert {e}")
+
+
+@pytest.mark.parametrize("ue8m0", [False, True], ids=["f32", "ue8m0"])
+@pytest.mark.parametrize("shape", [(131072, 128), (2, 65792, 256)])
+def test_weights_of_a_wide_gate_to_blocks(shape, ue8m0):
+    w = rnd(5, shape)
+    q, s = m.quantize_blocks_fp8(w, ue8m0)
+    g = w.double().view(*shape[:-2], shape[-2] // 128, 128, shape[-1] // 128, 128)
+    _, scales = ref.block_groups(w, ue8m0)
+    assert torch.equal(ref.scale_values(s), scales)
+    quotient = (g / scales[..., :, None, :, None]).float()          # (rounded to float32 before it is to e4m3)
+    assert torch.equal(q.view(ref.E4M3).float(), quotient.to(ref.E4M3).float().view(shape))
