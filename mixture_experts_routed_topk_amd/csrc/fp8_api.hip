@@ -60,9 +60,6 @@ void set_weights(Fp8Gemm& g, const Size& z, const void* w, const void* w_scale, 
   g.cs_expert = z.cols / 128 * kb;
 }
 
-struct ForwardLayout {
-  size_t runs, gemm, total;
-};
 Fp8Gemm forward_gemm(const Size& z) {
   Fp8Gemm g{};
   g.g.M = z.T;
@@ -70,19 +67,27 @@ Fp8Gemm forward_gemm(const Size& z) {
   g.g.gated = z.gated;
   g.g.e.N = z.N;
   g.E = z.E;
+  g.few = fp8_rows_take(z.T, z.K, z.E, z.gated);
   return g;
 }
-ForwardLayout forward_layout(const Size& z) {
+// The tables of runs, of tiles of `height` rows (0: none are needed), then the product's own
+struct ForwardLayout {
+  int height;
+  size_t gemm, total;
+};
+ForwardLayout forward_layout(const Size& z, const Fp8Gemm& g) {
   ForwardLayout L{};
   if (z.T == 0) return L;
-  L.gemm = z.E && !fp8_rows_take(z.T, z.K, z.E, z.gated) ? up256(runs_bytes(z.T, z.E, fp8_grouped_height(z.T, z.E, z.K, z.cols))) : 0;
-  L.total = L.gemm + fp8_gemm_workspace(forward_gemm(z));
+  L.height = z.E && !g.few ? fp8_grouped_height(z.T, z.E, z.K, z.cols) : 0;
+  L.gemm = L.height ? up256(runs_bytes(z.T, z.E, L.height)) : 0;
+  L.total = L.gemm + fp8_gemm_workspace(g);
   return L;
 }
 
 struct BackwardLayout {
   size_t runs, zr, zr_scale, zc, zc_scale, xc, xc_scale, part, gemm, total;
   int64_t tiles;                // 128-row tiles at most
+  int height;                   // of dx's tiles by runs
 };
 BackwardLayout backward_layout(const Size& z, bool bias) {
   BackwardLayout L{};
@@ -94,7 +99,8 @@ BackwardLayout backward_layout(const Size& z, bool bias) {
     o = up256(o + bytes);
     return at;
   };
-  L.runs = take(z.E ? runs_bytes(z.T, z.E, fp8_dx_height(z.T, z.E, z.cols, z.ue8m0)) : 0);
+  L.height = z.E ? fp8_dx_height(z.T, z.E, z.cols, z.ue8m0) : 0;
+  L.runs = take(z.E ? runs_bytes(z.T, z.E, L.height) : 0);
   L.zr = take(z.T * z.cols);
   L.zr_scale = take(z.T * (z.cols / 128) * 4);
   L.zc = take(L.tiles * 128 * z.cols);
@@ -120,7 +126,8 @@ moe_status run_forward(const moe_fp8_problem* p, bool gated, const uint8_t* x_q,
   const Size z = size_of(*p, gated);
   if (z.E && (bias || residual || (pre && !gated))) return MOE_ERR_UNSUPPORTED;
   if (z.T == 0) return MOE_OK;
-  const ForwardLayout L = forward_layout(z);
+  Fp8Gemm g = forward_gemm(z);
+  const ForwardLayout L = forward_layout(z, g);
   if (!x_q || !x_scale || !w_q || !w_scale || !y || (z.E && !offsets) || (L.total && !workspace)) return MOE_ERR_NULL_ARG;
   if (!all_aligned16(x_q, w_q, bias, residual, y, pre, workspace) || !aligned4(x_scale) || (!z.ue8m0 && !aligned4(w_scale)) ||
       !aligned4(offsets))
@@ -128,7 +135,6 @@ moe_status run_forward(const moe_fp8_problem* p, bool gated, const uint8_t* x_q,
   if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   (void)hipGetLastError();   // an error left by an earlier, unrelated HIP call is not ours
   char* ws = static_cast<char*>(workspace);
-  Fp8Gemm g = forward_gemm(z);
   g.g.r = x_q;
   g.g.ldr = pitch(p->ldx, z.K);
   g.rs = Fp8Scales{x_scale, z.K / 128, 1, 0};
@@ -143,8 +149,8 @@ moe_status run_forward(const moe_fp8_problem* p, bool gated, const uint8_t* x_q,
   g.g.e.act = z.act;
   g.g.e.vec = 1;
   g.offsets = offsets;
-  if (z.E && !fp8_rows_take(z.T, z.K, z.E, z.gated)) {
-    g.runs = runs_at(ws, z.T, z.E, fp8_grouped_height(z.T, z.E, z.K, z.cols));
+  if (L.height) {
+    g.runs = runs_at(ws, z.T, z.E, L.height);
     MOE_HIP_CHECK(launch_runs(g.runs, offsets, z.T, z.E, s));
   }
   MOE_HIP_CHECK(launch_fp8_gemm(g, ws + L.gemm, s));
@@ -176,7 +182,7 @@ moe_status run_backward(const moe_fp8_problem* p, bool gated, const void* dy, co
   auto bytes = [&](size_t at) { return reinterpret_cast<uint8_t*>(ws + at); };
   Runs runs{};
   if (z.E) {
-    runs = runs_at(ws + L.runs, z.T, z.E, fp8_dx_height(z.T, z.E, z.cols, z.ue8m0));
+    runs = runs_at(ws + L.runs, z.T, z.E, L.height);
     MOE_HIP_CHECK(launch_runs(runs, offsets, z.T, z.E, s));
   }
   GroupsArgs a{};
@@ -251,7 +257,7 @@ moe_status workspace_size(const moe_fp8_problem* p, bool gated, int backward, si
   if (st != MOE_OK) return st;
   if (!bytes) return MOE_ERR_NULL_ARG;
   const Size z = size_of(*p, gated);
-  *bytes = backward ? backward_layout(z, backward != MOE_BACKWARD_NO_BIAS).total : forward_layout(z).total;
+  *bytes = backward ? backward_layout(z, backward != MOE_BACKWARD_NO_BIAS).total : forward_layout(z, forward_gemm(z)).total;
   return MOE_OK;
 }
 

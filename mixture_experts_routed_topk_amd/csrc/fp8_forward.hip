@@ -33,12 +33,12 @@ int fp8_grouped_height(int64_t T, int E, int64_t K, int64_t cols) {
 }
 
 size_t fp8_gemm_workspace(const Fp8Gemm& g) {
-  if (g.g.M == 0 || g.E || fp8_rows_take(g.g.M, g.g.K, 0, g.g.gated)) return 0;
+  if (g.g.M == 0 || g.E || g.few) return 0;
   return forward_part(plan_fp8(g.g.M, g.g.e.N, g.g.K, g.g.gated), g.g.M, g.g.e.N, g.g.gated, 1);
 }
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t s) {
-  if (fp8_rows_take(g.g.M, g.g.K, g.E, g.g.gated)) return launch_fp8_rows(g, s);
+  if (g.few) return launch_fp8_rows(g, s);
   if (g.E) {
     const int height = g.runs.height;
     Job job{};

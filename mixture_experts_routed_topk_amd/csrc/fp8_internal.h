@@ -82,7 +82,8 @@ struct Fp8Gemm {
   int E;                        // 0: none
   int64_t c_expert;             // bytes from an expert's c to the next one's
   int64_t cs_expert;            // entries
-  const int32_t* offsets;       // few rows: the runs themselves, without tables
+  int few;                      // forward: the kernel of few rows (fp8_rows_take)
+  const int32_t* offsets;       // which finds the runs in here, without tables
   Runs runs;
 };
 // Rows of the tiles that a product by runs takes: forward, K x cols weights an expert, and dx
