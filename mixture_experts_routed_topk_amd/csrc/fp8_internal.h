@@ -82,9 +82,9 @@ struct Fp8Gemm {
   int E;                        // 0: none
   int64_t c_expert;             // bytes from an expert's c to the next one's
   int64_t cs_expert;            // entries
-  int few;                      // forward: the kernel of few rows (fp8_rows_take)
-  const int32_t* offsets;       // which finds the runs in here, without tables
+  const int32_t* offsets;       // few rows: the runs themselves, without tables
   Runs runs;
+  int few;                      // forward: the kernel of few rows takes it (fp8_rows_take)
 };
 // Rows of the tiles that a product by runs takes: forward, K x cols weights an expert, and dx
 int fp8_grouped_height(int64_t T, int E, int64_t K, int64_t cols);
