@@ -509,7 +509,7 @@ typedef struct {
 
 /*
  * y[inv[t*k + j]] = x[t] for every slot (t, j) with a position: 0 <= inv < rows (others, -1 among them, are left out).
- * Rows of y that no slot names are left as they were.  Positions are distinct, as moe_route leaves them.
+ * Rows of y (and of y_scale) that no slot names are left as they were.  Positions are distinct, as moe_route leaves them.
  *
  *   x [T, H], inv [T*k] int32, y [rows, H] out
  *   x_scale [T, H/128] and y_scale [rows, H/128] float32, packed: the scales of e4m3 rows, moved along; both or neither

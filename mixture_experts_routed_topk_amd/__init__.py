@@ -763,8 +763,8 @@ def permute(x: torch.Tensor, inv: torch.Tensor, rows: Optional[int] = None, scal
             out: Optional[torch.Tensor] = None):
     """(y, y_scale): y[inv[t*k + j]] = x[t], the tokens' rows in expert order, for inv [T*k] int32 as route and
     route_logits return it (-1: no row).  x [T,H] bf16 or float32, or e4m3 codes (uint8 or float8_e4m3fn) with scale
-    [T,H/128] float32, which is moved along (y_scale; None otherwise).  y has `rows` rows (default T*k, or out's); those that no
-    slot names are left as they were in `out`, and unset without it.  See moe_permute."""
+    [T,H/128] float32, which is moved along (y_scale, a new tensor; None otherwise).  y has `rows` rows (default T*k, or out's);
+    those that no slot names are left as they were in `out`, and unset without it and in y_scale.  See moe_permute."""
     if isinstance(x, torch.Tensor) and x.dtype in _CODES:
         if x.device.type != "cuda" or x.dim() != 2:
             raise ValueError("x must be a GPU tensor of two dimensions")

@@ -188,6 +188,9 @@ void launch_heights(const Fp8Gemm& g, hipStream_t s) {
 // of 18 shapes where tiles win).
 // Runs, eight rows of one at a time: 4 rows of 60 runs, 2048 -> 1408 5.2 / 23.4, gated 5.8 / 23.6; 16 rows 10.7 / 24.7, 19.4 / 27.0; 64 rows
 // 28.6 / 29.3, 50.7 / 50.6, of 256 runs, 7168 -> 512 44.7 / 59.0, 103.6 / 90.1; 128 rows of 32, 7168 -> 2048 114 / 103, 221 / 187.
+// Long runs pass over their matrix once for every eight rows, from the caches: 64 rows of one run, 2048 -> 1408 15.6 / 23.7 (as one matrix 6.3),
+// 7168 -> 2048 24.4 / 58.3 (11.9), of two 9.2 / 22.9 and 16.0 / 56.9, of four 6.9 / 22.9 and 20.5 / 56.6; gated, 32 rows of one 9.6 / 23.1 (4.4)
+// and 15.7 / 56.2 (8.1), of four 5.6 / 23.0 and 26.0 / 55.5.
 bool fp8_rows_take(int64_t M, int64_t K, int E, bool gated) {
   return E ? M <= (gated ? 32 : 64) : M <= 64 && M * (K / 128) <= kMaxScales;
 }

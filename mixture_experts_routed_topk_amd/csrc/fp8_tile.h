@@ -34,9 +34,9 @@
 // A slice of 256 x 256 x 128 is 2048 cycles of MFMAs on each SIMD.  Measured: 2670 with the MFMA's own scales, 3500 to 3600
 // with FOLD, 4130 for dw, whose short contractions lie between bursts of stores.  The clock falls to 1.4 to 1.9 GHz under
 // these kernels (it depends on the codes): with three quarters of the FMAs left out a slice takes as long, in fewer
-// cycles.  8192 x 8192 x 8192 of random codes: 497 us (2.21 PFLOP/s) with powers of two as weights' scales, 542 (2.03) with
-// float32 ones.  16384 rows of 32 runs, 2048 -> 7168: 325 us (1.48 PFLOP/s, 0.74 GB).  Gated, 8192 x 7168 -> 2 x 2048 with saved
-// projections: 240 us (2.0).  dx and dw of 16384 rows of 32 runs, 7168 <- 2 x 2048: 1200 us (1.6, beside 2.1 GB of results).
+// cycles.  8192 x 8192 x 8192 of random codes: 526 to 530 us (2.08 PFLOP/s) with powers of two as weights' scales in either format (the
+// forward folds both), 535 with other float32 ones.  16384 rows of 32 runs, 2048 -> 7168: 325 us (1.48 PFLOP/s, 0.74 GB).  Gated,
+// 8192 x 7168 -> 2 x 2048 with saved projections: 240 us (2.0).  dx and dw of 16384 rows of 32 runs, 7168 <- 2 x 2048: 1200 us (1.6, beside 2.1 GB of results).
 #pragma once
 
 #include <type_traits>

@@ -4,8 +4,8 @@
 //   permute            y[inv] = x[t]                     (also the rows' scales, for e4m3 codes)
 //   unpermute          out[t] = sum_j w[t, j] y[inv]     (w = 1: the gradient of permute)
 //   its gradient       dy[inv] = w[t, j] dout[t],  dw[t, j] = <dout[t], y[inv]>
-// All three go by token: a token's row is read (or written) once and its k rows follow from inv, so nothing
-// is read twice, no atomics are needed, and the sums over j are in slot order.  A position outside [0, rows) is treated as
+// All three go by token, whose k rows follow from inv: no atomics are needed, and the sums over j are in slot order.  Rows of
+// eight slots go together, so with k <= 8 nothing is read twice; with more, permute and the gradient read a token's row ceil(k / 8) times.  A position outside [0, rows) is treated as
 // -1.  Memory-bound, in pieces of 16 bytes; a token's row belongs to 64 lanes, or to 256 where it has
 // more than 64 pieces.  4096 tokens of eight slots: codes of 7168 with their scales 61 us (0.27 GB, 4.4 TB/s, most of it stores); the gradient
 // of the way back in bf16, a quarter of the slots dropped, 157 us (0.77 GB, 4.9 TB/s).  8192 tokens of four slots, 2048 bf16: the gradient
